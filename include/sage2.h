@@ -66,10 +66,11 @@ typedef enum {
   SAGE2_ERR_CUDA = 4,        /* a CUDA runtime/driver call or launch failed   */
   SAGE2_ERR_NO_MEM = 5,      /* workspace allocation failed                   */
   SAGE2_ERR_TIMEOUT = 6,     /* a kernel's bounded wait ran out (device word) */
-  SAGE2_ERR_TOO_LARGE = 7    /* scratch needed exceeds the fixed no-allocation buffer */
+  SAGE2_ERR_TOO_LARGE = 7,   /* scratch needed exceeds the fixed no-allocation buffer */
+  SAGE2_ERR_BAD_INDEX = 8    /* a length, page or slot on the device is out of range (device word) */
 } sage2_status;
 
-typedef enum { SAGE2_F16 = 0, SAGE2_BF16 = 1, SAGE2_F32 = 2 } sage2_dtype;
+typedef enum { SAGE2_F16 = 0, SAGE2_BF16 = 1, SAGE2_F32 = 2, SAGE2_E4M3 = 3 /* caches only */ } sage2_dtype;
 
 /*
  * Integer format of the Q^/K^ payloads (q_i4, k_i4).
@@ -260,6 +261,131 @@ sage2_status sage2_attn_fwd_host(const void* q, const void* k, const void* v, vo
                                  float sm_scale, int qk_format, int smooth_v,
                                  sage2_stream_t stream);
 
+/*
+ * Paged key/value cache
+ * ---------------------
+ * What follows the prompt: its keys and values, and those of each token decoded
+ * or drafted after it, are kept in pools of pages that the sequences share.
+ *   k, v     : [pages, Hkv, page_size, d] in kv_dtype (SAGE2_F16, SAGE2_BF16, or
+ *              SAGE2_E4M3: one code a value and one fp32 scale a row), contiguous,
+ *              16-byte aligned.
+ *   k_scale, v_scale : f32 [pages, Hkv, page_size], SAGE2_E4M3 only: the row
+ *              stands for code * scale.  16-byte aligned.
+ *   page_size: 16, 32, 64 or 128.  d: 64 or 128.
+ * A sequence's slot s is row s % page_size of page table[b][s / page_size];
+ * `table` is a DEVICE int32 array [B, max_pages], `lens` a DEVICE int32 array [B]
+ * of tokens in the cache.  T drafted tokens of sequence b (a tree, a chain or the
+ * one token of a decode step) occupy the slots behind them: lens[b] + j, j < n[b]
+ * (`n`: DEVICE int32 [B], 0 <= n[b] <= T; NULL: T for each).
+ * Device integers are not read on the host.  The kernels check them: a length
+ * that the table cannot hold, a page outside the pool or a slot outside the table
+ * sets the device error word (SAGE2_ERR_BAD_INDEX on the next
+ * sage2_check_device_error), nothing outside the buffers is touched, and the
+ * outputs that depend on it are not meaningful.  Table entries behind the last
+ * slot in use are not read.
+ * Stride arrays are HOST arrays of elements and may be NULL for contiguous
+ * tensors; q, k, v strides are {batch, head, token}, >= 0 and multiples of 8, the d
+ * values of a row are contiguous.
+ */
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int kv_dtype;
+  int pages;
+  int Hkv;
+  int page_size;
+  int d;
+} sage2_cache;
+
+/*
+ * Writes new tokens to the cache: slot lens[b] + t of each head takes k[b][h][t]
+ * and v[b][h][t], t < n[b].  `lens` is not changed.
+ *   k, v : [B, Hkv, T, d] in dtype (SAGE2_F16 or SAGE2_BF16; a 16-bit cache has the same).
+ * SAGE2_E4M3: scale = amax/448, code = RNE e4m3 of fp32(x * (448/amax)), each
+ * fp32 operation rounded once.  A row with amax below 2^-100 is stored as zeros
+ * (scale 0), a row with an infinity or NaN gets scale NaN.
+ * Two tokens of one call must not name the same row of a page.
+ */
+sage2_status sage2_cache_append(const void* k, const void* v, int dtype, const int64_t* k_strides,
+                                const int64_t* v_strides, const sage2_cache* cache,
+                                const int* table, int max_pages, const int* lens, const int* n,
+                                int B, int T, sage2_stream_t stream);
+
+/*
+ * Attention of the drafted tokens over the cache and one another:
+ *   o[b][hq][i] = sum_s softmax_s(sm_scale * q[b][hq][i] . K_s) V_s
+ * over the slots s < lens[b] and those lens[b] + j, j < n[b], with
+ * mask[b][i][j] != 0 (a token's ancestors in the tree and itself; mask NULL:
+ * j <= i).  Query head hq reads key/value head hq / (Hq/Hkv).
+ *   q    : [B, Hq, T, d] in dtype (SAGE2_F16 or SAGE2_BF16; a 16-bit cache has the
+ *          same), Hq a multiple of Hkv, 1 <= T <= 1024.  T = 1 is a decode step.
+ *   mask : DEVICE bytes [T, T] per sequence, mask_stride bytes apart (0: one for all).
+ *   o    : [B, Hq, T, d] contiguous in o_dtype (SAGE2_F16, SAGE2_BF16 or SAGE2_F32).
+ *   lse  : f32 [B, Hq, T] contiguous or NULL: ln sum_s exp(sm_scale * q . K_s).
+ * A token with nothing to attend and the tokens i >= n[b] get o = 0, lse = -inf.
+ * Slots that no token attends may hold any bits.  K and V of a slot that some
+ * drafted token attends must be finite.  Scores, their maxima and sums and the
+ * accumulators are fp32; P is rounded to the MMA's 16-bit type.  The order of the
+ * sums depends on the sizes and lengths alone, so equal calls give equal bits.
+ */
+sage2_status sage2_attn_tree(const void* q, int dtype, const int64_t* q_strides,
+                             const sage2_cache* cache, const int* table, int max_pages,
+                             const int* lens, const int* n, const uint8_t* mask,
+                             int64_t mask_stride, void* o, int o_dtype, float* lse, int B, int Hq,
+                             int T, float sm_scale, sage2_stream_t stream);
+
+/*
+ * Adds to a tally the attention weight that each cached token received:
+ *   acc[b][h][s] += sum over the query heads hq of h and the tokens i < n[b] that
+ *                   attend slot s of exp(sm_scale * q[b][hq][i] . K_s - lse[b][hq][i])
+ * with the arguments of sage2_attn_tree and the lse it wrote (rows with lse = -inf
+ * add nothing).
+ *   acc : f32, slots contiguous, acc_strides {batch, head} in elements, S slots a
+ *         head (a slot >= S is left out and sets the device error word).
+ */
+sage2_status sage2_cache_weights(const void* q, int dtype, const int64_t* q_strides,
+                                 const float* lse, const sage2_cache* cache, const int* table,
+                                 int max_pages, const int* lens, const int* n, const uint8_t* mask,
+                                 int64_t mask_stride, float* acc, const int64_t* acc_strides, int S,
+                                 int B, int Hq, int T, float sm_scale, sage2_stream_t stream);
+
+/*
+ * Moves rows: slot base[b] + i of out_table takes slot idx[b][h][i] of table, for
+ * K, V, their scales and (if acc is given) the tally: acc_out[b][h][base[b] + i] =
+ * acc[b][h][idx[b][h][i]], i < n[b].
+ *   idx  : DEVICE int32 [B, Hkv, M], idx_strides {batch, head} (0 allowed).
+ *   n, base : DEVICE int32 [B]; NULL: M and 0.
+ * out_table NULL or equal to table: in place.  Rows then only move towards the
+ * front, idx[i] >= base + i, in any order and with repeats; a row that would move
+ * back is left out and sets the device error word.  acc_out may be acc then.
+ * Otherwise the pages of out_table must not be among those of table, nor acc_out
+ * overlap acc.  No row of the result may be named twice.
+ */
+sage2_status sage2_cache_compact(const sage2_cache* cache, const int* table, int max_pages,
+                                 const int* out_table, int out_max_pages, const int* idx,
+                                 const int64_t* idx_strides, const int* n, const int* base,
+                                 const float* acc, const int64_t* acc_strides, int S, float* acc_out,
+                                 const int64_t* acc_out_strides, int SO, int B, int M,
+                                 sage2_stream_t stream);
+
+/*
+ * Cuts each sequence to at most `keep` tokens a head: the first `sinks`, the last
+ * `recent` and, of those between, the ones with the largest acc (equal ones from
+ * the lowest slot on; NaN counts as lowest).  Sequences with lens[b] <= keep keep
+ * all.  The kept slots go to idx[b][h][..] in ascending order (-1 behind the
+ * last), their number to new_lens[b], and their rows and tallies to the slots 0..
+ * of out_table and acc_out, as sage2_cache_compact does (acc_out NULL is not
+ * allowed; it may be acc when in place).  sinks + recent <= keep.
+ *   idx : DEVICE int32 [B, Hkv, keep].  new_lens : DEVICE int32 [B], not lens.
+ */
+sage2_status sage2_cache_evict(const sage2_cache* cache, const int* table, int max_pages,
+                               const int* out_table, int out_max_pages, const int* lens,
+                               const float* acc, const int64_t* acc_strides, int S, float* acc_out,
+                               const int64_t* acc_out_strides, int SO, int B, int keep, int sinks,
+                               int recent, int* idx, int* new_lens, sage2_stream_t stream);
+
 /* Bytes of workspace sage2_attn_fwd takes for this problem (0 on bad sizes). */
 size_t sage2_workspace_bytes(int B, int H, int N, int d);
 
@@ -292,7 +418,8 @@ sage2_status sage2_debug_wait_timeout(sage2_stream_t stream);
 /*
  * Synchronizes `stream`, then reads and clears the device error word that
  * kernels set instead of trapping.  SAGE2_ERR_TIMEOUT if a bounded wait ran
- * out, SAGE2_ERR_CUDA on a sticky CUDA error, else SAGE2_OK.
+ * out, SAGE2_ERR_BAD_INDEX if a cache entry met a device integer out of range,
+ * SAGE2_ERR_CUDA on a sticky CUDA error, else SAGE2_OK.
  * After SAGE2_ERR_TIMEOUT the outputs of the work enqueued since the last
  * check are invalid (a block that gave up left its rows unwritten); the
  * context stays usable and the call may simply be repeated.  A wait gives up

@@ -19,12 +19,14 @@ import torch
 
 __all__ = [
     "sage2_smooth_quant_qk", "sage2_quant_v", "sage2_attn_fwd_quantized", "sage2_attn_fwd",
-    "sage2_attn_fwd_noalloc", "sage2_attn_fwd_varlen", "sage2_attn_fwd_host", "sage2_debug_qk_s32", "sage2_workspace_bytes", "sage2_check_device_error",
+    "sage2_attn_fwd_noalloc", "sage2_attn_fwd_varlen", "sage2_attn_fwd_host",
+    "sage2_cache_alloc", "sage2_cache_append", "sage2_attn_tree", "sage2_cache_weights",
+    "sage2_cache_compact", "sage2_cache_evict", "sage2_debug_qk_s32", "sage2_workspace_bytes", "sage2_check_device_error",
     "sage2_status_string", "sage2_version", "sage2_layout_info", "attn", "Sage2Error", "lib", "LIB_PATH",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libsage2.so")
-F16, BF16, F32 = 0, 1, 2
+F16, BF16, F32, E4M3 = 0, 1, 2, 3
 QK_INT4, QK_INT8, QK_INT4_PACKED = 0, 1, 2
 _QKF = {4: QK_INT4, 8: QK_INT8}
 
@@ -41,12 +43,13 @@ def _fmt(qk_bits: int, packed: bool = False) -> int:
 _DT = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}
 STATUS = {0: "SAGE2_OK", 1: "SAGE2_ERR_INVALID_ARG", 2: "SAGE2_ERR_UNSUPPORTED",
           3: "SAGE2_ERR_MISALIGNED", 4: "SAGE2_ERR_CUDA", 5: "SAGE2_ERR_NO_MEM",
-          6: "SAGE2_ERR_TIMEOUT", 7: "SAGE2_ERR_TOO_LARGE"}
+          6: "SAGE2_ERR_TIMEOUT", 7: "SAGE2_ERR_TOO_LARGE", 8: "SAGE2_ERR_BAD_INDEX"}
 
 _lib = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
+_L = ctypes.c_int64
 _SIGS = {
     "sage2_smooth_quant_qk": (_I, [_P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P]),
     "sage2_quant_v": (_I, [_P, _I, _I, _I, _I, _I, _P, _P, _P]),
@@ -68,6 +71,14 @@ _SIGS = {
     "sage2_status_string": (ctypes.c_char_p, [_I]),
     "sage2_version": (_I, []),
     "sage2_layout_info": (_I, [_P]),
+    "sage2_cache_append": (_I, [_P, _P, _I, _P, _P, _P, _P, _I, _P, _P, _I, _I, _P]),
+    "sage2_attn_tree": (_I, [_P, _I, _P, _P, _P, _I, _P, _P, _P, _L, _P, _I, _P, _I, _I, _I, _F, _P]),
+    "sage2_cache_weights": (_I, [_P, _I, _P, _P, _P, _P, _I, _P, _P, _P, _L, _P, _P, _I, _I, _I, _I,
+                                 _F, _P]),
+    "sage2_cache_compact": (_I, [_P, _P, _I, _P, _I, _P, _P, _P, _P, _P, _P, _I, _P, _P, _I, _I, _I,
+                                 _P]),
+    "sage2_cache_evict": (_I, [_P, _P, _I, _P, _I, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _P,
+                               _P, _P]),
 }
 
 
@@ -75,6 +86,11 @@ class _Layout(ctypes.Structure):
     _fields_ = [("version", _I), ("block_rows", _I), ("tile_keys", _I), ("int4_max", _I),
                 ("int8_max", _I), ("p_scale", _F), ("v_scale_div", _F),
                 ("packed_low_first", _I), ("key_perm", _I * 128), ("value_perm", _I * 128)]
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = [("k", _P), ("v", _P), ("k_scale", _P), ("v_scale", _P), ("kv_dtype", _I),
+                ("pages", _I), ("Hkv", _I), ("page_size", _I), ("d", _I)]
 
 
 class Sage2Error(RuntimeError):
@@ -382,3 +398,245 @@ def sage2_attn_fwd_host(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: 
                                        float(sm_scale), fmt, int(bool(smooth_v)), st)
     _check("sage2_attn_fwd_host", status)
     return out
+
+
+# ---------------------------------------------------------------------------
+# Paged key/value cache (see include/sage2.h for the layout and the rules)
+
+_KV = {torch.float16: F16, torch.bfloat16: BF16, torch.float8_e4m3fn: E4M3}
+_S2, _S3 = _L * 2, _L * 3
+
+
+def sage2_cache_alloc(pages: int, Hkv: int, page_size: int, d: int, dtype=torch.bfloat16,
+                      device="cuda") -> dict:
+    """An empty cache: the pools k, v [pages, Hkv, page_size, d] in `dtype`
+    (float16, bfloat16, or float8_e4m3fn with the fp32 row scales k_scale,
+    v_scale [pages, Hkv, page_size]).  Any dict of such tensors is a cache."""
+    if dtype not in _KV:
+        raise ValueError("a cache is float16, bfloat16 or float8_e4m3fn")
+    cache = {n: torch.zeros(pages, Hkv, page_size, d, dtype=dtype, device=device) for n in "kv"}
+    if dtype == torch.float8_e4m3fn:
+        for n in "kv":
+            cache[n + "_scale"] = torch.zeros(pages, Hkv, page_size, dtype=torch.float32,
+                                              device=device)
+    return cache
+
+
+def _cache_of(cache: dict):
+    """(sage2_cache, k): the checked cache of a dict."""
+    k, v = cache["k"], cache["v"]
+    if k.dim() != 4 or not k.is_cuda or not k.is_contiguous():
+        raise ValueError("a cache holds contiguous CUDA tensors [pages, Hkv, page_size, d]")
+    if v.shape != k.shape or v.dtype != k.dtype or v.device != k.device or not v.is_contiguous():
+        raise ValueError("the cache's k and v must be alike")
+    ty = _KV.get(k.dtype)
+    if ty is None:
+        raise ValueError("a cache is float16, bfloat16 or float8_e4m3fn")
+    pages, Hkv, page, d = k.shape
+    ks = vs = 0
+    if ty == E4M3:
+        for t in (cache["k_scale"], cache["v_scale"]):
+            if t.shape != k.shape[:3] or t.dtype != torch.float32 or t.device != k.device \
+                    or not t.is_contiguous():
+                raise ValueError("k_scale and v_scale must be contiguous float32 "
+                                 "[pages, Hkv, page_size] on the cache's device")
+        ks, vs = cache["k_scale"].data_ptr(), cache["v_scale"].data_ptr()
+    return _Cache(k.data_ptr(), v.data_ptr(), ks, vs, ty, pages, Hkv, page, d), k
+
+
+def _ints(t: torch.Tensor | None, shape, dev, what: str) -> int:
+    """Address of a contiguous int32 tensor of that shape (0 for None)."""
+    if t is None:
+        return 0
+    if t.dtype != torch.int32 or t.device != dev or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous int32 tensor {list(shape)} on the cache's device")
+    return t.data_ptr()
+
+
+def _table(t: torch.Tensor, dev, B: int | None = None):
+    if t.dim() != 2 or t.dtype != torch.int32 or t.device != dev or not t.is_contiguous() \
+            or (B is not None and t.shape[0] != B):
+        raise ValueError("a page table is a contiguous int32 tensor [B, max_pages] on the cache's device")
+    return t.data_ptr(), t.shape[1]
+
+
+def _bhtd(t: torch.Tensor, dev, d: int, what: str):
+    """Strides of a [B, H, T, d] tensor whose rows are contiguous."""
+    if t.dim() != 4 or t.device != dev or t.shape[3] != d or (d > 1 and t.stride(3) != 1):
+        raise ValueError(f"{what} must be [B, H, T, {d}] on the cache's device, its last dimension contiguous")
+    if t.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError(f"{what} must be float16 or bfloat16")
+    # the stride of a dimension of one element says nothing
+    return _S3(*(t.stride(i) if t.shape[i] > 1 else 0 for i in range(3)))
+
+
+def _tally(t: torch.Tensor, dev, B: int, H: int, what: str):
+    if t.dim() != 3 or t.dtype != torch.float32 or t.device != dev or t.shape[0] != B \
+            or t.shape[1] != H or (t.shape[2] > 1 and t.stride(2) != 1):
+        raise ValueError(f"{what} must be float32 [B, Hkv, slots] on the cache's device, slots contiguous")
+    return _S2(t.stride(0), t.stride(1))
+
+
+def _mask(mask: torch.Tensor | None, dev, B: int, T: int):
+    """(address, bytes between sequences) of a tree mask."""
+    if mask is None:
+        return 0, 0
+    if mask.dtype not in (torch.bool, torch.uint8) or mask.device != dev \
+            or tuple(mask.shape) not in ((T, T), (B, T, T)):
+        raise ValueError("mask must be bool [T, T] or [B, T, T] on the cache's device")
+    if T > 1 and (mask.stride(-1) != 1 or mask.stride(-2) != T):
+        raise ValueError("mask must be contiguous in its last two dimensions")
+    return mask.data_ptr(), mask.stride(0) if mask.dim() == 3 and B > 1 else 0
+
+
+def _run(name: str, dev: torch.device, *args):
+    """The call on torch's current stream of `dev`, with that device current."""
+    fn = getattr(lib(), name)
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if st != 0:
+        raise Sage2Error(name, st)
+
+
+def sage2_cache_append(k: torch.Tensor, v: torch.Tensor, cache: dict, table: torch.Tensor,
+                       lens: torch.Tensor, n: torch.Tensor | None = None) -> dict:
+    """Writes k, v [B, Hkv, T, d] behind the lens[b] tokens in the cache (n[b] of
+    the T tokens; None: all), in the cache's type.  `lens` is not changed."""
+    cs, pool = _cache_of(cache)
+    dev = pool.device
+    if k.shape != v.shape or k.dtype != v.dtype:
+        raise ValueError("k and v must have the same shape and dtype")
+    sk, sv = _bhtd(k, dev, cs.d, "k"), _bhtd(v, dev, cs.d, "v")
+    B, H, T = k.shape[:3]
+    if H != cs.Hkv:
+        raise ValueError("k and v must have the cache's heads")
+    tp, mp = _table(table, dev, B)
+    _run("sage2_cache_append", dev, k.data_ptr(), v.data_ptr(), _DT[k.dtype], sk, sv,
+         ctypes.byref(cs), tp, mp, _ints(lens, (B,), dev, "lens"), _ints(n, (B,), dev, "n"), B, T)
+    return cache
+
+
+def sage2_attn_tree(q: torch.Tensor, cache: dict, table: torch.Tensor, lens: torch.Tensor,
+                    mask: torch.Tensor | None = None, n: torch.Tensor | None = None,
+                    sm_scale: float | None = None, out_dtype=None,
+                    out: torch.Tensor | None = None, lse: torch.Tensor | None = None):
+    """Attention of T drafted tokens q [B, Hq, T, d] (T = 1: a decode step) over the
+    lens[b] cached tokens and the drafted ones behind them (already in the
+    cache).  mask [T, T] or [B, T, T]: row i marks the drafted tokens that token
+    i attends (None: those up to itself).  n[b] of the T tokens are in use (None:
+    all).  Returns (o [B, Hq, T, d], lse [B, Hq, T])."""
+    cs, pool = _cache_of(cache)
+    dev = pool.device
+    sq = _bhtd(q, dev, cs.d, "q")
+    B, Hq, T, d = q.shape
+    tp, mp = _table(table, dev, B)
+    mptr, mstride = _mask(mask, dev, B, T)
+    if out is None:
+        out = torch.empty(B, Hq, T, d, dtype=out_dtype or q.dtype, device=dev)
+    elif out.shape != q.shape or out.device != dev or not out.is_contiguous() or out.dtype not in _DT:
+        raise ValueError("out must be contiguous, of q's shape and on its device")
+    if lse is None:
+        lse = torch.empty(B, Hq, T, dtype=torch.float32, device=dev)
+    elif lse.shape != (B, Hq, T) or lse.dtype != torch.float32 or lse.device != dev \
+            or not lse.is_contiguous():
+        raise ValueError("lse must be contiguous float32 [B, Hq, T]")
+    _run("sage2_attn_tree", dev, q.data_ptr(), _DT[q.dtype], sq, ctypes.byref(cs), tp, mp,
+         _ints(lens, (B,), dev, "lens"), _ints(n, (B,), dev, "n"), mptr, mstride, out.data_ptr(),
+         _DT[out.dtype], lse.data_ptr(), B, Hq, T,
+         1.0 / math.sqrt(d) if sm_scale is None else sm_scale)
+    return out, lse
+
+
+def sage2_cache_weights(q: torch.Tensor, lse: torch.Tensor, cache: dict, table: torch.Tensor,
+                        lens: torch.Tensor, acc: torch.Tensor, mask: torch.Tensor | None = None,
+                        n: torch.Tensor | None = None, sm_scale: float | None = None) -> torch.Tensor:
+    """Adds to acc [B, Hkv, slots] (float32) the attention weight that each cached
+    token received from q, over all its heads and drafted tokens; the arguments
+    are those of sage2_attn_tree and the lse it returned."""
+    cs, pool = _cache_of(cache)
+    dev = pool.device
+    sq = _bhtd(q, dev, cs.d, "q")
+    B, Hq, T, d = q.shape
+    tp, mp = _table(table, dev, B)
+    mptr, mstride = _mask(mask, dev, B, T)
+    if lse.shape != (B, Hq, T) or lse.dtype != torch.float32 or lse.device != dev \
+            or not lse.is_contiguous():
+        raise ValueError("lse must be contiguous float32 [B, Hq, T]")
+    sa = _tally(acc, dev, B, cs.Hkv, "acc")
+    _run("sage2_cache_weights", dev, q.data_ptr(), _DT[q.dtype], sq, lse.data_ptr(),
+         ctypes.byref(cs), tp, mp, _ints(lens, (B,), dev, "lens"), _ints(n, (B,), dev, "n"), mptr,
+         mstride, acc.data_ptr(), sa, acc.shape[2], B, Hq, T,
+         1.0 / math.sqrt(d) if sm_scale is None else sm_scale)
+    return acc
+
+
+def _out_table(table, out_table, dev, B):
+    """(address, width) of the table to write to; 0: in place."""
+    if out_table is None or out_table is table:
+        return 0, table.shape[1]
+    return _table(out_table, dev, B)
+
+
+def sage2_cache_compact(cache: dict, table: torch.Tensor, idx: torch.Tensor,
+                        n: torch.Tensor | None = None, base: torch.Tensor | None = None,
+                        out_table: torch.Tensor | None = None, acc: torch.Tensor | None = None,
+                        acc_out: torch.Tensor | None = None) -> dict:
+    """Moves rows: slot base[b] + i of out_table takes slot idx[b, h, i] of table,
+    i < n[b] (None: all of idx [B, Hkv, M]; base None: 0).  out_table None: in
+    place, rows moving towards the front only.  For an accepted path of a tree:
+    idx = lens + path, base = lens, the same for every head (an expanded idx).  With
+    acc [B, Hkv, slots] its values move along, to acc_out (None: in place)."""
+    cs, pool = _cache_of(cache)
+    dev = pool.device
+    if idx.dim() != 3 or idx.dtype != torch.int32 or idx.device != dev or idx.shape[1] != cs.Hkv \
+            or (idx.shape[2] > 1 and idx.stride(2) != 1):
+        raise ValueError("idx must be int32 [B, Hkv, M] on the cache's device, M contiguous")
+    B, _, M = idx.shape
+    tp, mp = _table(table, dev, B)
+    op, om = _out_table(table, out_table, dev, B)
+    if acc is None and acc_out is not None:
+        raise ValueError("acc_out needs acc")
+    sa = so = None
+    S = SO = ap = aop = 0
+    if acc is not None:
+        acc_out = acc if acc_out is None else acc_out
+        if out_table is not None and out_table is not table and acc_out.data_ptr() == acc.data_ptr():
+            raise ValueError("acc_out must be another tensor than acc when out_table is another table")
+        sa, so = _tally(acc, dev, B, cs.Hkv, "acc"), _tally(acc_out, dev, B, cs.Hkv, "acc_out")
+        S, SO, ap, aop = acc.shape[2], acc_out.shape[2], acc.data_ptr(), acc_out.data_ptr()
+    _run("sage2_cache_compact", dev, ctypes.byref(cs), tp, mp, op, om, idx.data_ptr(),
+         _S2(idx.stride(0), idx.stride(1)), _ints(n, (B,), dev, "n"), _ints(base, (B,), dev, "base"),
+         ap, sa, S, aop, so, SO, B, M)
+    return cache
+
+
+def sage2_cache_evict(cache: dict, table: torch.Tensor, lens: torch.Tensor, acc: torch.Tensor,
+                      keep: int, sinks: int = 0, recent: int = 0,
+                      out_table: torch.Tensor | None = None, acc_out: torch.Tensor | None = None):
+    """Cuts each sequence to at most `keep` tokens a head: the first `sinks`, the last
+    `recent` and those of the largest acc [B, Hkv, slots] between them.  The kept
+    rows move to the slots 0.. of out_table (None: in place), their tallies to
+    acc_out (None: a new tensor [B, Hkv, keep]).  Returns (idx int32 [B, Hkv, keep]:
+    the kept slots, ascending, -1 behind the last; lens int32 [B]; acc_out)."""
+    cs, pool = _cache_of(cache)
+    dev = pool.device
+    B = lens.shape[0] if lens.dim() == 1 else -1
+    tp, mp = _table(table, dev, B)
+    op, om = _out_table(table, out_table, dev, B)
+    sa = _tally(acc, dev, B, cs.Hkv, "acc")
+    if keep <= 0:
+        raise ValueError("keep must be positive")
+    if acc_out is None:
+        acc_out = torch.zeros(B, cs.Hkv, keep, dtype=torch.float32, device=dev)
+    elif op and acc_out.data_ptr() == acc.data_ptr():
+        raise ValueError("acc_out must be another tensor than acc when out_table is another table")
+    so = _tally(acc_out, dev, B, cs.Hkv, "acc_out")
+    idx = torch.empty(B, cs.Hkv, keep, dtype=torch.int32, device=dev)
+    new = torch.empty(B, dtype=torch.int32, device=dev)
+    _run("sage2_cache_evict", dev, ctypes.byref(cs), tp, mp, op, om, _ints(lens, (B,), dev, "lens"),
+         acc.data_ptr(), sa, acc.shape[2], acc_out.data_ptr(), so, acc_out.shape[2], B, keep, sinks,
+         recent, idx.data_ptr(), new.data_ptr())
+    return idx, new, acc_out

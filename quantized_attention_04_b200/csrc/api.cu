@@ -484,6 +484,7 @@ sage2_status sage2_check_device_error(sage2_stream_t stream) {
       return SAGE2_ERR_CUDA;
   }
   if (word & DEVERR_TIMEOUT) return SAGE2_ERR_TIMEOUT;
+  if (word & DEVERR_BOUNDS) return SAGE2_ERR_BAD_INDEX;
   if (word) return SAGE2_ERR_CUDA;
   return SAGE2_OK;
 }
@@ -497,6 +498,7 @@ const char* sage2_status_string(sage2_status status) {
     case SAGE2_ERR_CUDA: return "CUDA error";
     case SAGE2_ERR_NO_MEM: return "out of device memory";
     case SAGE2_ERR_TIMEOUT: return "device wait timed out";
+    case SAGE2_ERR_BAD_INDEX: return "a length, page or slot on the device is out of range";
     case SAGE2_ERR_TOO_LARGE: return "scratch needed exceeds the fixed no-allocation buffer";
   }
   return "unknown status";

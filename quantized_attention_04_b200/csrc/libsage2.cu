@@ -9,3 +9,5 @@
 #include "noalloc.cu"
 #include "varlen.cu"
 #include "host_pipe.cu"
+#include "cache.cu"
+#include "tree.cu"

@@ -1,0 +1,1092 @@
+// Attention of drafted tokens over a paged cache (sage2_attn_tree) and the
+// tally of attention weight per cached token (sage2_cache_weights).
+//
+// Row r = g*T + i of key/value head h is drafted token i of query head h*G + g
+// (G = Hq/Hkv); its keys are the slots [0, lens[b]) and, of the drafted tokens'
+// slots lens[b] + j (j < n[b]), those that the mask allows (no mask: j <= i).
+//
+// Work split.  The tiles of all (sequence, head, row tile) pairs, in that order,
+// form one sequence that the blocks cut into equal runs, so unequal lengths
+// need no plan from the host, which does not know them.  A pair that one block
+// covers whole is written at once; the pieces of the others go to a
+// workspace with their row maxima and sums and k_tree_join adds them.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "sage2.h"
+#include "sage2_internal.h"
+#include "sm100_ptx.cuh"
+
+namespace sage2 {
+
+struct TreeArgs {
+  CacheView c;
+  const int* table;
+  const int* lens;
+  const int* n;             // null: T
+  const uint8_t* mask;      // null: j <= i
+  long long mask_sb;        // bytes between the masks of consecutive sequences
+  const void* q;
+  long long sb, sh, st;     // strides of q in elements
+  void* o;
+  int o_dtype;
+  float* lse;
+  int B, Hq, G, T, MP;
+  float sm_scale;
+  int RT;                   // row tiles of a (sequence, head) pair
+  float* part;              // [2*grid][rows of a tile][d]
+  float2* part_ml;          // [2*grid][rows of a tile]: (max in log2 units, sum)
+};
+
+// Context length and drafted tokens of sequence b, held to what the table can hold.
+struct SeqLen {
+  int len, n;
+};
+__device__ __forceinline__ SeqLen seq_len(const int* lens, const int* ns, int b, int T, int MP,
+                                          int page_shift) {
+  SeqLen s;
+  s.len = __ldg(lens + b);
+  s.n = ns ? __ldg(ns + b) : T;
+  const int cap = MP << page_shift;
+  if (static_cast<unsigned>(s.n) > static_cast<unsigned>(T) || s.len < 0 || s.len > cap - s.n) {
+    atomicOr(&g_device_error, DEVERR_BOUNDS);
+    s.n = min(max(s.n, 0), min(T, cap));
+    s.len = min(max(s.len, 0), cap - s.n);
+  }
+  return s;
+}
+
+// Is drafted token j among the keys of drafted token i?  (j < n)
+__device__ __forceinline__ bool tree_allows(const uint8_t* mask, int T, int i, int j) {
+  return mask ? __ldg(mask + (size_t)i * T + j) != 0 : j <= i;
+}
+
+// ------------------------------------------------------------ the work split
+// Tiles of one pair of sequence b: none if nothing is asked of it.
+__device__ __forceinline__ int pair_tiles(SeqLen s, int tile) {
+  return s.n == 0 ? 0 : (s.len + s.n + tile - 1) / tile;
+}
+
+// The block's run [t0, t1) of the global tile sequence, in shared memory, with
+// the pair it starts in.  `pairs`: pairs of one sequence (Hkv*RT).
+struct Run {
+  long long total, t0, t1;
+  int b, pair, tile;       // where t0 is
+  int grid;                // blocks that have work
+};
+
+__device__ __forceinline__ long long run_start(long long total, int grid, int c) {
+  return total * c / grid;
+}
+
+// Called by the whole block (blockDim.x threads, whole warps).  Finds the run of
+// block `c` of `grid`, no block taking fewer than `least` tiles while others have none.
+__device__ void find_run(const TreeArgs& a, int tile, int pairs, int grid, int c, int least, Run* out,
+                         long long* scratch) {
+  const int tid = threadIdx.x, nth = blockDim.x, lane = tid & 31, warp = tid >> 5;
+  // pass 1: the total; pass 2: the sequence that holds t0
+  long long total = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    long long carry = 0;
+    for (int b0 = 0; b0 < a.B; b0 += nth) {
+      const int b = b0 + tid;
+      int tl = 0;
+      if (b < a.B) tl = pair_tiles(seq_len(a.lens, a.n, b, a.T, a.MP, a.c.page_shift), tile);
+      const long long mine = (long long)tl * pairs;
+      long long incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      if (lane == 31) scratch[warp] = incl;
+      __syncthreads();
+      long long before = carry, all = 0;
+      for (int w = 0; w < nth / 32; ++w) {
+        const long long x = scratch[w];
+        if (w < warp) before += x;
+        all += x;
+      }
+      if (pass == 1) {
+        const long long first = before + incl - mine;
+        if (mine > 0 && out->t0 >= first && out->t0 < first + mine) {
+          const long long off = out->t0 - first;
+          out->b = b;
+          out->pair = (int)(off / tl);
+          out->tile = (int)(off % tl);
+        }
+      }
+      carry += all;
+      __syncthreads();
+    }
+    if (pass == 0) {
+      total = carry;
+      if (tid == 0) {
+        const long long most = (total + least - 1) / least;
+        const int g = (int)(most < grid ? (most < 1 ? 1 : most) : grid);
+        out->total = total;
+        out->grid = g;
+        out->t0 = c < g ? run_start(total, g, c) : total;
+        out->t1 = c < g ? run_start(total, g, c + 1) : total;
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// Walks the tiles of a run.
+struct Cursor {
+  int b, pair, tile, tiles;
+  SeqLen s;
+  __device__ __forceinline__ void load(const TreeArgs& a, int tl) {
+    s = seq_len(a.lens, a.n, b, a.T, a.MP, a.c.page_shift);
+    tiles = pair_tiles(s, tl);
+  }
+  __device__ __forceinline__ void start(const TreeArgs& a, const Run& r, int tl) {
+    b = r.b;
+    pair = r.pair;
+    tile = r.tile;
+    load(a, tl);
+  }
+  // to the next tile of the run, which exists
+  __device__ __forceinline__ void next(const TreeArgs& a, int pairs, int tl) {
+    if (++tile < tiles) return;
+    tile = 0;
+    if (++pair < pairs) return;
+    pair = 0;
+    do {
+      ++b;
+      load(a, tl);
+    } while (tiles == 0 && b + 1 < a.B);
+  }
+};
+
+// ------------------------------------------------------------ legacy-path MMA
+// D (16x8, fp32) += A (16x16) * B (16x8), fp16 or bf16.
+template <bool BF>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if (BF)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// Two e4m3 codes (bits 15:0) to two fp16 values, exact.
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t two) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3);
+  return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
+}
+template <bool BF>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if (BF) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Four consecutive values (index of the first, a multiple of 4) in the output type.
+__device__ __forceinline__ void store4(void* out, int dtype, size_t idx, const float (&f)[4]) {
+  if (dtype == 2) {
+    *reinterpret_cast<float4*>(static_cast<float*>(out) + idx) = make_float4(f[0], f[1], f[2], f[3]);
+  } else {
+    const uint2 w = dtype == 1 ? make_uint2(pack2<true>(f[0], f[1]), pack2<true>(f[2], f[3]))
+                               : make_uint2(pack2<false>(f[0], f[1]), pack2<false>(f[2], f[3]));
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + idx) = w;
+  }
+}
+// ln of a row's sum of exponentials from its maximum (log2 units) and the sum relative to it.
+__device__ __forceinline__ float row_lse(float m, float sum) {
+  return (m + log2f(sum)) * 0.6931471805599453f;
+}
+
+// ------------------------------------------------------------ few rows
+// k_tree_rows: a tile of 16*MT rows (all the rows of a pair where T*G is small)
+// against the keys.  Bound by the cache's bytes: at up to 32 rows a byte of
+// 16-bit cache meets at most 32 multiply-adds, which the legacy tensor path
+// (no TMEM round trip, P stays in registers) sustains well above the rate at
+// which HBM delivers.  Four warps; warp w owns keys 16w..16w+15 of each 64-key
+// tile, with its own ring of TMA-filled stages, its own running maximum and sum
+// and its own accumulator, so that nothing in the loop waits for another warp;
+// they are added when the piece ends.
+//
+// e4m3 cache: codes become fp16 in registers (exact).  Q (fp16 or bf16) enters as
+// fp16 scaled by a power of two that puts the row's largest value at 2^13 (what
+// falls below fp16's range is under 2^-37 of it).  The key scales multiply the
+// scores; the value scales multiply P relative to the largest one seen
+// (vref, carried like the running maximum), so P stays within [0, 1].
+constexpr int kRowsWarps = 4;
+constexpr float kVrefLeast = 1e-30f;   // value scales below it count as part of it
+constexpr int kRowsTile = 16 * kRowsWarps;
+
+template <int D, bool E4M3>
+struct RowsCfg {
+  static constexpr int kRowBytes = D * (E4M3 ? 1 : 2);
+  static constexpr int kBoxBytes = kRowBytes < 128 ? kRowBytes : 128;   // swizzle span
+  static constexpr int kBoxes = kRowBytes / kBoxBytes;
+  static constexpr int kTileBytes = 16 * kRowBytes;                     // K or V of a warp's 16 keys
+  static constexpr int kStageBytes = 2 * kTileBytes;
+  static constexpr int kStages = E4M3 ? (D == 128 ? 6 : 8) : (D == 128 ? 3 : 6);
+};
+
+template <int D, bool E4M3>
+struct __align__(1024) RowsSmem {
+  using C = RowsCfg<D, E4M3>;
+  uint8_t kv[kRowsWarps][C::kStages][C::kStageBytes];
+  float sc[kRowsWarps][C::kStages][E4M3 ? 32 : 4];  // key scales, value scales
+  float red[kRowsWarps][16][36];                    // 32 columns of the rows of an m-tile
+  float2 ml[kRowsWarps][16];
+  uint64_t full[kRowsWarps][C::kStages];
+  int bad[kRowsWarps][C::kStages];                  // the stage's page was out of range
+  long long scratch[kRowsWarps];
+  Run run;
+  int abort_flag;
+};
+
+// Byte offset of 16-byte chunk `ch` of row `r` in a tile of 16 rows.
+template <int D, bool E4M3>
+__device__ __forceinline__ uint32_t rows_off(int r, int ch) {
+  using C = RowsCfg<D, E4M3>;
+  if (C::kBoxBytes == 128)
+    return (ch >> 3) * (16 * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
+  return r * 64 + ((ch ^ ((r >> 1) & 3)) << 4);
+}
+
+template <int D, bool E4M3, bool QBF, int MT>
+__global__ void __launch_bounds__(32 * kRowsWarps, 2)
+    k_tree_rows(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                const __grid_constant__ TreeArgs a) {
+  using C = RowsCfg<D, E4M3>;
+  constexpr bool BF = QBF && !E4M3;           // type of the MMA operands
+  constexpr int NT = D / 8;                   // n-tiles of O
+  extern __shared__ uint8_t smem_raw[];
+  RowsSmem<D, E4M3>& sm = *reinterpret_cast<RowsSmem<D, E4M3>*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, c = lane & 3;
+  const int R = a.G * a.T, pairs = a.c.Hkv * a.RT;
+  if (tid == 0) {
+    for (int w = 0; w < kRowsWarps; ++w)
+      for (int s = 0; s < C::kStages; ++s) mbar_init(&sm.full[w][s], 1);
+    sm.abort_flag = 0;
+    fence_mbar_init();
+  }
+  find_run(a, kRowsTile, pairs, gridDim.x, blockIdx.x, 2, &sm.run, sm.scratch);
+  __syncthreads();
+  const long long t0 = sm.run.t0;
+  const int nt = (int)(sm.run.t1 - t0);
+  if (nt <= 0) return;
+  Cursor in, at;                              // where loads are issued; where work is done
+  in.start(a, sm.run, kRowsTile);
+  at = in;
+  int issued = 0, used = 0, in_t = 0;         // tiles with keys of this warp
+  // Issues the loads of the next tile in which this warp has keys, if the run has one.
+  auto issue = [&]() {
+    while (in_t < nt) {
+      const int key0 = in.tile * kRowsTile + warp * 16;
+      const bool here = key0 < in.s.len + in.s.n;
+      if (here && lane == 0) {
+        const int st = issued % C::kStages;
+        int page = __ldg(a.table + (size_t)in.b * a.MP + (key0 >> a.c.page_shift));
+        const bool ok = static_cast<unsigned>(page) < static_cast<unsigned>(a.c.pages);
+        if (!ok) {
+          atomicOr(&g_device_error, DEVERR_BOUNDS);
+          page = 0;
+        }
+        sm.bad[warp][st] = !ok;
+        const int h = in.pair / a.RT;
+        const int row = ((page * a.c.Hkv + h) << a.c.page_shift) + (key0 & ((1 << a.c.page_shift) - 1));
+        uint64_t* bar = &sm.full[warp][st];
+        uint8_t* dst = sm.kv[warp][st];
+        mbar_expect_tx(bar, C::kStageBytes + (E4M3 ? 128 : 0));
+#pragma unroll
+        for (int x = 0; x < C::kBoxes; ++x) {
+          tma_load_2d(dst + x * 2048, &tm_k, bar, x * 64, row);
+          tma_load_2d(dst + C::kTileBytes + x * 2048, &tm_v, bar, x * 64, row);
+        }
+        if (E4M3) {
+          bulk_load(sm.sc[warp][st], a.c.ks + row, 64, bar);
+          bulk_load(sm.sc[warp][st] + 16, a.c.vs + row, 64, bar);
+        }
+      }
+      ++in_t;
+      if (in_t < nt) in.next(a, pairs, kRowsTile);
+      if (here) {
+        ++issued;
+        return;
+      }
+    }
+  };
+  for (int s = 0; s < C::kStages; ++s) issue();
+  __syncwarp();                               // lane 0's sm.bad
+
+  uint32_t qf[MT][D / 16][4];
+  float acc[MT][NT][4];
+  float m[MT][2], l[MT][2], qs[MT][2], vref = kVrefLeast;
+  const float kL2E = 1.4426950408889634f;
+
+  for (int t = 0; t < nt; ++t) {
+    const int L = at.s.len + at.s.n;
+    const int row0 = (at.pair % a.RT) * 16 * MT;
+    const int h = at.pair / a.RT;
+    if (t == 0 || at.tile == 0) {
+      // a piece starts: its rows' Q fragments
+      vref = kVrefLeast;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const uint16_t* src[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = row0 + mt * 16 + g + 8 * e;
+          src[e] = r < R ? static_cast<const uint16_t*>(a.q) + at.b * a.sb +
+                               (long long)(h * a.G + r / a.T) * a.sh + (long long)(r % a.T) * a.st
+                         : nullptr;
+          m[mt][e] = -INFINITY;
+          l[mt][e] = 0.f;
+          qs[mt][e] = a.sm_scale * kL2E;
+        }
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            // 16 bit: k = 16 ks + 2c (+8).  e4m3: the thread's bytes of a key are
+            // contiguous (D/4 of them), so k-step ks takes d = (D/4) c + 4 ks + {0,1}, {2,3}
+            const int dd = E4M3 ? (D / 4) * c + 4 * ks + 2 * (u >> 1) : 16 * ks + 2 * c + 8 * (u >> 1);
+            qf[mt][ks][u] = src[u & 1] ? __ldg(reinterpret_cast<const uint32_t*>(src[u & 1] + dd)) : 0u;
+          }
+        if (E4M3) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float amax = 0.f;
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+              for (int u = e; u < 4; u += 2) {
+                const uint32_t w = qf[mt][ks][u];
+                float x, y;
+                if (QBF) {
+                  x = __uint_as_float(w << 16);
+                  y = __uint_as_float(w & 0xffff0000u);
+                } else {
+                  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+                  x = f.x;
+                  y = f.y;
+                }
+                amax = fmaxf(amax, fmaxf(fabsf(x), fabsf(y)));
+              }
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+            // 2^(13 - exponent): an exact power of two; left alone where the row is 0 or not finite
+            const int ex = (int)(__float_as_uint(amax) >> 23);
+            const int sh = (ex == 0 || ex == 255) ? 0 : max(-110, min(110, 13 + 127 - ex));
+            const float up = __uint_as_float((uint32_t)(127 + sh) << 23);
+            qs[mt][e] *= __uint_as_float((uint32_t)(127 - sh) << 23);
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+              for (int u = e; u < 4; u += 2) {
+                const uint32_t w = qf[mt][ks][u];
+                float x, y;
+                if (QBF) {
+                  x = __uint_as_float(w << 16);
+                  y = __uint_as_float(w & 0xffff0000u);
+                } else {
+                  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+                  x = f.x;
+                  y = f.y;
+                }
+                qf[mt][ks][u] = pack2<false>(x * up, y * up);
+              }
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) acc[mt][j][u] = 0.f;
+      }
+    }
+
+    const int key0 = at.tile * kRowsTile + warp * 16;
+    if (key0 < L) {
+      const int st = used % C::kStages;
+      if (!mbar_wait_warp(&sm.full[warp][st], (used / C::kStages) & 1, &sm.abort_flag)) {
+        // let the copies already issued land before the block exits
+        for (int u = used; u < issued; ++u)
+          mbar_wait(&sm.full[warp][u % C::kStages], (u / C::kStages) & 1, nullptr);
+        return;
+      }
+      const uint8_t* kt = sm.kv[warp][st];
+      const uint8_t* vt = kt + C::kTileBytes;
+      const int live = sm.bad[warp][st] ? 0 : min(16, L - key0);   // keys of this tile that exist
+      if (live < 16) {
+        // rows behind the last key may hold anything: P is 0 there, and V must not be NaN
+        uint8_t* vz = sm.kv[warp][st] + C::kTileBytes;
+        for (int i = lane; i < (16 - live) * (C::kRowBytes / 16); i += 32)
+          *reinterpret_cast<uint4*>(vz + rows_off<D, E4M3>(live + i / (C::kRowBytes / 16),
+                                                          i % (C::kRowBytes / 16))) =
+              make_uint4(0u, 0u, 0u, 0u);
+        if (E4M3 && lane >= live && lane < 16) {
+          sm.sc[warp][st][lane] = 0.f;
+          sm.sc[warp][st][16 + lane] = 0.f;
+        }
+        __syncwarp();
+      }
+      // ---- S = Q K^T
+      float s[MT][2][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) s[mt][j][u] = 0.f;
+      if (!E4M3) {
+        const uint32_t base = smem_u32(kt);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          uint32_t b[4];
+          const int key = (lane >> 4) * 8 + (lane & 7), ch = 2 * ks + ((lane >> 3) & 1);
+          ldsm4(base + rows_off<D, E4M3>(key, ch), b);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            mma16816<BF>(s[mt][0], qf[mt][ks], b[0], b[1]);
+            mma16816<BF>(s[mt][1], qf[mt][ks], b[2], b[3]);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int x = 0; x < D / 64; ++x) {
+            // 16 bytes of key 8j + g: d = (D/4) c + 16 x ..
+            const uint4 w = *reinterpret_cast<const uint4*>(
+                kt + rows_off<D, E4M3>(8 * j + g, (D / 64) * c + x));
+            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const uint32_t b0 = e4m3x2_f16x2(ww[y] & 0xffffu), b1 = e4m3x2_f16x2(ww[y] >> 16);
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) mma16816<BF>(s[mt][j], qf[mt][4 * x + y], b0, b1);
+            }
+          }
+      }
+      // ---- softmax of the 16 keys: this thread has keys 8j + 2c + {0,1} of rows g, g+8
+      float kscl[2][2], vscl[2][2];
+      bool vup = false;
+      float vold = vref;
+      if (E4M3) {
+        float vm = 0.f;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            kscl[j][e] = sm.sc[warp][st][8 * j + 2 * c + e];
+            vscl[j][e] = sm.sc[warp][st][16 + 8 * j + 2 * c + e];
+            vm = fmaxf(vm, vscl[j][e]);
+          }
+        vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 1));
+        vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 2));
+        vup = vm > vref;
+        vref = fmaxf(vref, vm);
+        const float iv = __fdividef(1.f, vref);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) vscl[j][e] *= iv;
+      }
+      const bool edge = key0 + 16 > at.s.len || live < 16;
+      uint32_t pf[MT][4];
+      bool grew = vup;
+      float al[MT][2];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x[2][2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+              x[j][y] = s[mt][j][2 * e + y] * (E4M3 ? qs[mt][e] * kscl[j][y] : qs[mt][e]);
+          if (edge) {
+            const int r = row0 + mt * 16 + g + 8 * e;
+            const int i = r % a.T;
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                const int k = 8 * j + 2 * c + y, jj = key0 + k - at.s.len;
+                const bool ok = k < live && r < R &&
+                                (jj < 0 || tree_allows(a.mask ? a.mask + at.b * a.mask_sb : nullptr, a.T, i, jj));
+                if (!ok) x[j][y] = -INFINITY;
+              }
+          }
+          float mx = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[1][0], x[1][1]));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          const float mn = fmaxf(m[mt][e], mx);
+          const float mb = mn == -INFINITY ? 0.f : mn;
+          al[mt][e] = ex2(m[mt][e] - mb);
+          grew = grew || mn > m[mt][e];
+          m[mt][e] = mn;
+          float p[2][2], sum = 0.f;
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              p[j][y] = ex2(x[j][y] - mb);
+              sum += p[j][y];
+              if (E4M3) p[j][y] *= vscl[j][y];
+            }
+          l[mt][e] = l[mt][e] * al[mt][e] + sum;
+          pf[mt][e] = pack2<BF>(p[0][0], p[0][1]);
+          pf[mt][2 + e] = pack2<BF>(p[1][0], p[1][1]);
+        }
+      if (__any_sync(0xffffffffu, grew)) {
+        const float vr = (E4M3 && vup) ? __fdividef(vold, vref) : 1.f;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            acc[mt][j][0] *= al[mt][0] * vr;
+            acc[mt][j][1] *= al[mt][0] * vr;
+            acc[mt][j][2] *= al[mt][1] * vr;
+            acc[mt][j][3] *= al[mt][1] * vr;
+          }
+      }
+      // ---- O += P V
+      if (!E4M3) {
+        const uint32_t base = smem_u32(vt);
+#pragma unroll
+        for (int jj = 0; jj < NT / 2; ++jj) {
+          uint32_t b[4];
+          const int key = ((lane >> 3) & 1) * 8 + (lane & 7), ch = 2 * jj + (lane >> 4);
+          ldsm4_t(base + rows_off<D, E4M3>(key, ch), b);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            mma16816<BF>(acc[mt][2 * jj], pf[mt], b[0], b[1]);
+            mma16816<BF>(acc[mt][2 * jj + 1], pf[mt], b[2], b[3]);
+          }
+        }
+      } else {
+        // keys 2c, 2c+1, 2c+8, 2c+9; column g of n-tile j is d = (D/8) g + j
+        uint32_t w[4][D / 32];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int key = 2 * c + (k & 1) + 8 * (k >> 1);
+          if (D == 128) {
+            *reinterpret_cast<uint4*>(w[k]) =
+                *reinterpret_cast<const uint4*>(vt + rows_off<D, E4M3>(key, g));
+          } else {
+            *reinterpret_cast<uint2*>(w[k]) =
+                *reinterpret_cast<const uint2*>(vt + rows_off<D, E4M3>(key, g >> 1) + 8 * (g & 1));
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < D / 32; ++x)
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            const uint32_t sel = hh ? 0x7362u : 0x5140u;
+            const uint32_t lo = __byte_perm(w[0][x], w[1][x], sel);
+            const uint32_t hi = __byte_perm(w[2][x], w[3][x], sel);
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const uint32_t b0 = e4m3x2_f16x2(y ? lo >> 16 : lo & 0xffffu);
+              const uint32_t b1 = e4m3x2_f16x2(y ? hi >> 16 : hi & 0xffffu);
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) mma16816<BF>(acc[mt][4 * x + 2 * hh + y], pf[mt], b0, b1);
+            }
+          }
+      }
+      __syncwarp();
+      if (live < 16) fence_proxy_async_smem();   // the zeros above, before the next TMA write
+      __syncwarp();
+      ++used;
+      issue();
+    }
+
+    // ---- the piece ends with the pair's last tile or the run's
+    if (at.tile + 1 == at.tiles || t + 1 == nt) {
+      const int first = at.tile - min(t, at.tile);   // the piece's first tile of the pair
+      const bool whole = first == 0 && at.tile + 1 == at.tiles;
+      const int slot = 2 * blockIdx.x + (first == 0 ? 1 : 0);
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        if (row0 + mt * 16 >= R) break;              // uniform: no such rows
+        float f[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = l[mt][e];
+          x += __shfl_xor_sync(0xffffffffu, x, 1);
+          x += __shfl_xor_sync(0xffffffffu, x, 2);
+          if (c == 0) sm.ml[warp][g + 8 * e] = make_float2(m[mt][e], x);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float M = -INFINITY;
+#pragma unroll
+          for (int w = 0; w < kRowsWarps; ++w) M = fmaxf(M, sm.ml[w][g + 8 * e].x);
+          f[e] = ex2(m[mt][e] - (M == -INFINITY ? 0.f : M)) * (E4M3 ? vref : 1.f);
+        }
+#pragma unroll
+        for (int part = 0; part < D / 32; ++part) {
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            if (!E4M3) {
+              if (j / 4 == part) {
+                *reinterpret_cast<float2*>(&sm.red[warp][g][8 * (j % 4) + 2 * c]) =
+                    make_float2(acc[mt][j][0] * f[0], acc[mt][j][1] * f[0]);
+                *reinterpret_cast<float2*>(&sm.red[warp][g + 8][8 * (j % 4) + 2 * c]) =
+                    make_float2(acc[mt][j][2] * f[1], acc[mt][j][3] * f[1]);
+              }
+            } else {
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                const int dd = (D / 8) * (2 * c + (u & 1)) + j;
+                if (dd / 32 == part) sm.red[warp][g + 8 * (u >> 1)][dd % 32] = acc[mt][j][u] * f[u >> 1];
+              }
+            }
+          }
+          __syncthreads();
+          const int rr = tid / 8, col = (tid % 8) * 4;
+          const int r = row0 + mt * 16 + rr;
+          if (r < R) {
+            float M = -INFINITY, sum = 0.f, o4[4];
+#pragma unroll
+            for (int w = 0; w < kRowsWarps; ++w) M = fmaxf(M, sm.ml[w][rr].x);
+            const float mb = M == -INFINITY ? 0.f : M;
+#pragma unroll
+            for (int w = 0; w < kRowsWarps; ++w) sum += ex2(sm.ml[w][rr].x - mb) * sm.ml[w][rr].y;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              o4[i] = sm.red[0][rr][col + i];
+#pragma unroll
+              for (int w = 1; w < kRowsWarps; ++w) o4[i] += sm.red[w][rr][col + i];
+            }
+            if (whole) {
+              const int i = r % a.T;
+              const bool none = i >= at.s.n || sum == 0.f;
+              const float inv = none ? 0.f : 1.f / sum;
+#pragma unroll
+              for (int x = 0; x < 4; ++x) o4[x] = none ? 0.f : o4[x] * inv;
+              const size_t orow = ((size_t)at.b * a.Hq + h * a.G + r / a.T) * a.T + i;
+              store4(a.o, a.o_dtype, orow * D + part * 32 + col, o4);
+              if (a.lse && part == 0 && col == 0) a.lse[orow] = none ? -INFINITY : row_lse(M, sum);
+            } else {
+              const size_t prow = (size_t)slot * (16 * MT) + mt * 16 + rr;
+              store4(a.part, 2, prow * D + part * 32 + col, o4);
+              if (part == 0 && col == 0) a.part_ml[prow] = make_float2(M, sum);
+            }
+          }
+          __syncthreads();
+        }
+      }
+    }
+    if (t + 1 < nt) at.next(a, pairs, kRowsTile);
+  }
+}
+
+// ------------------------------------------------------------ adding pieces
+// One warp per row.  Rows of a pair that one block covered are done; the others
+// (and the pairs without any tile) are written here.
+template <int D>
+__global__ void __launch_bounds__(128) k_tree_join(const __grid_constant__ TreeArgs a, int tile,
+                                                   int rows_tile, int grid, int least) {
+  __shared__ long long scratch[4];
+  const int pairs = a.c.Hkv * a.RT;
+  const int b = blockIdx.z, h = blockIdx.y;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const SeqLen s = seq_len(a.lens, a.n, b, a.T, a.MP, a.c.page_shift);
+  const int tiles = pair_tiles(s, tile);
+  // tiles before this sequence, and in all
+  long long before = 0, total = 0;
+  for (int x = tid; x < a.B; x += 128) {
+    const long long v =
+        (long long)pair_tiles(seq_len(a.lens, a.n, x, a.T, a.MP, a.c.page_shift), tile) * pairs;
+    total += v;
+    if (x < b) before += v;
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+    total += __shfl_xor_sync(0xffffffffu, total, o);
+  }
+  if (lane == 0) scratch[warp] = before;
+  __syncthreads();
+  before = scratch[0] + scratch[1] + scratch[2] + scratch[3];
+  __syncthreads();
+  if (lane == 0) scratch[warp] = total;
+  __syncthreads();
+  total = scratch[0] + scratch[1] + scratch[2] + scratch[3];
+  const long long most = (total + least - 1) / least;
+  const int gr = (int)(most < grid ? (most < 1 ? 1 : most) : grid);
+  const int R = a.G * a.T;
+  const int r = blockIdx.x * 4 + warp;
+  if (r >= R) return;
+  const int i = r % a.T;
+  const size_t orow = ((size_t)b * a.Hq + h * a.G + r / a.T) * a.T + i;
+  constexpr int PER = D / 32;
+  float o[PER] = {};
+  float M = -INFINITY, sum = 0.f;
+  if (tiles > 0) {
+    const long long P0 = before + (long long)(h * a.RT + r / rows_tile) * tiles, P1 = P0 + tiles;
+    const int c0 = (int)(((P0 + 1) * gr - 1) / total), c1 = (int)((P1 * gr - 1) / total);
+    if (c0 == c1) return;
+    for (int x = c0; x <= c1; ++x) {
+      const size_t prow = (size_t)(2 * x + (x == c0 ? 1 : 0)) * rows_tile + r % rows_tile;
+      const float2 ml = a.part_ml[prow];
+      const float mn = fmaxf(M, ml.x), mb = mn == -INFINITY ? 0.f : mn;
+      const float f0 = ex2(M - mb), f1 = ex2(ml.x - mb);
+      const float* src = a.part + prow * D + lane * PER;
+#pragma unroll
+      for (int y = 0; y < PER; ++y) o[y] = o[y] * f0 + src[y] * f1;
+      sum = sum * f0 + ml.y * f1;
+      M = mn;
+    }
+  }
+  const bool none = i >= s.n || sum == 0.f;
+  const float inv = none ? 0.f : 1.f / sum;
+#pragma unroll
+  for (int y = 0; y < PER; ++y) {
+    const float v = none ? 0.f : o[y] * inv;
+    const size_t idx = orow * D + lane * PER + y;
+    if (a.o_dtype == 0) static_cast<__half*>(a.o)[idx] = __float2half_rn(v);
+    else if (a.o_dtype == 1) static_cast<__nv_bfloat16*>(a.o)[idx] = __float2bfloat16_rn(v);
+    else static_cast<float*>(a.o)[idx] = v;
+  }
+  if (a.lse && lane == 0) a.lse[orow] = none ? -INFINITY : row_lse(M, sum);
+}
+
+// ------------------------------------------------------------ weights
+// acc[b][h][s] += sum over the rows that attend slot s of exp(x - lse).  A warp
+// holds 16 keys as the A operand, the rows pass as B in groups of 32, and a
+// thread adds up its keys' weights over all rows before the four threads that
+// share a key meet once: a slot is owned by one warp, so the sum has a fixed order.
+// e4m3: the codes become the type of Q, exactly; the key scale multiplies the score.
+constexpr int kWKeys = 64;
+
+template <int D, bool E4M3, bool BF>
+__global__ void __launch_bounds__(128) k_cache_weights(const __grid_constant__ TreeArgs a,
+                                                       const float* __restrict__ lse,
+                                                       float* __restrict__ tally, long long ab,
+                                                       long long ah, int S) {
+  constexpr int RS = D + 8;                   // 16-bit elements of a padded row
+  __shared__ __align__(16) uint16_t kt[kWKeys * RS];
+  __shared__ __align__(16) uint16_t qt[32 * RS];
+  __shared__ float z[32];
+  const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, c = lane & 3;
+  const SeqLen s = seq_len(a.lens, a.n, b, a.T, a.MP, a.c.page_shift);
+  const int L = s.n == 0 ? 0 : s.len + s.n;
+  const int key0 = blockIdx.x * kWKeys;
+  if (key0 >= L) return;
+  if (L > S && key0 == 0 && h == 0 && tid == 0) atomicOr(&g_device_error, DEVERR_BOUNDS);
+  for (int i = tid; i < kWKeys * (D / 8); i += 128) {
+    const int r = i / (D / 8), ch = i % (D / 8);
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (key0 + r < L) {
+      const int page = __ldg(a.table + (size_t)b * a.MP + ((key0 + r) >> a.c.page_shift));
+      if (static_cast<unsigned>(page) < static_cast<unsigned>(a.c.pages)) {
+        const long long row = (((long long)page * a.c.Hkv + h) << a.c.page_shift) +
+                              ((key0 + r) & ((1 << a.c.page_shift) - 1));
+        if (!E4M3) {
+          v = __ldg(reinterpret_cast<const uint4*>(a.c.k + row * D * 2) + ch);
+        } else {
+          const uint2 w = __ldg(reinterpret_cast<const uint2*>(a.c.k + row * D) + ch);
+          uint32_t o4[4] = {e4m3x2_f16x2(w.x & 0xffffu), e4m3x2_f16x2(w.x >> 16),
+                            e4m3x2_f16x2(w.y & 0xffffu), e4m3x2_f16x2(w.y >> 16)};
+          if (BF) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&o4[u]));
+              o4[u] = pack2<true>(f.x, f.y);
+            }
+          }
+          v = make_uint4(o4[0], o4[1], o4[2], o4[3]);
+        }
+      }
+    }
+    *reinterpret_cast<uint4*>(kt + r * RS + 8 * ch) = v;
+  }
+  __syncthreads();
+  uint32_t kf[D / 16][4];
+#pragma unroll
+  for (int ks = 0; ks < D / 16; ++ks)
+    ldsm4(smem_u32(kt + (warp * 16 + (lane & 15)) * RS + ks * 16 + 8 * (lane >> 4)), kf[ks]);
+  float ksc[2] = {1.f, 1.f};
+  bool there[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int k = key0 + warp * 16 + g + 8 * e;
+    there[e] = k < L;
+    if (k < L) {
+      const int page = __ldg(a.table + (size_t)b * a.MP + (k >> a.c.page_shift));
+      if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.c.pages)) {
+        atomicOr(&g_device_error, DEVERR_BOUNDS);
+        there[e] = false;
+      } else if (E4M3) {
+        ksc[e] = __ldg(a.c.ks + ((((long long)page * a.c.Hkv + h) << a.c.page_shift) +
+                                 (k & ((1 << a.c.page_shift) - 1))));
+      }
+    }
+  }
+  const float kL2E = 1.4426950408889634f;
+  const float scl[2] = {a.sm_scale * kL2E * ksc[0], a.sm_scale * kL2E * ksc[1]};
+  const uint8_t* mask = a.mask ? a.mask + b * a.mask_sb : nullptr;
+  const bool edge = key0 + kWKeys > s.len;
+  const int R = a.G * a.T;
+  float sum[2] = {0.f, 0.f};
+  for (int r0 = 0; r0 < R; r0 += 32) {
+    __syncthreads();
+    for (int i = tid; i < 32 * (D / 8); i += 128) {
+      const int r = i / (D / 8), ch = i % (D / 8);
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (r0 + r < R)
+        v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + b * a.sb +
+                                                 (long long)(h * a.G + (r0 + r) / a.T) * a.sh +
+                                                 (long long)((r0 + r) % a.T) * a.st) + ch);
+      *reinterpret_cast<uint4*>(qt + r * RS + 8 * ch) = v;
+    }
+    if (tid < 32) {
+      // a row that does not count: +inf, so that its weights are 0
+      float v = INFINITY;
+      const int r = r0 + tid;
+      if (r < R && r % a.T < s.n) {
+        v = __ldg(lse + ((size_t)b * a.Hq + h * a.G + r / a.T) * a.T + r % a.T) * kL2E;
+        if (v == -INFINITY) v = INFINITY;
+      }
+      z[tid] = v;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j2 = 0; j2 < 2; ++j2) {
+      float d[2][4] = {};
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        uint32_t bq[4];
+        ldsm4(smem_u32(qt + (j2 * 16 + (lane >> 4) * 8 + (lane & 7)) * RS + ks * 16 +
+                       8 * ((lane >> 3) & 1)), bq);
+        mma16816<BF>(d[0], kf[ks], bq[0], bq[1]);
+        mma16816<BF>(d[1], kf[ks], bq[2], bq[3]);
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int e = u >> 1, rr = j2 * 16 + j * 8 + 2 * c + (u & 1);
+          bool ok = there[e] && z[rr] < INFINITY;
+          if (edge && ok) {
+            const int jj = key0 + warp * 16 + g + 8 * e - s.len;
+            ok = jj < 0 || tree_allows(mask, a.T, (r0 + rr) % a.T, jj);
+          }
+          if (ok) sum[e] += ex2(d[j][u] * scl[e] - z[rr]);
+        }
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 1);
+    sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 2);
+    const int k = key0 + warp * 16 + g + 8 * e;
+    if (c == 0 && there[e] && k < S) tally[b * ab + h * ah + k] += sum[e];
+  }
+}
+
+// ------------------------------------------------------------ launches
+static int sm_count(int dev) {
+  static int n[64] = {};
+  if (dev < 0 || dev >= 64) return 148;
+  if (n[dev] == 0) {
+    int v = 0;
+    if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0)
+      v = 148;
+    n[dev] = v;
+  }
+  return n[dev];
+}
+
+constexpr int kRowsLeast = 2;   // tiles that a block takes at least
+
+template <int D, bool E4M3, bool QBF, int MT>
+static cudaError_t launch_rows(TreeArgs a, int dev, cudaMemPool_t pool, cudaStream_t st) {
+  using C = RowsCfg<D, E4M3>;
+  a.RT = (a.G * a.T + 16 * MT - 1) / (16 * MT);
+  const int grid = 2 * sm_count(dev);
+  CUtensorMap tk, tv;
+  const uint64_t rows = (uint64_t)a.c.pages * a.c.Hkv << a.c.page_shift;
+  const int eb = E4M3 ? 1 : 2;
+  const uint64_t dims[2] = {(uint64_t)D, rows};
+  const uint64_t strides[1] = {(uint64_t)D * eb};
+  const uint32_t box[2] = {(uint32_t)(C::kBoxBytes / eb), 16};
+  cudaError_t e = make_tmap(&tk, a.c.k, 2, dims, strides, box, eb, C::kBoxBytes);
+  if (e == cudaSuccess) e = make_tmap(&tv, a.c.v, 2, dims, strides, box, eb, C::kBoxBytes);
+  if (e != cudaSuccess) return e;
+  const size_t prow = (size_t)2 * grid * 16 * MT;
+  uint8_t* ws = nullptr;
+  e = cudaMallocFromPoolAsync(reinterpret_cast<void**>(&ws), up256(prow * D * 4) + prow * 8, pool, st);
+  if (e != cudaSuccess) return e;
+  a.part = reinterpret_cast<float*>(ws);
+  a.part_ml = reinterpret_cast<float2*>(ws + up256(prow * D * 4));
+  auto kern = k_tree_rows<D, E4M3, QBF, MT>;
+  const int smem = sizeof(RowsSmem<D, E4M3>) + 1024;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) {
+    kern<<<grid, 32 * kRowsWarps, smem, st>>>(tk, tv, a);
+    e = cudaGetLastError();
+  }
+  if (e == cudaSuccess) {
+    k_tree_join<D><<<dim3((a.G * a.T + 3) / 4, a.c.Hkv, a.B), 128, 0, st>>>(a, kRowsTile, 16 * MT, grid,
+                                                                          kRowsLeast);
+    e = cudaGetLastError();
+  }
+  const cudaError_t e2 = cudaFreeAsync(ws, st);
+  return e != cudaSuccess ? e : e2;
+}
+
+template <int D, bool E4M3, bool QBF>
+static cudaError_t rows_pick(const TreeArgs& a, int dev, cudaMemPool_t pool, cudaStream_t st) {
+  return a.G * a.T <= 16 ? launch_rows<D, E4M3, QBF, 1>(a, dev, pool, st)
+                         : launch_rows<D, E4M3, QBF, 2>(a, dev, pool, st);
+}
+
+template <int D, bool E4M3, bool QBF>
+static cudaError_t launch_weights(const TreeArgs& a, const float* lse, float* acc, long long ab,
+                                  long long ah, int S, cudaStream_t st) {
+  const int cap = a.MP << a.c.page_shift;
+  k_cache_weights<D, E4M3, QBF><<<dim3((cap + kWKeys - 1) / kWKeys, a.c.Hkv, a.B), 128, 0, st>>>(
+      a, lse, acc, ab, ah, S);
+  return cudaGetLastError();
+}
+
+// What sage2_attn_tree and sage2_cache_weights check alike.
+static sage2_status tree_args(const void* q, int dtype, const int64_t* q_strides,
+                              const sage2_cache* cache, const int* table, int max_pages,
+                              const int* lens, const int* n, const uint8_t* mask,
+                              int64_t mask_stride, int B, int Hq, int T, float sm_scale, TreeArgs* a) {
+  sage2_status s = check_cache(cache, &a->c);
+  if (s != SAGE2_OK) return s;
+  s = check_table(a->c, B, max_pages);
+  if (s != SAGE2_OK) return s;
+  if (dtype != SAGE2_F16 && dtype != SAGE2_BF16) return SAGE2_ERR_INVALID_ARG;
+  if (a->c.kv_dtype != SAGE2_E4M3 && dtype != a->c.kv_dtype) return SAGE2_ERR_INVALID_ARG;
+  if (Hq <= 0 || Hq % a->c.Hkv != 0 || T <= 0) return SAGE2_ERR_INVALID_ARG;
+  if (T > 1024 || (int64_t)Hq * T > INT32_MAX) return SAGE2_ERR_UNSUPPORTED;
+  if (!(sm_scale > 0.f) || sm_scale > 3.0e38f) return SAGE2_ERR_INVALID_ARG;
+  if (mask_stride < 0) return SAGE2_ERR_INVALID_ARG;
+  s = check_ptrs(q);
+  if (s != SAGE2_OK) return s;
+  s = check_words(table, lens);
+  if (s != SAGE2_OK) return s;
+  if (n && !aligned4(n)) return SAGE2_ERR_MISALIGNED;
+  long long st[3];
+  s = take_strides(q_strides, Hq, T, a->c.d, st);
+  if (s != SAGE2_OK) return s;
+  a->sb = st[0];
+  a->sh = st[1];
+  a->st = st[2];
+  a->table = table;
+  a->lens = lens;
+  a->n = n;
+  a->mask = mask;
+  a->mask_sb = mask_stride;
+  a->q = q;
+  a->B = B;
+  a->Hq = Hq;
+  a->G = Hq / a->c.Hkv;
+  a->T = T;
+  a->MP = max_pages;
+  a->sm_scale = sm_scale;
+  a->RT = 1;
+  return SAGE2_OK;
+}
+
+}  // namespace sage2
+
+extern "C" {
+
+sage2_status sage2_attn_tree(const void* q, int dtype, const int64_t* q_strides,
+                             const sage2_cache* cache, const int* table, int max_pages,
+                             const int* lens, const int* n, const uint8_t* mask,
+                             int64_t mask_stride, void* o, int o_dtype, float* lse, int B, int Hq,
+                             int T, float sm_scale, sage2_stream_t stream) {
+  using namespace sage2;
+  TreeArgs a{};
+  sage2_status s = tree_args(q, dtype, q_strides, cache, table, max_pages, lens, n, mask, mask_stride,
+                             B, Hq, T, sm_scale, &a);
+  if (s != SAGE2_OK) return s;
+  if (o_dtype < SAGE2_F16 || o_dtype > SAGE2_F32) return SAGE2_ERR_INVALID_ARG;
+  s = check_ptrs(o);
+  if (s != SAGE2_OK) return s;
+  if (lse && !aligned4(lse)) return SAGE2_ERR_MISALIGNED;
+  a.o = o;
+  a.o_dtype = o_dtype;
+  a.lse = lse;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return SAGE2_ERR_CUDA;
+  cudaMemPool_t pool = device_pool(dev);
+  if (!pool) return SAGE2_ERR_CUDA;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const bool bf = dtype == SAGE2_BF16, e4 = a.c.kv_dtype == SAGE2_E4M3;
+  cudaError_t e;
+  if (a.c.d == 64)
+    e = e4 ? (bf ? rows_pick<64, true, true>(a, dev, pool, st) : rows_pick<64, true, false>(a, dev, pool, st))
+           : (bf ? rows_pick<64, false, true>(a, dev, pool, st) : rows_pick<64, false, false>(a, dev, pool, st));
+  else
+    e = e4 ? (bf ? rows_pick<128, true, true>(a, dev, pool, st) : rows_pick<128, true, false>(a, dev, pool, st))
+           : (bf ? rows_pick<128, false, true>(a, dev, pool, st) : rows_pick<128, false, false>(a, dev, pool, st));
+  return from_cuda(e);
+}
+
+sage2_status sage2_cache_weights(const void* q, int dtype, const int64_t* q_strides,
+                                 const float* lse, const sage2_cache* cache, const int* table,
+                                 int max_pages, const int* lens, const int* n, const uint8_t* mask,
+                                 int64_t mask_stride, float* acc, const int64_t* acc_strides, int S,
+                                 int B, int Hq, int T, float sm_scale, sage2_stream_t stream) {
+  using namespace sage2;
+  TreeArgs a{};
+  sage2_status s = tree_args(q, dtype, q_strides, cache, table, max_pages, lens, n, mask, mask_stride,
+                             B, Hq, T, sm_scale, &a);
+  if (s != SAGE2_OK) return s;
+  s = check_words(lse, acc);
+  if (s != SAGE2_OK) return s;
+  if (S <= 0 || !acc_strides || acc_strides[0] < 0 || acc_strides[1] < 0) return SAGE2_ERR_INVALID_ARG;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const long long ab = acc_strides[0], ah = acc_strides[1];
+  const bool bf = dtype == SAGE2_BF16, e4 = a.c.kv_dtype == SAGE2_E4M3;
+  cudaError_t e;
+  if (a.c.d == 64)
+    e = e4 ? (bf ? launch_weights<64, true, true>(a, lse, acc, ab, ah, S, st)
+                 : launch_weights<64, true, false>(a, lse, acc, ab, ah, S, st))
+           : (bf ? launch_weights<64, false, true>(a, lse, acc, ab, ah, S, st)
+                 : launch_weights<64, false, false>(a, lse, acc, ab, ah, S, st));
+  else
+    e = e4 ? (bf ? launch_weights<128, true, true>(a, lse, acc, ab, ah, S, st)
+                 : launch_weights<128, true, false>(a, lse, acc, ab, ah, S, st))
+           : (bf ? launch_weights<128, false, true>(a, lse, acc, ab, ah, S, st)
+                 : launch_weights<128, false, false>(a, lse, acc, ab, ah, S, st));
+  return from_cuda(e);
+}
+
+}  // extern "C"

@@ -1,0 +1,336 @@
+"""The operators over a paged cache on the GPU against their 64-bit definitions
+(tests/cache_ref.py).
+
+Tolerances, derived from the arithmetic:
+ - Scores: products of 16-bit (or e4m3) values are exact in fp32; a sum of d of them
+   in fp32, whatever the order, is off by at most d 2^-23 sum|q k| (a rounding or
+   truncation a term); SCORE takes that bound with sum|q k| <= |q||k| from the
+   data, in units of the logit, plus the roundings of the scaling (4 2^-24 |x|) and of
+   ex2 (2^-22 relative).
+ - o: with logits off by at most e each weight is off by a factor exp(+-2e); P
+   is rounded to 16 bits (half a step, 2^-8 bf16 or 2^-11 fp16 relative, plus
+   2^-25 absolute in fp16 where P is subnormal; the fp32 scale of an e4m3 V adds
+   4 2^-24), all relative to sum w|V|; then the output rounding of half a step.
+ - lse: off by at most e, plus 2^-22 (|lse| + 1) for the fp32 sum and logarithm.
+ - weights: a factor exp(+-e) on each, and the fp32 sum of R terms (R 2^-24).
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from tests import cache_ref as R
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def qa():
+    from quantized_attention_04_b200 import build
+    build.build()
+    import quantized_attention_04_b200 as m
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    m.lib()
+    assert m.sage2_check_device_error() == 0
+    return m
+
+
+def logit_error(c):
+    """Bound on |logit - exact| over the case."""
+    qn = c.q.double().norm(dim=-1).max().item()
+    kn = max(c.dense("k", b, h, c.lens[b] + c.n[b]).norm(dim=-1).max().item()
+             for b in range(c.B) for h in range(c.Hkv) if c.lens[b] + c.n[b])
+    x = qn * kn * c.sm
+    return x * (c.d * 2.0 ** -23 + 4 * 2.0 ** -24) + 2.0 ** -22
+
+
+def check_tree(c, o, lse, want, odt):
+    wo, wl, mag = want
+    e = logit_error(c)
+    p16 = 2.0 ** -8 if c.dtype == torch.bfloat16 and c.kv != "e4m3" else 2.0 ** -11
+    out = 0.0 if odt == torch.float32 else torch.finfo(odt).eps / 2
+    keys = max(x + y for x, y in zip(c.lens, c.n))
+    vmax = max([c.dense("v", b, h, c.lens[b] + c.n[b]).abs().max().item()
+                for b in range(c.B) for h in range(c.Hkv) if c.lens[b] + c.n[b]] + [0.0])
+    rel = math.expm1(2 * e) + p16 + 4 * 2.0 ** -24 + keys * 2.0 ** -24
+    sub = 0.0 if p16 == 2.0 ** -8 else 2.0 ** -25 * keys * vmax
+    tol = rel * mag + sub
+    tol = tol + out * (wo.abs() + tol) + 1e-30
+    o, lse = o.double().cpu(), lse.double().cpu()
+    assert torch.isfinite(o).all()
+    bad = (o - wo).abs() > tol
+    assert not bad.any(), ("o", bad.nonzero()[:5].tolist(), ((o - wo).abs() / tol).max().item())
+    none = wl == -math.inf
+    assert torch.equal(lse == -math.inf, none)
+    assert (o[none] == 0).all()
+    ltol = e + 2.0 ** -22 * (wl[~none].abs() + 1) + keys * 2.0 ** -24
+    assert ((lse[~none] - wl[~none]).abs() <= ltol).all(), (lse[~none] - wl[~none]).abs().max()
+
+
+# (lens, T, Hkv, G, d, page, dtype, kv, n)
+TREE = [
+    ([1], 1, 1, 1, 128, 16, "bf16", "same", None),
+    ([0], 1, 2, 1, 64, 16, "fp16", "same", None),
+    ([0, 5, 16, 17], 1, 2, 4, 128, 16, "fp16", "same", None),
+    ([63, 64, 65, 0], 1, 1, 8, 128, 32, "bf16", "e4m3", None),
+    ([130, 1, 700], 3, 2, 4, 128, 16, "bf16", "same", [3, 0, 2]),
+    ([33, 257], 5, 1, 3, 64, 64, "fp16", "e4m3", [5, 1]),
+    ([500, 77], 4, 2, 5, 128, 128, "bf16", "same", None),
+    ([200, 31, 90], 7, 2, 4, 64, 16, "bf16", "e4m3", [7, 3, 6]),
+    ([1000], 16, 1, 2, 128, 32, "fp16", "e4m3", None),
+    ([129, 640], 17, 2, 2, 128, 64, "bf16", "same", [17, 9]),
+    ([411], 61, 1, 4, 128, 32, "bf16", "same", None),
+    ([300, 0], 64, 1, 4, 128, 64, "bf16", "e4m3", [64, 33]),
+    ([150], 40, 2, 7, 64, 16, "fp16", "same", None),
+    ([77, 300], 33, 1, 8, 64, 128, "bf16", "e4m3", [33, 33]),
+    ([900, 10], 100, 1, 1, 128, 16, "fp16", "same", [100, 70]),
+    ([2500], 1, 1, 1, 128, 16, "bf16", "e4m3", None),
+]
+ids = lambda c: "-".join(str(x) for x in c[1:8])
+
+
+@pytest.mark.parametrize("case", TREE, ids=map(ids, TREE))
+@pytest.mark.parametrize("masked", [True, False])
+def test_tree(qa, case, masked):
+    lens, T, Hkv, G, d, page, dtype, kv, n = case
+    c = R.Case(7, lens, T, Hkv, G, d, page, dtype, kv, n)
+    x = c.cuda()
+    if not masked:
+        x["mask"] = None
+    want = R.attend(c, True if masked else None)
+    for odt in (c.dtype, torch.float32):
+        o, lse = qa.sage2_attn_tree(out_dtype=odt, **x)
+        assert qa.sage2_check_device_error() == 0
+        check_tree(c, o, lse, want, odt)
+
+
+@pytest.mark.parametrize("case", TREE, ids=map(ids, TREE))
+def test_weights(qa, case):
+    lens, T, Hkv, G, d, page, dtype, kv, n = case
+    c = R.Case(8, lens, T, Hkv, G, d, page, dtype, kv, n)
+    x = c.cuda()
+    _, lse, _ = R.attend(c)
+    lse = lse.float()
+    want = R.weights(c, lse)
+    acc = torch.full((c.B, Hkv, c.MP * page + 3), 0.5, device="cuda")
+    got = qa.sage2_cache_weights(x["q"], lse.cuda(), x["cache"], x["table"], x["lens"], acc,
+                                 mask=x["mask"], n=x["n"])
+    assert got is acc and qa.sage2_check_device_error() == 0
+    got = acc.double().cpu()
+    assert (got[:, :, c.MP * page:] == 0.5).all()
+    got = got[:, :, :c.MP * page]
+    e = logit_error(c) + 2.0 ** -22 * (lse[lse > -math.inf].abs().max().item() + 1 if (lse > -math.inf).any() else 1)
+    tol = want * (math.expm1(e) + (G * T + 4) * 2.0 ** -24) + 2.0 ** -24 * (want + 0.5)
+    assert ((got - 0.5 - want).abs() <= tol).all(), ((got - 0.5 - want).abs() / (tol + 1e-30)).max()
+    # slots that nothing attends keep their value bit for bit
+    assert (got[want == 0] == 0.5).all()
+
+
+def pools_after_append(c, k, v):
+    """The pools after writing k, v [B, Hkv, T, d] behind lens, by the definition."""
+    out = {n: t.clone() for n, t in c.pool.items()}
+    for b in range(c.B):
+        for t in range(c.n[b]):
+            s = c.lens[b] + t
+            p, r = int(c.table[b, s // c.page]), s % c.page
+            for name, x in (("k", k), ("v", v)):
+                if c.kv == "e4m3":
+                    code, out[name + "_scale"][p, :, r] = R.codes(x[b, :, t])
+                    out[name].view(torch.uint8)[p, :, r] = code.view(torch.uint8)
+                else:
+                    out[name][p, :, r] = x[b, :, t]
+    return out
+
+
+def same_bits(a, b):
+    raw = {1: torch.uint8, 2: torch.int16, 4: torch.int32}[a.element_size()]
+    return torch.equal(a.cpu().contiguous().view(raw), b.cpu().contiguous().view(raw))
+
+
+@pytest.mark.parametrize("case", TREE, ids=map(ids, TREE))
+@pytest.mark.parametrize("strided", [False, True])
+def test_append(qa, case, strided):
+    lens, T, Hkv, G, d, page, dtype, kv, n = case
+    c = R.Case(9, lens, T, Hkv, G, d, page, dtype, kv, n)
+    x = c.cuda()
+    g = torch.Generator().manual_seed(3)
+    k, v = (torch.randn(c.B, Hkv, T, d, generator=g).to(c.dtype) * 3 for _ in range(2))
+    if kv == "e4m3":
+        k[0, 0, 0] = 0                          # a row of zeros
+        v[0, 0, 0, 1:] = 0                      # a row of one value
+        k[-1, -1, -1] *= 2.0 ** -9
+    want = pools_after_append(c, k, v)
+    kd, vd = k.cuda(), v.cuda()
+    if strided:                                 # [B, T, Hkv, 2, d]: what a fused projection returns
+        both = torch.stack([kd, vd], 3).transpose(1, 2).contiguous()
+        kd, vd = both[:, :, :, 0].transpose(1, 2), both[:, :, :, 1].transpose(1, 2)
+    qa.sage2_cache_append(kd, vd, x["cache"], x["table"], x["lens"], n=x["n"])
+    assert qa.sage2_check_device_error() == 0
+    for name, t in want.items():
+        assert same_bits(x["cache"][name], t), name
+
+
+def test_append_rows_that_are_not_finite(qa):
+    """Zero below 2^-100, NaN scale for a row with an infinity or NaN, the other rows untouched."""
+    c = R.Case(1, [4], 6, 1, 1, 128, 16, "bf16", "e4m3")
+    x = c.cuda()
+    k = torch.ones(1, 1, 6, 128, dtype=torch.bfloat16)
+    k[0, 0, 1, 5], k[0, 0, 2, 127], k[0, 0, 3, 0] = math.inf, math.nan, -math.inf
+    k[0, 0, 4] = 2.0 ** -101
+    qa.sage2_cache_append(k.cuda(), k.cuda(), x["cache"], x["table"], x["lens"])
+    p = int(c.table[0, 0])
+    for name in "kv":
+        s = x["cache"][name + "_scale"][p, 0, 4:10].cpu()
+        assert torch.isnan(s[1:4]).all() and s[4] == 0
+        assert s[0] == s[5] == torch.tensor(1.0) / 448
+        codes = x["cache"][name].view(torch.uint8)[p, 0, 4:10].cpu()
+        assert (codes[4] == 0).all() and (codes[0] == 0x7e).all() and (codes[5] == 0x7e).all()
+
+
+def pools_after_move(pool, table, out_table, page, idx, count, base):
+    out = {n: t.clone() for n, t in pool.items()}
+    for b in range(table.shape[0]):
+        for h in range(idx.shape[1]):
+            for i in range(count[b]):
+                s, t = int(idx[b, h, i]), base[b] + i
+                sp, sr, dp, dr = int(table[b, s // page]), s % page, int(out_table[b, t // page]), t % page
+                for name in pool:
+                    raw = lambda t: t.view(torch.uint8) if t.dtype == torch.float8_e4m3fn else t
+                    raw(out[name])[dp, h, dr] = raw(pool[name])[sp, h, sr]
+    return out
+
+
+MOVE = [([300, 40, 1], 2, 128, 16, "bf16", "same"), ([700, 513], 3, 64, 64, "fp16", "e4m3"),
+        ([1500], 1, 64, 32, "fp16", "same"), ([260, 999], 2, 128, 128, "bf16", "e4m3")]
+
+
+@pytest.mark.parametrize("case", MOVE, ids=lambda c: f"{c[2]}-{c[3]}-{c[5]}")
+@pytest.mark.parametrize("in_place", [True, False])
+def test_evict(qa, case, in_place):
+    lens, Hkv, d, page, dtype, kv = case
+    c = R.Case(5, lens, 1, Hkv, 1, d, page, dtype, kv, junk=False)
+    x = c.cuda()
+    g = torch.Generator().manual_seed(4)
+    S = c.MP * page
+    acc = torch.rand(c.B, Hkv, S, generator=g)
+    acc[:, :, ::3] = 0.25                       # many equal ones
+    acc[0, 0, 5:9] = torch.tensor([math.inf, math.nan, 0.0, -0.0])
+    for keep, sinks, recent in ((256, 4, 31), (37, 0, 0), (64, 32, 32), (64, 64, 0), (1, 0, 1), (2000, 1, 1)):
+        keep = min(keep, c.MP * page)
+        sinks, recent = min(sinks, keep), min(recent, keep)
+        x = c.cuda()
+        out_table, pool, ot = None, dict(c.pool), c.table
+        if not in_place:                        # pages behind the ones of the sequences
+            MO = -(-keep // page)
+            pool = {n: torch.cat([(t.view(torch.uint8) if t.dtype == torch.float8_e4m3fn else t),
+                                  torch.zeros(c.B * MO, *t.shape[1:], dtype=t.dtype).view(
+                                      torch.uint8 if t.dtype == torch.float8_e4m3fn else t.dtype)]).view(t.dtype)
+                    for n, t in c.pool.items()}
+            ot = (c.pages + torch.arange(c.B * MO, dtype=torch.int32)).view(c.B, MO)
+            out_table = ot.cuda()
+        cache = {n: t.cuda() for n, t in pool.items()}
+        idx, new, kept = qa.sage2_cache_evict(cache, x["table"], x["lens"], acc.cuda(), keep, sinks,
+                                              recent, out_table=out_table)
+        assert qa.sage2_check_device_error() == 0
+        count = [min(keep, l) for l in lens]
+        assert new.tolist() == count
+        want = torch.full((c.B, Hkv, keep), -1, dtype=torch.int32)
+        wacc = torch.zeros(c.B, Hkv, keep)
+        for b in range(c.B):
+            for h in range(Hkv):
+                got = torch.tensor(R.choose(acc[b, h], lens[b], keep, sinks, recent))
+                want[b, h, :count[b]], wacc[b, h, :count[b]] = got, acc[b, h, got]
+        assert torch.equal(idx.cpu(), want)
+        assert same_bits(kept, wacc)
+        after = pools_after_move(pool, c.table, ot, page, want, count, [0] * c.B)
+        for name, t in after.items():
+            assert same_bits(cache[name], t), (name, keep, sinks, recent)
+
+
+@pytest.mark.parametrize("case", MOVE, ids=lambda c: f"{c[2]}-{c[3]}-{c[5]}")
+def test_compact_path_in_place(qa, case):
+    """An accepted path of a tree moves behind the context, the same for all heads."""
+    lens, Hkv, d, page, dtype, kv = case
+    T = 30
+    c = R.Case(6, lens, T, Hkv, 1, d, page, dtype, kv, junk=False)
+    x = c.cuda()
+    path = torch.tensor([0, 1, 4, 5, 11, 29])
+    count = [(6, 3, 0)[b % 3] for b in range(c.B)]
+    idx = torch.stack([path + l for l in lens]).to(torch.int32)[:, None].expand(c.B, Hkv, 6)
+    want = pools_after_move(c.pool, c.table, c.table, page, idx, count, lens)
+    S = c.MP * page
+    acc = torch.rand(c.B, Hkv, S)
+    wacc = acc.clone()
+    for b in range(c.B):
+        for i in range(count[b]):
+            wacc[b, :, lens[b] + i] = acc[b, :, lens[b] + path[i]]
+    accd = acc.cuda()
+    qa.sage2_cache_compact(x["cache"], x["table"], idx.cuda(), torch.tensor(count, dtype=torch.int32).cuda(),
+                           base=x["lens"], acc=accd)
+    assert qa.sage2_check_device_error() == 0
+    for name, t in want.items():
+        assert same_bits(x["cache"][name], t), name
+    assert same_bits(accd, wacc)
+
+
+def test_compact_repeats_in_place(qa):
+    """In place a row may be taken more than once, in any order that moves towards the front."""
+    c = R.Case(6, [900], 1, 2, 1, 128, 16, "bf16", "e4m3", junk=False)
+    x = c.cuda()
+    g = torch.Generator().manual_seed(1)
+    i = torch.arange(700)
+    idx = torch.stack([i + (torch.rand(700, generator=g) * (900 - i)).long() for _ in range(2)])[None]
+    idx = idx.to(torch.int32)
+    want = pools_after_move(c.pool, c.table, c.table, 16, idx, [700], [0])
+    qa.sage2_cache_compact(x["cache"], x["table"], idx.cuda())
+    assert qa.sage2_check_device_error() == 0
+    for name, t in want.items():
+        assert same_bits(x["cache"][name], t), name
+
+
+def test_serving_run(qa):
+    """The operators together: prompt, tree, accepted path, tally and eviction, then a decode step,
+    in both cache types, against the same steps on the host."""
+    for kv in ("same", "e4m3"):
+        lens, T, Hkv, G, d, page = [70, 41], 6, 2, 2, 64, 16
+        c = R.Case(11, lens, T, Hkv, G, d, page, "bf16", kv, extra=2)
+        x = c.cuda()
+        g = torch.Generator().manual_seed(2)
+        table, cache = x["table"], x["cache"]
+        # prompt (the shorter one padded), then the tree's tokens
+        P = max(lens)
+        k, v = (torch.randn(2, Hkv, P, d, generator=g).to(c.dtype) for _ in range(2))
+        zero = torch.zeros(2, dtype=torch.int32, device="cuda")
+        qa.sage2_cache_append(k.cuda(), v.cuda(), cache, table, zero, n=x["lens"])
+        kt, vt = (torch.randn(2, Hkv, T, d, generator=g).to(c.dtype) for _ in range(2))
+        qa.sage2_cache_append(kt.cuda(), vt.cuda(), cache, table, x["lens"])
+        c.pool = {n: t.cpu() for n, t in cache.items()}
+        ref = {"k": [torch.cat([k[b, :, :lens[b]], kt[b]], 1) for b in range(2)]}
+        if kv == "same":
+            for b in range(2):
+                assert torch.equal(c.dense("k", b, 1, lens[b] + T), ref["k"][b][1].double())
+        o, lse = qa.sage2_attn_tree(x["q"], cache, table, x["lens"], mask=x["mask"])
+        check_tree(c, o, lse, R.attend(c), c.dtype)
+        acc = torch.zeros(2, Hkv, c.MP * page, device="cuda")
+        qa.sage2_cache_weights(x["q"], lse, cache, table, x["lens"], acc, mask=x["mask"])
+        # every attended weight is in the tally: G*T rows a head, each of weight 1
+        # (lse and the weight are each off by the error of a logit, the sums by 2^-24 a term)
+        total = acc.double().sum(-1).cpu()
+        rel = math.expm1(2 * logit_error(c)) + (G * T + max(lens) + T) * 2.0 ** -23
+        assert (total - G * T).abs().max() <= G * T * rel
+        path = torch.tensor([[0, 3, 5], [0, 1, 2]], dtype=torch.int32)
+        took = torch.tensor([3, 2], dtype=torch.int32)
+        idx = (path + torch.tensor(lens, dtype=torch.int32)[:, None])[:, None].expand(2, Hkv, 3)
+        qa.sage2_cache_compact(cache, table, idx.cuda(), took.cuda(), base=x["lens"], acc=acc)
+        now = x["lens"] + took.cuda()
+        idx, new, _ = qa.sage2_cache_evict(cache, table, now, acc, 48, sinks=2, recent=8, acc_out=acc)
+        assert new.tolist() == [48, 43]
+        # one more token
+        k1, v1 = (torch.randn(2, Hkv, 1, d, generator=g).to(c.dtype) for _ in range(2))
+        qa.sage2_cache_append(k1.cuda(), v1.cuda(), cache, table, new)
+        c2 = R.Case(12, [48, 43], 1, Hkv, G, d, page, "bf16", kv, junk=False)
+        c2.pool, c2.table = {n: t.cpu() for n, t in cache.items()}, c.table
+        o, lse = qa.sage2_attn_tree(c2.q.cuda(), cache, table, new)
+        assert qa.sage2_check_device_error() == 0
+        check_tree(c2, o, lse, R.attend(c2), c2.dtype)
