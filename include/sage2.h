@@ -321,12 +321,14 @@ sage2_status sage2_cache_append(const void* k, const void* v, int dtype, const i
  * j <= i).  Query head hq reads key/value head hq / (Hq/Hkv).
  *   q    : [B, Hq, T, d] in dtype (SAGE2_F16 or SAGE2_BF16; a 16-bit cache has the
  *          same), Hq a multiple of Hkv, 1 <= T <= 1024.  T = 1 is a decode step.
+ *   sm_scale : 1e-20 .. 1e20.
  *   mask : DEVICE bytes [T, T] per sequence, mask_stride bytes apart (0: one for all).
  *   o    : [B, Hq, T, d] contiguous in o_dtype (SAGE2_F16, SAGE2_BF16 or SAGE2_F32).
  *   lse  : f32 [B, Hq, T] contiguous or NULL: ln sum_s exp(sm_scale * q . K_s).
  * A token with nothing to attend and the tokens i >= n[b] get o = 0, lse = -inf.
- * Slots that no token attends may hold any bits.  K and V of a slot that some
- * drafted token attends must be finite.  Scores, their maxima and sums and the
+ * Slots from lens[b] + n[b] on may hold any bits, and an infinity or NaN in the
+ * row of a drafted token reaches only the tokens that attend it (their whole o
+ * is NaN).  Scores, their maxima and sums and the
  * accumulators are fp32; P is rounded to the MMA's 16-bit type.  The order of the
  * sums depends on the sizes and lengths alone, so equal calls give equal bits.
  */

@@ -13,6 +13,7 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include "cache_index.h"
 #include "sage2.h"
 #include "sage2_internal.h"
 #include "sm100_ptx.cuh"
@@ -23,17 +24,16 @@ namespace sage2 {
 // error word) if the slot or its page is out of range.
 __device__ __forceinline__ long long cache_row(const CacheView& c, const int* table, int MP, int b,
                                                int h, int slot) {
-  const int p = slot >> c.page_shift;
-  if (slot < 0 || p >= MP) {
+  if (!slot_inside(slot, c.page_shift, MP)) {
     atomicOr(&g_device_error, DEVERR_BOUNDS);
     return -1;
   }
-  const int page = __ldg(table + (size_t)b * MP + p);
-  if (static_cast<unsigned>(page) >= static_cast<unsigned>(c.pages)) {
+  const int page = __ldg(table + (size_t)b * MP + (slot >> c.page_shift));
+  if (!page_inside(page, c.pages)) {
     atomicOr(&g_device_error, DEVERR_BOUNDS);
     return -1;
   }
-  return (((long long)page * c.Hkv + h) << c.page_shift) + (slot & ((1 << c.page_shift) - 1));
+  return row_of(page, c.Hkv, h, c.page_shift, slot);
 }
 
 // ---------------------------------------------------------------------------

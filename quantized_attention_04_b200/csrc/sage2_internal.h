@@ -64,17 +64,6 @@ struct AttnArgs {
   int64_t ldo;             // tokens between consecutive heads of o (N when contiguous)
 };
 
-// A paged key/value cache (sage2_cache, checked): rows of d values, row
-// ((page*Hkv + h) << page_shift) + slot % page of the pools.
-struct CacheView {
-  uint8_t* k;
-  uint8_t* v;
-  float* ks;               // row scales (e4m3), else null
-  float* vs;
-  int pages, Hkv, page_shift, d;
-  int kv_dtype;            // 0 fp16, 1 bf16, 3 e4m3
-};
-
 cudaError_t launch_smooth_quant_qk(const QKArgs& a, cudaStream_t st);
 cudaError_t launch_quant_v(const VArgs& a, cudaStream_t st);
 cudaError_t launch_attn(const AttnArgs& a, cudaStream_t st);

@@ -15,6 +15,7 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include "cache_index.h"
 #include "sage2.h"
 #include "sage2_internal.h"
 #include "sm100_ptx.cuh"
@@ -41,19 +42,15 @@ struct TreeArgs {
 };
 
 // Context length and drafted tokens of sequence b, held to what the table can hold.
-struct SeqLen {
-  int len, n;
-};
 __device__ __forceinline__ SeqLen seq_len(const int* lens, const int* ns, int b, int T, int MP,
                                           int page_shift) {
   SeqLen s;
   s.len = __ldg(lens + b);
   s.n = ns ? __ldg(ns + b) : T;
   const int cap = MP << page_shift;
-  if (static_cast<unsigned>(s.n) > static_cast<unsigned>(T) || s.len < 0 || s.len > cap - s.n) {
+  if (!seq_fits(s.len, s.n, T, cap)) {
     atomicOr(&g_device_error, DEVERR_BOUNDS);
-    s.n = min(max(s.n, 0), min(T, cap));
-    s.len = min(max(s.len, 0), cap - s.n);
+    s = seq_clamped(s.len, s.n, T, cap);
   }
   return s;
 }
@@ -64,11 +61,6 @@ __device__ __forceinline__ bool tree_allows(const uint8_t* mask, int T, int i, i
 }
 
 // ------------------------------------------------------------ the work split
-// Tiles of one pair of sequence b: none if nothing is asked of it.
-__device__ __forceinline__ int pair_tiles(SeqLen s, int tile) {
-  return s.n == 0 ? 0 : (s.len + s.n + tile - 1) / tile;
-}
-
 // The block's run [t0, t1) of the global tile sequence, in shared memory, with
 // the pair it starts in.  `pairs`: pairs of one sequence (Hkv*RT).
 struct Run {
@@ -76,10 +68,6 @@ struct Run {
   int b, pair, tile;       // where t0 is
   int grid;                // blocks that have work
 };
-
-__device__ __forceinline__ long long run_start(long long total, int grid, int c) {
-  return total * c / grid;
-}
 
 // Called by the whole block (blockDim.x threads, whole warps).  Finds the run of
 // block `c` of `grid`, no block taking fewer than `least` tiles while others have none.
@@ -124,8 +112,7 @@ __device__ void find_run(const TreeArgs& a, int tile, int pairs, int grid, int c
     if (pass == 0) {
       total = carry;
       if (tid == 0) {
-        const long long most = (total + least - 1) / least;
-        const int g = (int)(most < grid ? (most < 1 ? 1 : most) : grid);
+        const int g = run_blocks(total, grid, least);
         out->total = total;
         out->grid = g;
         out->t0 = c < g ? run_start(total, g, c) : total;
@@ -205,6 +192,29 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   }
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// The two values of a packed pair.
+template <bool BF>
+__device__ __forceinline__ float2 halves(uint32_t w) {
+  if (BF) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+// Does a 16-byte piece of a cached row hold an infinity or NaN?
+template <bool E4M3, bool BF>
+__device__ __forceinline__ bool not_finite16(uint4 u) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (E4M3) {
+      bad = bad || (((w[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u);
+    } else {
+      constexpr uint32_t e = BF ? 0x7f80u : 0x7c00u;
+      bad = bad || (w[i] & e) == e || ((w[i] >> 16) & e) == e;
+    }
+  }
+  return bad;
 }
 
 // Four consecutive values (index of the first, a multiple of 4) in the output type.
@@ -384,40 +394,22 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 2)
             for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
               for (int u = e; u < 4; u += 2) {
-                const uint32_t w = qf[mt][ks][u];
-                float x, y;
-                if (QBF) {
-                  x = __uint_as_float(w << 16);
-                  y = __uint_as_float(w & 0xffff0000u);
-                } else {
-                  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
-                  x = f.x;
-                  y = f.y;
-                }
-                amax = fmaxf(amax, fmaxf(fabsf(x), fabsf(y)));
+                const float2 f = halves<QBF>(qf[mt][ks][u]);
+                amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
               }
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
             // 2^(13 - exponent): an exact power of two; left alone where the row is 0 or not finite
             const int ex = (int)(__float_as_uint(amax) >> 23);
-            const int sh = (ex == 0 || ex == 255) ? 0 : max(-110, min(110, 13 + 127 - ex));
+            const int sh = (ex == 0 || ex == 255) ? 0 : max(-114, min(60, 13 + 127 - ex));
             const float up = __uint_as_float((uint32_t)(127 + sh) << 23);
             qs[mt][e] *= __uint_as_float((uint32_t)(127 - sh) << 23);
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
               for (int u = e; u < 4; u += 2) {
-                const uint32_t w = qf[mt][ks][u];
-                float x, y;
-                if (QBF) {
-                  x = __uint_as_float(w << 16);
-                  y = __uint_as_float(w & 0xffff0000u);
-                } else {
-                  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
-                  x = f.x;
-                  y = f.y;
-                }
-                qf[mt][ks][u] = pack2<false>(x * up, y * up);
+                const float2 f = halves<QBF>(qf[mt][ks][u]);
+                qf[mt][ks][u] = pack2<false>(f.x * up, f.y * up);
               }
           }
         }
@@ -440,17 +432,32 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 2)
       const uint8_t* kt = sm.kv[warp][st];
       const uint8_t* vt = kt + C::kTileBytes;
       const int live = sm.bad[warp][st] ? 0 : min(16, L - key0);   // keys of this tile that exist
-      if (live < 16) {
-        // rows behind the last key may hold anything: P is 0 there, and V must not be NaN
+      // Edge tiles: rows behind the last key may hold anything, and V there must not be
+      // NaN under P = 0; nor in a drafted token's row, which some rows do not attend: such
+      // a row becomes zeros, and the rows that do attend it get NaN from their scores.
+      const bool edge = key0 + 16 > at.s.len || live < 16;
+      unsigned badrows = 0;
+      if (edge) {
+        constexpr int PPR = C::kRowBytes / 16;
         uint8_t* vz = sm.kv[warp][st] + C::kTileBytes;
-        for (int i = lane; i < (16 - live) * (C::kRowBytes / 16); i += 32)
-          *reinterpret_cast<uint4*>(vz + rows_off<D, E4M3>(live + i / (C::kRowBytes / 16),
-                                                          i % (C::kRowBytes / 16))) =
-              make_uint4(0u, 0u, 0u, 0u);
-        if (E4M3 && lane >= live && lane < 16) {
-          sm.sc[warp][st][lane] = 0.f;
-          sm.sc[warp][st][16 + lane] = 0.f;
+        const int first = max(0, at.s.len - key0);
+        for (int i = lane; i < 16 * PPR; i += 32) {
+          const int r = i / PPR;
+          if (r >= first && r < live && not_finite16<E4M3, QBF>(*reinterpret_cast<const uint4*>(
+                                            vz + rows_off<D, E4M3>(r, i % PPR))))
+            badrows |= 1u << r;
         }
+        if (E4M3 && lane < 16) {
+          if (lane >= live) sm.sc[warp][st][lane] = 0.f;
+          const float w = sm.sc[warp][st][16 + lane];
+          if (lane >= first && lane < live && !(fabsf(w) < INFINITY)) badrows |= 1u << lane;
+        }
+        badrows = __reduce_or_sync(0xffffffffu, badrows);
+        for (int i = lane; i < 16 * PPR; i += 32)
+          if (i / PPR >= live || (badrows >> (i / PPR)) & 1u)
+            *reinterpret_cast<uint4*>(vz + rows_off<D, E4M3>(i / PPR, i % PPR)) =
+                make_uint4(0u, 0u, 0u, 0u);
+        if (E4M3 && lane < 16 && (lane >= live || (badrows >> lane) & 1u)) sm.sc[warp][st][16 + lane] = 0.f;
         __syncwarp();
       }
       // ---- S = Q K^T
@@ -515,7 +522,6 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 2)
 #pragma unroll
           for (int e = 0; e < 2; ++e) vscl[j][e] *= iv;
       }
-      const bool edge = key0 + 16 > at.s.len || live < 16;
       uint32_t pf[MT][4];
       bool grew = vup;
       float al[MT][2];
@@ -540,6 +546,7 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 2)
                 const bool ok = k < live && r < R &&
                                 (jj < 0 || tree_allows(a.mask ? a.mask + at.b * a.mask_sb : nullptr, a.T, i, jj));
                 if (!ok) x[j][y] = -INFINITY;
+                else if ((badrows >> k) & 1u) x[j][y] = __int_as_float(0x7fffffff);
               }
           }
           float mx = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[1][0], x[1][1]));
@@ -620,7 +627,7 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 2)
           }
       }
       __syncwarp();
-      if (live < 16) fence_proxy_async_smem();   // the zeros above, before the next TMA write
+      if (edge) fence_proxy_async_smem();        // the zeros above, before the next TMA write
       __syncwarp();
       ++used;
       issue();
@@ -740,8 +747,7 @@ __global__ void __launch_bounds__(128) k_tree_join(const __grid_constant__ TreeA
   if (lane == 0) scratch[warp] = total;
   __syncthreads();
   total = scratch[0] + scratch[1] + scratch[2] + scratch[3];
-  const long long most = (total + least - 1) / least;
-  const int gr = (int)(most < grid ? (most < 1 ? 1 : most) : grid);
+  const int gr = run_blocks(total, grid, least);
   const int R = a.G * a.T;
   const int r = blockIdx.x * 4 + warp;
   if (r >= R) return;
@@ -752,7 +758,7 @@ __global__ void __launch_bounds__(128) k_tree_join(const __grid_constant__ TreeA
   float M = -INFINITY, sum = 0.f;
   if (tiles > 0) {
     const long long P0 = before + (long long)(h * a.RT + r / rows_tile) * tiles, P1 = P0 + tiles;
-    const int c0 = (int)(((P0 + 1) * gr - 1) / total), c1 = (int)((P1 * gr - 1) / total);
+    const int c0 = run_of(P0, total, gr), c1 = run_of(P1 - 1, total, gr);
     if (c0 == c1) return;
     for (int x = c0; x <= c1; ++x) {
       const size_t prow = (size_t)(2 * x + (x == c0 ? 1 : 0)) * rows_tile + r % rows_tile;
@@ -965,10 +971,17 @@ static cudaError_t launch_rows(TreeArgs a, int dev, cudaMemPool_t pool, cudaStre
   return e != cudaSuccess ? e : e2;
 }
 
+}  // namespace sage2
+#include "tree_tiles.cu"
+namespace sage2 {
+
 template <int D, bool E4M3, bool QBF>
-static cudaError_t rows_pick(const TreeArgs& a, int dev, cudaMemPool_t pool, cudaStream_t st) {
-  return a.G * a.T <= 16 ? launch_rows<D, E4M3, QBF, 1>(a, dev, pool, st)
-                         : launch_rows<D, E4M3, QBF, 2>(a, dev, pool, st);
+static cudaError_t tree_pick(const TreeArgs& a, int dev, cudaMemPool_t pool, cudaStream_t st) {
+  const int R = a.G * a.T;
+  if (R <= 16) return launch_rows<D, E4M3, QBF, 1>(a, dev, pool, st);
+  if (R <= 32) return launch_rows<D, E4M3, QBF, 2>(a, dev, pool, st);
+  if (R <= kTT) return launch_tiles<D, E4M3, QBF, false>(a, dev, pool, st);
+  return launch_tiles<D, E4M3, QBF, true>(a, dev, pool, st);
 }
 
 template <int D, bool E4M3, bool QBF>
@@ -993,7 +1006,7 @@ static sage2_status tree_args(const void* q, int dtype, const int64_t* q_strides
   if (a->c.kv_dtype != SAGE2_E4M3 && dtype != a->c.kv_dtype) return SAGE2_ERR_INVALID_ARG;
   if (Hq <= 0 || Hq % a->c.Hkv != 0 || T <= 0) return SAGE2_ERR_INVALID_ARG;
   if (T > 1024 || (int64_t)Hq * T > INT32_MAX) return SAGE2_ERR_UNSUPPORTED;
-  if (!(sm_scale > 0.f) || sm_scale > 3.0e38f) return SAGE2_ERR_INVALID_ARG;
+  if (!(sm_scale >= 1e-20f) || sm_scale > 1e20f) return SAGE2_ERR_INVALID_ARG;
   if (mask_stride < 0) return SAGE2_ERR_INVALID_ARG;
   s = check_ptrs(q);
   if (s != SAGE2_OK) return s;
@@ -1051,11 +1064,11 @@ sage2_status sage2_attn_tree(const void* q, int dtype, const int64_t* q_strides,
   const bool bf = dtype == SAGE2_BF16, e4 = a.c.kv_dtype == SAGE2_E4M3;
   cudaError_t e;
   if (a.c.d == 64)
-    e = e4 ? (bf ? rows_pick<64, true, true>(a, dev, pool, st) : rows_pick<64, true, false>(a, dev, pool, st))
-           : (bf ? rows_pick<64, false, true>(a, dev, pool, st) : rows_pick<64, false, false>(a, dev, pool, st));
+    e = e4 ? (bf ? tree_pick<64, true, true>(a, dev, pool, st) : tree_pick<64, true, false>(a, dev, pool, st))
+           : (bf ? tree_pick<64, false, true>(a, dev, pool, st) : tree_pick<64, false, false>(a, dev, pool, st));
   else
-    e = e4 ? (bf ? rows_pick<128, true, true>(a, dev, pool, st) : rows_pick<128, true, false>(a, dev, pool, st))
-           : (bf ? rows_pick<128, false, true>(a, dev, pool, st) : rows_pick<128, false, false>(a, dev, pool, st));
+    e = e4 ? (bf ? tree_pick<128, true, true>(a, dev, pool, st) : tree_pick<128, true, false>(a, dev, pool, st))
+           : (bf ? tree_pick<128, false, true>(a, dev, pool, st) : tree_pick<128, false, false>(a, dev, pool, st));
   return from_cuda(e);
 }
 

@@ -86,6 +86,11 @@ TREE = [
     ([77, 300], 33, 1, 8, 64, 128, "bf16", "e4m3", [33, 33]),
     ([900, 10], 100, 1, 1, 128, 16, "fp16", "same", [100, 70]),
     ([2500], 1, 1, 1, 128, 16, "bf16", "e4m3", None),
+    ([1, 0, 2, 127, 128, 129, 255, 60], 20, 2, 2, 128, 16, "bf16", "same", [20, 0, 1, 7, 20, 3, 2, 11]),
+    ([3, 0, 90, 127, 128, 130, 255, 64], 30, 3, 5, 64, 32, "fp16", "e4m3", [30, 20, 0, 1, 30, 5, 12, 30]),
+    ([1, 70, 0, 300], 33, 5, 1, 128, 16, "fp16", "e4m3", [33, 1, 0, 20]),
+    ([40, 700], 200, 1, 2, 64, 64, "bf16", "same", [200, 77]),
+    ([0], 1024, 1, 1, 64, 128, "fp16", "same", None),
 ]
 ids = lambda c: "-".join(str(x) for x in c[1:8])
 
@@ -103,6 +108,33 @@ def test_tree(qa, case, masked):
         o, lse = qa.sage2_attn_tree(out_dtype=odt, **x)
         assert qa.sage2_check_device_error() == 0
         check_tree(c, o, lse, want, odt)
+
+
+@pytest.mark.parametrize("kv", ["same", "e4m3"])
+@pytest.mark.parametrize("T, G, d", [(5, 3, 128), (7, 4, 64), (40, 2, 128), (40, 4, 64), (33, 6, 128)])
+def test_not_finite_in_masked_places(qa, T, G, d, kv):
+    """An infinity or NaN in a drafted token's K or V reaches the tokens that attend it, no others."""
+    c = R.Case(13, [150, 3], T, 1, G, d, 32, "bf16", kv)
+    clean = R.attend(c)
+    x = c.cuda()
+    hit = torch.zeros(2, T, dtype=torch.bool)
+    for b, j, name in ((0, 2, "v"), (0, 4, "k"), (1, 1, "v"), (1, 3, "k"), (1, 4, "v")):
+        s = c.lens[b] + j
+        p, r = int(c.table[b, s // 32]), s % 32
+        if kv == "e4m3" and j != 2:
+            x["cache"][name + "_scale"][p, 0, r] = math.nan
+        elif kv == "e4m3":
+            x["cache"][name].view(torch.uint8)[p, 0, r, 5] = 0xff
+        else:
+            x["cache"][name][p, 0, r, 3] = math.inf if name == "v" and b else math.nan
+        hit[b] |= c.mask[b, :, j]
+    o, lse = qa.sage2_attn_tree(out_dtype=torch.float32, **x)
+    assert qa.sage2_check_device_error() == 0
+    assert 0 < hit.sum() < hit.numel()
+    at = hit[:, None].expand(2, G, T)
+    assert torch.isnan(o.cpu()[at]).all()
+    o[at.cuda()], lse[at.cuda()] = clean[0][at].float().cuda(), clean[1][at].float().cuda()
+    check_tree(c, o, lse, clean, torch.float32)
 
 
 @pytest.mark.parametrize("case", TREE, ids=map(ids, TREE))
