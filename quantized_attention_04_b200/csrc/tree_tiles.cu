@@ -13,13 +13,12 @@
 // TMEM for the whole run of a pair.
 //
 // The softmax passes over S once: exponentials are taken against the reference
-// left by the earlier tiles, and only if some score of the warp's rows lies more
-// than 2^8 above it (P could then grow beyond fp16 in a few such steps) the tile
-// is read again for its maximum and O and the row sums are rescaled.  P up to 2^8
-// keeps its relative precision.
+// left by the earlier keys, and only if some score of the warp's rows lies far above
+// it (kGrow) the reference moves, and O, the row sums and the tile's P so far are
+// rescaled.  A P above 1 keeps its relative precision.
 //
-// 16-bit caches: K and V arrive by TMA, a box a page.  e4m3 caches: four warps load
-// the codes (16 bytes a lane, two tiles ahead, in registers), widen them to fp16
+// 16-bit caches: K and V arrive by TMA, a box a page.  e4m3 caches: eight warps load
+// the codes (16 bytes a lane, in registers, two groups in turn), widen them to fp16
 // (exact) and store them in the same layout.  Q enters as fp16 scaled by a power of
 // two a row; the key scales multiply the scores and the value scales multiply P,
 // whose reference includes the tile's largest value scale.
@@ -35,9 +34,12 @@
 namespace sage2 {
 
 constexpr int kTT = 128;                  // keys of a tile, rows of a slot
-constexpr int kTThreads = 13 * 32;        // 8 softmax warps, 4 loader warps, 1 MMA warp
+// Warps: 16 softmax, 4 loaders (e4m3: two groups of 4, which take turns), the MMA warp and 3 idle ones.
+template <bool E4M3>
+constexpr int kTLoad = E4M3 ? 8 : 4;
+template <bool E4M3>
+constexpr int kTThreads = (16 + kTLoad<E4M3> + 4) * 32;
 constexpr int kTScales = 4;               // tiles of scales that a slot keeps
-constexpr float kTGrow = 8.f;             // log2 of how far P may exceed 1
 
 template <int D, bool E4M3>
 struct TilesCfg {
@@ -51,20 +53,21 @@ struct __align__(1024) TilesSmem {
   using C = TilesCfg<D, E4M3>;
   uint8_t q[2][C::kTileBytes];
   uint8_t kv[C::kBufs][C::kTileBytes];
-  float ks[E4M3 ? 2 : 1][kTScales][E4M3 ? kTT : 4];     // key scales of a slot's last tiles
-  float vs[E4M3 ? 2 : 1][kTScales][E4M3 ? kTT : 4];
+  // scales of a slot's last tiles; keys 2i, 2i+1: key scales at 4i, 4i+1, value scales at 4i+2, 4i+3
+  float scl[E4M3 ? 2 : 1][kTScales][E4M3 ? 2 * kTT : 4];
   uint64_t full[C::kBufs];   // the four loader warps (and the TMA's bytes)
   uint64_t empty[C::kBufs];  // commit of the last MMA that reads the buffer
-  uint64_t q_full[2];        // the slot's four softmax warps
+  uint64_t q_full[2];        // the slot's eight softmax warps
   uint64_t s_full[2];        // the MMA thread (it has seen the tile's scales) and the commit of S
-  uint64_t p_full[2];        // the slot's four softmax warps: S read, P written
+  uint64_t p_full[2];        // the slot's eight softmax warps: S read, P written
   uint64_t o_done[2];        // commit of O += P V
   uint64_t tail[C::kBufs];   // bytes of a V tile that is checked before use
   uint64_t drain;
-  long long scratch[16];
+  long long scratch[28];
   Run run[2];
+  Cursor mma_at[2];          // the MMA thread's: the piece that each slot is in
   uint32_t tmem;
-  int bad_v;                 // a drafted token's V row was not finite
+  int bad_v;                 // a drafted token's V row or scale was not finite
   int abort_flag;
 };
 
@@ -174,74 +177,57 @@ __device__ __forceinline__ uint32_t allowed32(const TreeArgs& a, const uint8_t* 
   return bits;
 }
 
-// ex2(x*qs - ref) for 32 scores of a row, packed to 16 bits; adds to sum (the
-// unrounded values) and to mx (the largest x).  EDGE: x of a clear bit is -inf.
-template <bool E4M3, bool BF, bool EDGE>
-__device__ __forceinline__ void soft32(const uint32_t (&s)[32], const float* ks, const float* vs,
-                                       uint32_t bits, float qs, float nref, float2& sum, float& mx,
-                                       uint32_t* out) {
-  const float2 q2 = make_float2(qs, qs), r2 = make_float2(nref, nref);
-#pragma unroll
-  for (int c = 0; c < 32; c += 4) {
-    float2 x0 = make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-    float2 x1 = make_float2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
-    if (E4M3) {
-      const float4 k4 = *reinterpret_cast<const float4*>(ks + c);
-      x0 = __fmul2_rn(x0, make_float2(k4.x, k4.y));
-      x1 = __fmul2_rn(x1, make_float2(k4.z, k4.w));
-    }
-    if (EDGE) {
-      if (!((bits >> c) & 1u)) x0.x = -INFINITY;
-      if (!((bits >> (c + 1)) & 1u)) x0.y = -INFINITY;
-      if (!((bits >> (c + 2)) & 1u)) x1.x = -INFINITY;
-      if (!((bits >> (c + 3)) & 1u)) x1.y = -INFINITY;
-    }
-    mx = max3f(mx, x0.x, x0.y);
-    mx = max3f(mx, x1.x, x1.y);
-    float2 e0 = __ffma2_rn(x0, q2, r2), e1 = __ffma2_rn(x1, q2, r2);
-    e0.x = ex2(e0.x);
-    e0.y = ex2(e0.y);
-    e1.x = ex2(e1.x);
-    e1.y = ex2(e1.y);
-    sum = __fadd2_rn(sum, e0);
-    sum = __fadd2_rn(sum, e1);
-    if (E4M3) {
-      const float4 v4 = *reinterpret_cast<const float4*>(vs + c);
-      e0 = __fmul2_rn(e0, make_float2(v4.x, v4.y));
-      e1 = __fmul2_rn(e1, make_float2(v4.z, v4.w));
-    }
-    out[c / 2] = pack2<BF>(e0.x, e0.y);
-    out[c / 2 + 1] = pack2<BF>(e1.x, e1.y);
-  }
+// Does drafted token i of a sequence attend slot `key`?
+__device__ __forceinline__ bool slot_allowed(const TreeArgs& a, const uint8_t* mask, SeqLen s, int i, int key) {
+  const int j = key - s.len;
+  return j < 0 || (j < s.n && tree_allows(mask, a.T, i, j));
 }
 
-// The largest of 32 scores of a row (scaled as in soft32), joined to mx.
-template <bool E4M3, bool EDGE>
-__device__ __forceinline__ float max32(const uint32_t (&s)[32], const float* ks, uint32_t bits, float mx) {
-#pragma unroll
-  for (int c = 0; c < 32; c += 2) {
-    float x0 = __uint_as_float(s[c]), x1 = __uint_as_float(s[c + 1]);
-    if (E4M3) {
-      const float2 k2 = *reinterpret_cast<const float2*>(ks + c);
-      x0 *= k2.x;
-      x1 *= k2.y;
-    }
-    if (EDGE) {
-      if (!((bits >> c) & 1u)) x0 = -INFINITY;
-      if (!((bits >> (c + 1)) & 1u)) x1 = -INFINITY;
-    }
-    mx = max3f(mx, x0, x1);
-  }
-  return mx;
+// .16x256b.x4: 16 lanes x 32 columns.  Thread t gets, for k = 0..3, the columns 8k + 2(t%4) + {0,1}
+// of lane t/4 (registers 4k, 4k+1) and of lane t/4 + 8 (4k+2, 4k+3).
+__device__ __forceinline__ void tmem_ld16x256_16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+// .16x128b.x8: 16 lanes x 32 columns.  Thread t has, for k = 0..7, column 4k + t%4 of lane t/4
+// (register 2k) and of lane t/4 + 8 (2k+1).
+__device__ __forceinline__ void tmem_st16x128_16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+        "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+        "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld16x128_16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x128b.x8.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
 }
 
-// Does the V row of slot `slot` hold an infinity or NaN?  (A drafted token's, its page checked.)
+// Two consecutive values (index of the first, even) in the output type.
+__device__ __forceinline__ void store2(void* out, int dtype, size_t idx, float x, float y) {
+  if (dtype == 2) *reinterpret_cast<float2*>(static_cast<float*>(out) + idx) = make_float2(x, y);
+  else *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(out) + idx) = dtype == 1 ? pack2<true>(x, y) : pack2<false>(x, y);
+}
+
+// Does the V row of slot `slot`, or one of its scales, hold an infinity or NaN?
 template <int D, bool E4M3, bool BF>
 __device__ __noinline__ bool v_row_bad(const TreeArgs& a, int b, int h, int slot) {
   const int page = __ldg(a.table + (size_t)b * a.MP + (slot >> a.c.page_shift));
   if (!page_inside(page, a.c.pages)) return false;
   const long long row = row_of(page, a.c.Hkv, h, a.c.page_shift, slot);
-  bool bad = E4M3 && !(fabsf(__ldg(a.c.vs + row)) < INFINITY);
+  bool bad = E4M3 && !(fabsf(__ldg(a.c.vs + row)) < INFINITY && fabsf(__ldg(a.c.ks + row)) < INFINITY);
   for (int i = 0; i < D * (E4M3 ? 1 : 2) / 16; ++i)
     bad = bad || not_finite16<E4M3, BF>(
                      __ldg(reinterpret_cast<const uint4*>(a.c.v + row * D * (E4M3 ? 1 : 2)) + i));
@@ -249,12 +235,16 @@ __device__ __noinline__ bool v_row_bad(const TreeArgs& a, int b, int h, int slot
 }
 
 template <int D, bool E4M3, bool QBF, bool SHARE>
-__global__ void __launch_bounds__(kTThreads, 1)
+__global__ void __launch_bounds__(kTThreads<E4M3>, 1)
     k_tree_tiles(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                  const __grid_constant__ TreeArgs a, int rows_unit) {
   using C = TilesCfg<D, E4M3>;
   using Smem = TilesSmem<D, E4M3>;
   constexpr bool BF = QBF && !E4M3;              // type of the MMA operands
+  // log2 of how far P may exceed 1 before the reference moves: fp16 ends at 2^16; a bf16 P of
+  // 2^40 leaves its sums and O (fp32) far from their end
+  constexpr float kGrow = BF ? 40.f : 14.f;
+  constexpr int kMma = 16 + kTLoad<E4M3>;
   extern __shared__ uint8_t smem_raw[];
   Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                       ~static_cast<uintptr_t>(1023));
@@ -268,9 +258,9 @@ __global__ void __launch_bounds__(kTThreads, 1)
       mbar_init(&sm.tail[i], 1);
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&sm.q_full[s], 4);
+      mbar_init(&sm.q_full[s], 8);
       mbar_init(&sm.s_full[s], 2);
-      mbar_init(&sm.p_full[s], 4);
+      mbar_init(&sm.p_full[s], 8);
       mbar_init(&sm.o_done[s], 1);
     }
     mbar_init(&sm.drain, 1);
@@ -278,7 +268,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
     sm.bad_v = 0;
     fence_mbar_init();
   }
-  if (warp == 12) {
+  if (warp == kMma) {
     tmem_alloc(&sm.tmem, 512);
     tmem_relinquish();
   }
@@ -292,11 +282,15 @@ __global__ void __launch_bounds__(kTThreads, 1)
   const Run& run0 = sm.run[0];
   const Run& run1 = sm.run[SHARE ? 0 : 1];
 
-  if (warp >= 8 && warp < 12) {
+  // registers at launch and by role: 768 x 80 = 512 x 96 + 128 x 48 + 128 x 48, and with
+  // e4m3, whose loaders hold a tile, 896 x 72 = 512 x 80 + 256 x 72 + 128 x 40
+  constexpr int kRegSoft = E4M3 ? 80 : 96, kRegMma = E4M3 ? 40 : 48;
+  if (warp >= 16 && warp < 16 + kTLoad<E4M3>) {
     // ------------------------------------------------------------ loaders
+    if (!E4M3) setmaxnreg_dec<48>();
     Walk<SHARE> w;
     w.start(a, sm.run);
-    const int lw = warp - 8;
+    const int lw = (warp - 16) & 3, lgroup = (warp - 16) >> 2;
     bool ok = true;
     if (!E4M3) {
       int e = 0;
@@ -341,7 +335,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
             break;
           }
           tails ^= 1u << buf;
-          const int r = tid - 8 * 32;
+          const int r = tid - 16 * 32;
           if (key0 + r >= c.s.len) {
             bool zero = key0 + r >= L;
             if (!zero) {
@@ -367,9 +361,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
           mbar_wait(&sm.full[u % C::kBufs], (u / C::kBufs) & 1, nullptr);
       }
     } else {
-      // registers of two tiles: one being stored, the next one on its way
       constexpr int LPR = D / 16, RPP = 128 / LPR, NP = kTT / RPP;   // lanes of a row, rows of a pass
-      const int lt = tid - 8 * 32, lr = lt / LPR, lc = lt % LPR;
+      const int lt = (tid - 16 * 32) & 127, lr = lt / LPR, lc = lt % LPR;
       struct Ahead {
         uint4 u[NP];
         float ks, vs;
@@ -419,8 +412,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
         }
         w.step(a, pairs);
       };
-      int e = 0;
-      auto put = [&](Ahead& x) -> bool {
+      auto put = [&](Ahead& x, int e) -> bool {
         const int buf = e % C::kBufs;
         if (e >= C::kBufs && !mbar_wait_warp(&sm.empty[buf], (e / C::kBufs - 1) & 1, abort_flag)) return false;
         uint8_t* dst = sm.kv[buf];
@@ -428,13 +420,21 @@ __global__ void __launch_bounds__(kTThreads, 1)
         if (!x.v) {
           // the scales of both; slot x.t % kTScales was last read kTScales tiles ago, and a
           // V tile later than that one has been freed
-          float vs = x.vs;
-          if (edge && x.key0 + lt >= x.len && !(fabsf(vs) < INFINITY)) {
-            vs = 0.f;
-            sm.bad_v = 1;
+          float ks = x.ks, vs = x.vs;
+          if (x.key0 + lt >= x.len) {
+            // masked scores are -inf before the key scale multiplies them, and P is 0 before the
+            // value scale does: the scales of drafted rows become finite, a key's not 0 (a row of
+            // scale 0 has codes 0), those behind the last key are 0
+            if (!(fabsf(vs) < INFINITY) || !(fabsf(ks) < INFINITY)) {
+              if (!(fabsf(vs) < INFINITY)) vs = 0.f;
+              if (!(fabsf(ks) < INFINITY)) ks = 1.f;
+              sm.bad_v = 1;
+            }
+            if (ks == 0.f) ks = 1.f;
           }
-          sm.ks[x.s][x.t % kTScales][lt] = x.ks;
-          sm.vs[x.s][x.t % kTScales][lt] = vs;
+          float* sc = sm.scl[x.s][x.t % kTScales] + 4 * (lt >> 1) + (lt & 1);
+          sc[0] = ks;
+          sc[2] = vs;
         }
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
@@ -467,23 +467,22 @@ __global__ void __launch_bounds__(kTThreads, 1)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.full[buf]);
-        ++e;
         return true;
       };
-      Ahead x0, x1;
-      fetch(x0);
-      fetch(x1);
-      while (x0.there) {
-        if (!put(x0)) break;
-        fetch(x0);
-        if (!x1.there) break;
-        if (!put(x1)) break;
-        fetch(x1);
+      // the two groups take every other tile: one loads while the other stores
+      if (lgroup && w.more) w.step(a, pairs);
+      int e = lgroup;
+      Ahead x;
+      for (fetch(x); x.there; fetch(x)) {
+        if (!put(x, e)) break;
+        e += 2;
+        if (w.more) w.step(a, pairs);
       }
     }
-  } else if (warp == 12) {
+  } else if (warp >= 16) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
+    setmaxnreg_dec<kRegMma>();
+    if (warp == kMma && lane == 0) {
       constexpr uint32_t idesc_s = idesc_f16_f32(kTT, kTT, BF);
       constexpr uint32_t idesc_o = idesc_f16_f32(kTT, D, BF) | (1u << 16);   // B is [k][n]
       const uint64_t dq = smem_desc_kmajor(sm.q[0], 128);
@@ -491,12 +490,19 @@ __global__ void __launch_bounds__(kTThreads, 1)
       const uint64_t dv = smem_desc_nmajor(sm.kv[0], kTT * 128);
       constexpr uint32_t kBuf16 = C::kTileBytes >> 4;
       int nt[2] = {(int)(run0.t1 - run0.t0), (int)(run1.t1 - run1.t0)};
-      Cursor c0, c1;
-      if (nt[0] > 0) c0.start(a, run0, kTT);
-      if (nt[1] > 0) c1.start(a, run1, kTT);
+      // tiles of the slot's piece from the current one on; a piece's first tile is next
+      int left0 = 0, left1 = 0;
+      bool new0 = true, new1 = true;
+      if (nt[0] > 0) {
+        sm.mma_at[0].start(a, run0, kTT);
+        left0 = sm.mma_at[0].tiles - sm.mma_at[0].tile;
+      }
+      if (nt[1] > 0) {
+        sm.mma_at[1].start(a, run1, kTT);
+        left1 = sm.mma_at[1].tiles - sm.mma_at[1].tile;
+      }
       int e = 0;                   // buffers taken
-      int piece0 = 0, piece1 = 0;
-      int k_at = 0;                // SHARE: entry of the K tile that slot 0 took last
+      int pieces = 0;              // parity of each slot's piece
       bool ok = true;
       auto wait_full = [&](int u) {
         return mbar_wait(&sm.full[u % C::kBufs], (u / C::kBufs) & 1, abort_flag);
@@ -504,9 +510,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
       // S of slot s; entry u; `first`: a piece starts with this tile
       auto scores = [&](int s, int u, bool first, bool release) -> bool {
         if (first) {
-          int& piece = s ? piece1 : piece0;
-          if (!mbar_wait(&sm.q_full[s], piece & 1, abort_flag)) return false;
-          ++piece;
+          if (!mbar_wait(&sm.q_full[s], (pieces >> s) & 1, abort_flag)) return false;
+          pieces ^= 1 << s;
         }
         if (!wait_full(u)) return false;
         mbar_arrive(&sm.s_full[s]);
@@ -544,22 +549,37 @@ __global__ void __launch_bounds__(kTThreads, 1)
         if (nt[0] > 0) ok = scores(0, e++, true, true);
         if (ok && nt[1] > 0) ok = scores(1, e++, true, true);
       }
-      for (int t = 0; ok && t < nt[0]; ++t) {
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          if (!ok || t >= nt[s]) continue;
-          Cursor& c = s ? c1 : c0;
-          const int u = SHARE ? k_at + 1 : e;        // this V; K of the next tile is u + 1
-          const bool first = t == 0 || c.tile == 0, more = t + 1 < nt[s];
-          const bool rel = SHARE ? s == 1 : true;
-          ok = values(s, t, u, first, rel);
-          if (ok && more) {
+      const int nt0 = nt[0], nt1 = nt[1];
+#pragma unroll 1
+      for (int ts = 0; ok && ts < 2 * nt0; ++ts) {
+        const int t = ts >> 1, s = ts & 1, n = s ? nt1 : nt0;
+        if (t >= n) continue;
+        int left = s ? left1 : left0;
+        bool fresh = s ? new1 : new0;
+        const int u = SHARE ? 2 * t + 1 : e;       // this V; K of the next tile is u + 1
+        const bool more = t + 1 < n;
+        const bool rel = SHARE ? s == 1 : true;
+        ok = values(s, t, u, fresh, rel);
+        fresh = false;
+        if (ok && more) {
+          if (--left == 0) {
+            Cursor c = sm.mma_at[s];
+            c.tile = c.tiles - 1;
             c.next(a, pairs, kTT);
-            ok = scores(s, u + 1, c.tile == 0, rel);
+            sm.mma_at[s] = c;
+            left = c.tiles;
+            fresh = true;
           }
-          if (!SHARE) e += more ? 2 : 1;
+          ok = scores(s, u + 1, fresh, rel);
         }
-        if (SHARE) k_at += 2;
+        if (s) {
+          left1 = left;
+          new1 = fresh;
+        } else {
+          left0 = left;
+          new0 = fresh;
+        }
+        if (!SHARE) e += more ? 2 : 1;
       }
       // every MMA issued so far completes before the block frees TMEM
       tc_commit(&sm.drain);
@@ -567,77 +587,81 @@ __global__ void __launch_bounds__(kTThreads, 1)
     }
     __syncwarp();
   } else {
-    // ------------------------------------------------------------ softmax, a thread per row
-    const int s = warp >> 2, rl = (warp & 3) * 32 + lane;        // row of the slot
+    // ------------------------------------------------------------ softmax
+    // Eight warps a slot.  The .16x256b loads give a warp 16 TMEM lanes and each of its
+    // quads two rows, t/4 and t/4 + 8, so that four warps share a scheduler.  Row r
+    // of the slot is on lane 32 (r/16 % 4) + 16 (r/64) + r%16: any number of rows is
+    // spread evenly over the schedulers.
+    setmaxnreg_inc<kRegSoft>();
+    const int s = warp >> 3, quad = warp & 3, hf = (warp >> 2) & 1, g = lane & 3;
+    const int lo = (SHARE ? s * kTT : 0) + 64 * hf + 16 * quad + (lane >> 2);   // of the unit's rows: lo, lo + 8
+    const int ml = 32 * quad + 16 * hf + (lane >> 2);                           // TMEM lane: ml, ml + 8
     const Run& run = s ? run1 : run0;
     const int nt = (int)(run.t1 - run.t0);
-    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t lanes = static_cast<uint32_t>(32 * quad + 16 * hf) << 16;
     const uint32_t tS = tmem + lanes + s * 128, tO = tmem + lanes + 256 + s * 128;
     const float kL2E = 1.4426950408889634f;
     Cursor at;
     if (nt > 0) at.start(a, run, kTT);
-    int piece = 0;
     bool ok = true;
-    float ref = -INFINITY, l = 0.f, qs = 0.f;
-    int r = 0, i = 0;
+    float ref[2], l[2], qs[2];
+    int r[2];
     bool active = false;
     for (int t = 0; t < nt; ++t) {
-      const int h = at.pair / a.RT;
-      if (t == 0 || at.tile == 0) {
+      const bool first = t == 0 || at.tile == 0;
+      if (first) {
         // a piece starts: the slot's rows of Q.  The last S of the piece before has been waited
         // for, so nothing reads the buffer.
-        const int unit0 = (at.pair % a.RT) * rows_unit;
-        const int lo = (SHARE ? s * kTT : 0) + rl;
-        r = lo < rows_unit ? unit0 + lo : R;
-        active = __any_sync(0xffffffffu, r < R);
-        i = r % a.T;
-        qs = a.sm_scale * kL2E;
-        ref = -INFINITY;
-        l = 0.f;
-        uint4 u[D / 8];
-        if (r < R) {
+        const int unit0 = (at.pair % a.RT) * rows_unit, h = at.pair / a.RT;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          r[e] = lo + 8 * e < rows_unit ? min(unit0 + lo + 8 * e, R) : R;
+          qs[e] = a.sm_scale * kL2E;
+          ref[e] = -INFINITY;
+          l[e] = 0.f;
+          uint4 u[D / 32];
           const uint4* src = reinterpret_cast<const uint4*>(
-              static_cast<const uint16_t*>(a.q) + at.b * a.sb + (long long)(h * a.G + r / a.T) * a.sh +
-              (long long)i * a.st);
+              static_cast<const uint16_t*>(a.q) + at.b * a.sb + (long long)(h * a.G + r[e] / a.T) * a.sh +
+              (long long)(r[e] % a.T) * a.st);
 #pragma unroll
-          for (int c = 0; c < D / 8; ++c) u[c] = __ldg(src + c);
-        } else {
+          for (int c = 0; c < D / 32; ++c) u[c] = r[e] < R ? __ldg(src + 4 * c + g) : make_uint4(0u, 0u, 0u, 0u);
+          if (E4M3) {
+            float amax = 0.f;
 #pragma unroll
-          for (int c = 0; c < D / 8; ++c) u[c] = make_uint4(0u, 0u, 0u, 0u);
-        }
-        if (E4M3) {
-          float amax = 0.f;
+            for (int c = 0; c < D / 32; ++c) {
+              const uint32_t w4[4] = {u[c].x, u[c].y, u[c].z, u[c].w};
 #pragma unroll
-          for (int c = 0; c < D / 8; ++c) {
-            const uint32_t w4[4] = {u[c].x, u[c].y, u[c].z, u[c].w};
+              for (int y = 0; y < 4; ++y) {
+                const float2 f = halves<QBF>(w4[y]);
+                amax = max3f(amax, fabsf(f.x), fabsf(f.y));
+              }
+            }
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+            // an exact power of two that puts the largest value at 2^13
+            const int ex = (int)(__float_as_uint(amax) >> 23);
+            const int sh = (ex == 0 || ex == 255) ? 0 : max(-114, min(60, 13 + 127 - ex));
+            const float up = __uint_as_float((uint32_t)(127 + sh) << 23);
+            qs[e] *= __uint_as_float((uint32_t)(127 - sh) << 23);
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const float2 f = halves<QBF>(w4[y]);
-              amax = max3f(amax, fabsf(f.x), fabsf(f.y));
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t w4[4] = {u[c].x, u[c].y, u[c].z, u[c].w};
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                const float2 f = halves<QBF>(w4[y]);
+                w4[y] = pack2<false>(f.x * up, f.y * up);
+              }
+              u[c] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
             }
           }
-          // an exact power of two that puts the largest value at 2^13
-          const int ex = (int)(__float_as_uint(amax) >> 23);
-          const int sh = (ex == 0 || ex == 255) ? 0 : max(-114, min(60, 13 + 127 - ex));
-          const float up = __uint_as_float((uint32_t)(127 + sh) << 23);
-          qs *= __uint_as_float((uint32_t)(127 - sh) << 23);
 #pragma unroll
-          for (int c = 0; c < D / 8; ++c) {
-            uint32_t w4[4] = {u[c].x, u[c].y, u[c].z, u[c].w};
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const float2 f = halves<QBF>(w4[y]);
-              w4[y] = pack2<false>(f.x * up, f.y * up);
-            }
-            u[c] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
-          }
+          for (int c = 0; c < D / 32; ++c)
+            *reinterpret_cast<uint4*>(sm.q[s] + tile_off(ml + 8 * e, 4 * c + g)) = u[c];
         }
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) *reinterpret_cast<uint4*>(sm.q[s] + tile_off(rl, c)) = u[c];
+        active = __any_sync(0xffffffffu, r[0] < R);
         fence_proxy_async_smem();
         __syncwarp();
         mbar_arrive_lane0(&sm.q_full[s], lane);
-        ++piece;
       }
       if (!mbar_wait_warp(&sm.s_full[s], t & 1, abort_flag)) {
         ok = false;
@@ -645,87 +669,126 @@ __global__ void __launch_bounds__(kTThreads, 1)
       }
       tc_fence_after();
       const int key0 = at.tile * kTT;
-      const bool edge = key0 + kTT > at.s.len, first = t == 0 || at.tile == 0;
       if (active) {
-        const float* ks = sm.ks[E4M3 && !SHARE ? s : 0][E4M3 ? t % kTScales : 0];
-        const float* vs = sm.vs[E4M3 && !SHARE ? s : 0][E4M3 ? t % kTScales : 0];
+        const float* sc = sm.scl[E4M3 && !SHARE ? s : 0][E4M3 ? t % kTScales : 0];
         float lv = 0.f;
         if (E4M3) {
-          const float4 v4 = *reinterpret_cast<const float4*>(vs + 4 * lane);
-          float m = fmaxf(fmaxf(v4.x, v4.y), fmaxf(v4.z, v4.w));
+          const float4 v0 = *reinterpret_cast<const float4*>(sc + 8 * lane);
+          const float4 v1 = *reinterpret_cast<const float4*>(sc + 8 * lane + 4);
+          float m = fmaxf(fmaxf(v0.z, v0.w), fmaxf(v1.z, v1.w));
 #pragma unroll
           for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
           lv = log2f(fmaxf(m, kVrefLeast));
         }
-        uint32_t bits[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
-        if (edge) {
+        if (key0 + kTT > at.s.len) {
+          // scores that the mask or the length leaves out become -inf where they lie
           const uint8_t* mask = a.mask ? a.mask + at.b * a.mask_sb : nullptr;
+          const int i0 = r[0] % a.T, i1 = r[1] % a.T;
+#pragma unroll 1
+          for (int c = 0; c < kTT; c += 32) {
+            uint32_t x[16];
+            tmem_ld16x256_16(tS + c, x);
+            tmem_ld_wait();
 #pragma unroll
-          for (int c = 0; c < 4; ++c) bits[c] = r < R ? allowed32(a, mask, at.s, i, key0 + 32 * c) : 0u;
-        }
-        uint32_t p0[32], p1[32];
-        float lsum;
-        bool fresh = first;
-        while (true) {
-          if (fresh) {
-            float mx = -INFINITY;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t x[32];
-              tmem_ld32(tS + 32 * c, x);
-              tmem_ld_wait();
-              mx = edge ? max32<E4M3, true>(x, E4M3 ? ks + 32 * c : nullptr, bits[c], mx)
-                        : max32<E4M3, false>(x, E4M3 ? ks + 32 * c : nullptr, 0u, mx);
+            for (int y = 0; y < 16; ++y) {
+              const int key = key0 + c + 8 * (y >> 2) + 2 * g + (y & 1);
+              if (!slot_allowed(a, mask, at.s, y & 2 ? i1 : i0, key)) x[y] = 0xff800000u;
             }
-            const float want = mx == -INFINITY ? mx : mx * qs + lv;
-            const float now = fmaxf(ref, want);
+            tmem_st16x256_16(tS + c, x);
+          }
+          tmem_st_wait();
+        }
+        // P of chunk c (64 keys, 32 columns) goes over scores that have been read
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+          uint32_t p[16];
+          float2 sum[2];
+          while (true) {
+            const float n0 = ref[0] == -INFINITY ? 0.f : -ref[0], n1 = ref[1] == -INFINITY ? 0.f : -ref[1];
+            const float2 q0 = make_float2(qs[0], qs[0]), q1 = make_float2(qs[1], qs[1]);
+            const float2 m0 = make_float2(n0, n0), m1 = make_float2(n1, n1);
+            float mx[2] = {-INFINITY, -INFINITY};
+            sum[0] = sum[1] = make_float2(0.f, 0.f);
+            uint32_t x[32];
+            tmem_ld16x256_32(tS + 64 * c, x);
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              float2 x0 = make_float2(__uint_as_float(x[4 * k]), __uint_as_float(x[4 * k + 1]));
+              float2 x1 = make_float2(__uint_as_float(x[4 * k + 2]), __uint_as_float(x[4 * k + 3]));
+              float4 f4;
+              if (E4M3) {
+                // two key scales and two value scales
+                f4 = *reinterpret_cast<const float4*>(sc + 2 * (64 * c + 8 * k + 2 * g));
+                x0 = __fmul2_rn(x0, make_float2(f4.x, f4.y));
+                x1 = __fmul2_rn(x1, make_float2(f4.x, f4.y));
+              }
+              mx[0] = max3f(mx[0], x0.x, x0.y);
+              mx[1] = max3f(mx[1], x1.x, x1.y);
+              float2 e0 = __ffma2_rn(x0, q0, m0), e1 = __ffma2_rn(x1, q1, m1);
+              e0.x = ex2(e0.x);
+              e0.y = ex2(e0.y);
+              e1.x = ex2(e1.x);
+              e1.y = ex2(e1.y);
+              sum[0] = __fadd2_rn(sum[0], e0);
+              sum[1] = __fadd2_rn(sum[1], e1);
+              if (E4M3) {
+                e0 = __fmul2_rn(e0, make_float2(f4.z, f4.w));
+                e1 = __fmul2_rn(e1, make_float2(f4.z, f4.w));
+              }
+              p[2 * k] = pack2<BF>(e0.x, e0.y);
+              p[2 * k + 1] = pack2<BF>(e1.x, e1.y);
+            }
+            const bool over = (mx[0] > -INFINITY && mx[0] * qs[0] + lv > ref[0] + kGrow) ||
+                              (mx[1] > -INFINITY && mx[1] * qs[1] + lv > ref[1] + kGrow);
+            if (!__any_sync(0xffffffffu, over)) break;
+            // the references move to the largest scores so far: the sums, O (at rest once P V of the
+            // tile before is done) and the P of chunk 0 follow, and this chunk is done again
+            float f[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
+              mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
+              const float now = mx[e] == -INFINITY ? ref[e] : fmaxf(ref[e], mx[e] * qs[e] + lv);
+              f[e] = ref[e] == -INFINITY ? 0.f : ex2(ref[e] - now);
+              ref[e] = now;
+              l[e] *= f[e];
+            }
             if (!first) {
-              // O and the sum move to the new reference; O is at rest once P V of the tile before is done
-              const float f = ref == -INFINITY ? 0.f : ex2(ref - now);
-              l *= f;
               if (!mbar_wait_warp(&sm.o_done[s], (t - 1) & 1, abort_flag)) {
                 ok = false;
                 break;
               }
               tc_fence_after();
-#pragma unroll
-              for (int c = 0; c < D; c += 32) {
-                uint32_t x[32];
-                tmem_ld32(tO + c, x);
+#pragma unroll 1
+              for (int d0 = 0; d0 < D; d0 += 32) {
+                uint32_t y[16];
+                tmem_ld16x256_16(tO + d0, y);
                 tmem_ld_wait();
 #pragma unroll
-                for (int y = 0; y < 32; ++y) x[y] = __float_as_uint(__uint_as_float(x[y]) * f);
-                tmem_st32(tO + c, x);
+                for (int z = 0; z < 16; ++z) y[z] = __float_as_uint(__uint_as_float(y[z]) * f[(z >> 1) & 1]);
+                tmem_st16x256_16(tO + d0, y);
               }
-              tmem_st_wait();
             }
-            ref = now;
-          }
-          const float nref = ref == -INFINITY ? 0.f : -ref;
-          float2 sum = make_float2(0.f, 0.f);
-          float mx = -INFINITY;
+            tmem_st_wait();
+            if (c == 1) {
+              uint32_t y[16];
+              tmem_ld16x128_16(tS, y);
+              tmem_ld_wait();
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t x[32];
-            tmem_ld32(tS + 32 * c, x);
-            tmem_ld_wait();
-            uint32_t* out = (c < 2 ? p0 : p1) + 16 * (c & 1);
-            if (edge)
-              soft32<E4M3, BF, true>(x, E4M3 ? ks + 32 * c : nullptr, E4M3 ? vs + 32 * c : nullptr, bits[c],
-                                     qs, nref, sum, mx, out);
-            else
-              soft32<E4M3, BF, false>(x, E4M3 ? ks + 32 * c : nullptr, E4M3 ? vs + 32 * c : nullptr, 0u, qs,
-                                      nref, sum, mx, out);
+              for (int z = 0; z < 16; ++z) {
+                const float2 w2 = halves<BF>(y[z]);
+                y[z] = pack2<BF>(w2.x * f[z & 1], w2.y * f[z & 1]);
+              }
+              tmem_st16x128_16(tS, y);
+            }
           }
-          lsum = sum.x + sum.y;
-          if (fresh) break;
-          fresh = __any_sync(0xffffffffu, mx > -INFINITY && mx * qs + lv > ref + kTGrow);
-          if (!fresh) break;
+          if (!ok) break;
+          tmem_st16x128_16(tS + 32 * c, p);
+          l[0] += sum[0].x + sum[0].y;
+          l[1] += sum[1].x + sum[1].y;
         }
         if (!ok) break;
-        l += lsum;
-        tmem_st32(tS, p0);
-        tmem_st32(tS + 32, p1);
         tmem_st_wait();
       }
       tc_fence_before();
@@ -742,41 +805,46 @@ __global__ void __launch_bounds__(kTThreads, 1)
         if (active) {
           const int start = at.tile - min(t, at.tile);     // the piece's first tile of the pair
           const bool whole = start == 0 && at.tile + 1 == at.tiles;
-          const int vb = SHARE ? blockIdx.x : 2 * blockIdx.x + s;
-          if (*static_cast<volatile int*>(&sm.bad_v) && r < R) {
-            // a drafted token's V was not finite somewhere: rows that attend such a one get NaN
-            const uint8_t* mask = a.mask ? a.mask + at.b * a.mask_sb : nullptr;
-            for (int j = 0; j < at.s.n; ++j)
-              if (tree_allows(mask, a.T, i, j) && v_row_bad<D, E4M3, QBF>(a, at.b, h, at.s.len + j))
-                l = __int_as_float(0x7fffffff);
-          }
-          const bool none = i >= at.s.n || l == 0.f;
-          const float inv = none ? 0.f : 1.f / l;
-          const size_t orow = ((size_t)at.b * a.Hq + h * a.G + r / a.T) * a.T + i;
-          const size_t prow = (size_t)(2 * vb + (start == 0 ? 1 : 0)) * rows_unit +
-                              (SHARE ? s * kTT : 0) + rl;
+          const int vb = SHARE ? blockIdx.x : 2 * blockIdx.x + s, h = at.pair / a.RT;
+          float inv[2];
+          bool none[2];
+          size_t row[2];
 #pragma unroll
-          for (int c = 0; c < D; c += 32) {
-            uint32_t x[32];
-            tmem_ld32(tO + c, x);
-            tmem_ld_wait();
-            if (r < R) {
-#pragma unroll
-              for (int y = 0; y < 32; y += 4) {
-                float f[4];
-#pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                  f[z] = __uint_as_float(x[y + z]);
-                  if (whole) f[z] = none ? 0.f : f[z] * inv;
-                }
-                if (whole) store4(a.o, a.o_dtype, orow * D + c + y, f);
-                else store4(a.part, 2, prow * D + c + y, f);
-              }
+          for (int e = 0; e < 2; ++e) {
+            const int i = r[e] % a.T;
+            l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+            l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+            if (*static_cast<volatile int*>(&sm.bad_v) && r[e] < R) {
+              // a drafted token's V was not finite somewhere: rows that attend such a one get NaN
+              const uint8_t* mask = a.mask ? a.mask + at.b * a.mask_sb : nullptr;
+              for (int j = 0; j < at.s.n; ++j)
+                if (tree_allows(mask, a.T, i, j) && v_row_bad<D, E4M3, QBF>(a, at.b, h, at.s.len + j))
+                  l[e] = __int_as_float(0x7fffffff);
+            }
+            none[e] = i >= at.s.n || l[e] == 0.f;
+            inv[e] = none[e] ? 0.f : 1.f / l[e];
+            row[e] = whole ? ((size_t)at.b * a.Hq + h * a.G + r[e] / a.T) * a.T + i
+                           : (size_t)(2 * vb + (start == 0 ? 1 : 0)) * rows_unit + lo + 8 * e;
+            if (r[e] < R && g == 0) {
+              if (!whole) a.part_ml[row[e]] = make_float2(ref[e], l[e]);
+              else if (a.lse) a.lse[row[e]] = none[e] ? -INFINITY : row_lse(ref[e], l[e]);
             }
           }
-          if (r < R) {
-            if (!whole) a.part_ml[prow] = make_float2(ref, l);
-            else if (a.lse) a.lse[orow] = none ? -INFINITY : row_lse(ref, l);
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t x[16];
+            tmem_ld16x256_16(tO + c, x);
+            tmem_ld_wait();
+#pragma unroll
+            for (int y = 0; y < 16; y += 2) {
+              const int e = (y >> 1) & 1;
+              if (r[e] < R) {
+                float f0 = __uint_as_float(x[y]), f1 = __uint_as_float(x[y + 1]);
+                const size_t idx = row[e] * D + c + 8 * (y >> 2) + 2 * g;
+                if (whole) store2(a.o, a.o_dtype, idx, none[e] ? 0.f : f0 * inv[e], none[e] ? 0.f : f1 * inv[e]);
+                else store2(a.part, 2, idx, f0, f1);
+              }
+            }
           }
         }
       }
@@ -785,7 +853,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == kMma) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -819,7 +887,7 @@ static cudaError_t launch_tiles(TreeArgs a, int dev, cudaMemPool_t pool, cudaStr
   const int smem = sizeof(TilesSmem<D, E4M3>) + 1024;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e == cudaSuccess) {
-    kern<<<grid, kTThreads, smem, st>>>(tk, tv, a, unit);
+    kern<<<grid, kTThreads<E4M3>, smem, st>>>(tk, tv, a, unit);
     e = cudaGetLastError();
   }
   if (e == cudaSuccess) {
