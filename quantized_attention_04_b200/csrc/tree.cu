@@ -61,81 +61,89 @@ __device__ __forceinline__ bool tree_allows(const uint8_t* mask, int T, int i, i
 }
 
 // ------------------------------------------------------------ the work split
-// The block's run [t0, t1) of the global tile sequence, in shared memory, with
-// the pair it starts in.  `pairs`: pairs of one sequence (Hkv*RT).
+// A block's run of the global tile sequence and the pair it starts in.
 struct Run {
-  long long total, t0, t1;
-  int b, pair, tile;       // where t0 is
-  int grid;                // blocks that have work
+  int n;                   // tiles
+  int b, pair, tile;       // the first one
+  SeqLen s;                // of sequence b
 };
 
-// Called by the whole block (blockDim.x threads, whole warps).  Finds the run of
-// block `c` of `grid`, no block taking fewer than `least` tiles while others have none.
-__device__ void find_run(const TreeArgs& a, int tile, int pairs, int grid, int c, int least, Run* out,
-                         long long* scratch) {
-  const int tid = threadIdx.x, nth = blockDim.x, lane = tid & 31, warp = tid >> 5;
-  // pass 1: the total; pass 2: the sequence that holds t0
+// The run of block `c` of `grid`, by a whole warp (every warp that needs it works it out
+// for itself: no barrier).  No block takes fewer than `least` tiles while others have none.
+// `pairs`: pairs of one sequence (Hkv*RT).
+__device__ __forceinline__ Run warp_run(const TreeArgs& a, int tile, int pairs, int grid, int c, int least) {
+  const int lane = threadIdx.x & 31;
+  Run r{0, 0, 0, 0, {0, 0}};
+  SeqLen s{0, 0};
+  int tl = 0;
   long long total = 0;
-  for (int pass = 0; pass < 2; ++pass) {
-    long long carry = 0;
-    for (int b0 = 0; b0 < a.B; b0 += nth) {
-      const int b = b0 + tid;
-      int tl = 0;
-      if (b < a.B) tl = pair_tiles(seq_len(a.lens, a.n, b, a.T, a.MP, a.c.page_shift), tile);
-      const long long mine = (long long)tl * pairs;
-      long long incl = mine;
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    tl = 0;
+    if (b0 + lane < a.B) {
+      s = seq_len(a.lens, a.n, b0 + lane, a.T, a.MP, a.c.page_shift);
+      tl = pair_tiles(s, tile);
+    }
+    total += tl;
+  }
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
+  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  total *= pairs;
+  const int g = run_blocks(total, grid, least);
+  if (c >= g) return r;
+  const long long t0 = run_start(total, g, c);
+  r.n = (int)(run_start(total, g, c + 1) - t0);
+  if (r.n == 0) return r;
+  long long before = 0;    // tiles of the sequences before b0
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    if (a.B > 32) {        // else s and tl are at hand
+      tl = 0;
+      if (b0 + lane < a.B) {
+        s = seq_len(a.lens, a.n, b0 + lane, a.T, a.MP, a.c.page_shift);
+        tl = pair_tiles(s, tile);
       }
-      if (lane == 31) scratch[warp] = incl;
-      __syncthreads();
-      long long before = carry, all = 0;
-      for (int w = 0; w < nth / 32; ++w) {
-        const long long x = scratch[w];
-        if (w < warp) before += x;
-        all += x;
-      }
-      if (pass == 1) {
-        const long long first = before + incl - mine;
-        if (mine > 0 && out->t0 >= first && out->t0 < first + mine) {
-          const long long off = out->t0 - first;
-          out->b = b;
-          out->pair = (int)(off / tl);
-          out->tile = (int)(off % tl);
+    }
+    long long incl = (long long)tl * pairs;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const long long off = t0 - before - (incl - (long long)tl * pairs);
+    const unsigned here = __ballot_sync(0xffffffffu, off >= 0 && off < (long long)tl * pairs);
+    if (here) {
+      const int src = __ffs(here) - 1;
+      int pair = 0, at = 0;
+      if (lane == src) {
+        if (off <= INT_MAX) {
+          pair = (int)off / tl;
+          at = (int)off % tl;
+        } else {
+          pair = (int)(off / tl);
+          at = (int)(off % tl);
         }
       }
-      carry += all;
-      __syncthreads();
+      r.b = b0 + src;
+      r.pair = __shfl_sync(0xffffffffu, pair, src);
+      r.tile = __shfl_sync(0xffffffffu, at, src);
+      r.s.len = __shfl_sync(0xffffffffu, s.len, src);
+      r.s.n = __shfl_sync(0xffffffffu, s.n, src);
+      break;
     }
-    if (pass == 0) {
-      total = carry;
-      if (tid == 0) {
-        const int g = run_blocks(total, grid, least);
-        out->total = total;
-        out->grid = g;
-        out->t0 = c < g ? run_start(total, g, c) : total;
-        out->t1 = c < g ? run_start(total, g, c + 1) : total;
-      }
-      __syncthreads();
-    }
+    before += __shfl_sync(0xffffffffu, incl, 31);
   }
+  return r;
 }
 
 // Walks the tiles of a run.
 struct Cursor {
   int b, pair, tile, tiles;
   SeqLen s;
-  __device__ __forceinline__ void load(const TreeArgs& a, int tl) {
-    s = seq_len(a.lens, a.n, b, a.T, a.MP, a.c.page_shift);
-    tiles = pair_tiles(s, tl);
-  }
-  __device__ __forceinline__ void start(const TreeArgs& a, const Run& r, int tl) {
+  __device__ __forceinline__ void start(const Run& r, int tl) {
     b = r.b;
     pair = r.pair;
     tile = r.tile;
-    load(a, tl);
+    s = r.s;
+    tiles = pair_tiles(s, tl);
   }
   // to the next tile of the run, which exists
   __device__ __forceinline__ void next(const TreeArgs& a, int pairs, int tl) {
@@ -145,7 +153,8 @@ struct Cursor {
     pair = 0;
     do {
       ++b;
-      load(a, tl);
+      s = seq_len(a.lens, a.n, b, a.T, a.MP, a.c.page_shift);
+      tiles = pair_tiles(s, tl);
     } while (tiles == 0 && b + 1 < a.B);
   }
 };
@@ -250,6 +259,7 @@ __device__ __forceinline__ float row_lse(float m, float sum) {
 constexpr int kRowsWarps = 4;
 constexpr float kVrefLeast = 1e-30f;   // value scales below it count as part of it
 constexpr int kRowsTile = 16 * kRowsWarps;
+constexpr int kRowsLeast = 2;          // tiles that a block takes at least
 
 template <int D, bool E4M3>
 struct RowsCfg {
@@ -270,8 +280,6 @@ struct __align__(1024) RowsSmem {
   float2 ml[kRowsWarps][16];
   uint64_t full[kRowsWarps][C::kStages];
   int bad[kRowsWarps][C::kStages];                  // the stage's page was out of range
-  long long scratch[kRowsWarps];
-  Run run;
   int abort_flag;
 };
 
@@ -303,13 +311,12 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 2)
     sm.abort_flag = 0;
     fence_mbar_init();
   }
-  find_run(a, kRowsTile, pairs, gridDim.x, blockIdx.x, 2, &sm.run, sm.scratch);
+  const Run run = warp_run(a, kRowsTile, pairs, gridDim.x, blockIdx.x, kRowsLeast);
   __syncthreads();
-  const long long t0 = sm.run.t0;
-  const int nt = (int)(sm.run.t1 - t0);
-  if (nt <= 0) return;
+  const int nt = run.n;
+  if (nt == 0) return;
   Cursor in, at;                              // where loads are issued; where work is done
-  in.start(a, sm.run, kRowsTile);
+  in.start(run, kRowsTile);
   at = in;
   int issued = 0, used = 0, in_t = 0;         // tiles with keys of this warp
   // Issues the loads of the next tile in which this warp has keys, if the run has one.
@@ -933,8 +940,6 @@ static int sm_count(int dev) {
   return n[dev];
 }
 
-constexpr int kRowsLeast = 2;   // tiles that a block takes at least
-
 template <int D, bool E4M3, bool QBF, int MT>
 static cudaError_t launch_rows(TreeArgs a, int dev, cudaMemPool_t pool, cudaStream_t st) {
   using C = RowsCfg<D, E4M3>;
@@ -980,7 +985,7 @@ static cudaError_t tree_pick(const TreeArgs& a, int dev, cudaMemPool_t pool, cud
   const int R = a.G * a.T;
   if (R <= 16) return launch_rows<D, E4M3, QBF, 1>(a, dev, pool, st);
   if (R <= 32) return launch_rows<D, E4M3, QBF, 2>(a, dev, pool, st);
-  if (R <= kTT) return launch_tiles<D, E4M3, QBF, false>(a, dev, pool, st);
+  if (R <= kTR) return launch_tiles<D, E4M3, QBF, false>(a, dev, pool, st);
   return launch_tiles<D, E4M3, QBF, true>(a, dev, pool, st);
 }
 

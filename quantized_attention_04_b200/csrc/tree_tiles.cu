@@ -1,27 +1,29 @@
 // Attention of drafted tokens over a paged cache, many rows: k_tree_tiles.
 //
-// Row tiles of 128 against key tiles of 128 on the 5th-generation tensor cores.
-// A block holds two row tiles ("slots", one softmax warpgroup each), so that one
-// slot's softmax runs while the tensor cores work for the other:
+// Row tiles of 128 against key tiles of 64 on the 5th-generation tensor cores.
+// A block holds two row tiles ("slots", eight softmax warps each):
 //   SHARE   (more than 128 rows a pair): both slots walk the same run of key
 //           tiles with the two halves of up to 256 rows; K and V are loaded once.
 //   !SHARE  (up to 128 rows): each slot has a run of its own, as if it were a
 //           block, and its own K and V tiles.
-// Per slot and key tile: S = Q K^T (both in shared memory, fp32 S in TMEM),
-// softmax by a thread per row, P (16 bits) written over S in TMEM, O += P V with
-// P as the TMEM operand and V as it is cached ([key][d], the "MN-major" form), O in
-// TMEM for the whole run of a pair.
+// Per slot and key tile: S = Q K^T (both in shared memory, fp32 S in TMEM), softmax,
+// P (16 bits) written over S in TMEM, O += P V with P as the TMEM operand and V as it is
+// cached ([key][d], the "MN-major" form), O in TMEM for the whole run of a pair.  S is
+// double-buffered: S of the next tile is there when the softmax of this one ends, so
+// that the exponentials (16 a cycle and SM: 2048 cycles for 256 rows x 128 keys) and
+// the tensor cores (as many for both products) run side by side.
 //
 // The softmax passes over S once: exponentials are taken against the reference
 // left by the earlier keys, and only if some score of the warp's rows lies far above
-// it (kGrow) the reference moves, and O, the row sums and the tile's P so far are
-// rescaled.  A P above 1 keeps its relative precision.
+// it (kGrow) the reference moves, and O and the row sums are rescaled.  A P above 1
+// keeps its relative precision.
 //
 // 16-bit caches: K and V arrive by TMA, a box a page.  e4m3 caches: eight warps load
-// the codes (16 bytes a lane, in registers, two groups in turn), widen them to fp16
-// (exact) and store them in the same layout.  Q enters as fp16 scaled by a power of
-// two a row; the key scales multiply the scores and the value scales multiply P,
-// whose reference includes the tile's largest value scale.
+// the codes (16 bytes a lane, in registers), widen them to fp16
+// (exact) and store them in the same layout, while a warp ahead of them brings the rows
+// into L2.  Q enters as fp16 scaled by a power of two a row; the key scales multiply
+// the scores and the value scales multiply P, whose reference includes the tile's
+// largest value scale.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -33,43 +35,54 @@
 
 namespace sage2 {
 
-constexpr int kTT = 128;                  // keys of a tile, rows of a slot
-// Warps: 16 softmax, 4 loaders (e4m3: two groups of 4, which take turns), the MMA warp and 3 idle ones.
+constexpr int kTR = 128;                  // rows of a slot
+constexpr int kTK = 64;                   // keys of a tile
+constexpr int kTAhead = 8;                // tiles between the L2 prefetch and the loaders
+// Warps: 16 softmax, 4 loaders (one a ring; e4m3: 8, 4 or 2 a ring), 2 MMA warps, with e4m3 one
+// that prefetches and one that loads the scales.
 template <bool E4M3>
 constexpr int kTLoad = E4M3 ? 8 : 4;
 template <bool E4M3>
 constexpr int kTThreads = (16 + kTLoad<E4M3> + 4) * 32;
-constexpr int kTScales = 4;               // tiles of scales that a slot keeps
 
 template <int D, bool E4M3>
 struct TilesCfg {
   static constexpr int kBlk = D / 64;                    // 128-byte blocks of a row
-  static constexpr int kTileBytes = kTT * D * 2;         // a 16-bit tile of Q, K or V
-  static constexpr int kBufs = D == 128 ? (E4M3 ? 4 : 5) : 6;
+  static constexpr int kQBytes = kTR * D * 2;            // a tile of Q
+  static constexpr int kTileBytes = kTK * D * 2;         // a 16-bit tile of K or V
+  static constexpr int kBufs = D == 128 ? 8 : 16;        // rings of K and V (SHARE), or of each slot's K and V
+  // Tiles of scales that a slot keeps.  When K(t) is stored, K(t - kBufs/2), whose buffer it takes (or
+  // a later one), has been freed, so S of it and P V of the second tile before that are done: the
+  // softmax reads scales of the kBufs/2 + 2 tiles up to t at most.
+  static constexpr int kScales = kBufs;
+  static_assert(kScales >= kBufs / 2 + 2, "scales in use");
 };
 
 template <int D, bool E4M3>
 struct __align__(1024) TilesSmem {
   using C = TilesCfg<D, E4M3>;
-  uint8_t q[2][C::kTileBytes];
+  uint8_t q[2][C::kQBytes];
   uint8_t kv[C::kBufs][C::kTileBytes];
   // scales of a slot's last tiles; keys 2i, 2i+1: key scales at 4i, 4i+1, value scales at 4i+2, 4i+3
-  float scl[E4M3 ? 2 : 1][kTScales][E4M3 ? 2 * kTT : 4];
-  uint64_t full[C::kBufs];   // the four loader warps (and the TMA's bytes)
-  uint64_t empty[C::kBufs];  // commit of the last MMA that reads the buffer
-  uint64_t q_full[2];        // the slot's eight softmax warps
-  uint64_t s_full[2];        // the MMA thread (it has seen the tile's scales) and the commit of S
-  uint64_t p_full[2];        // the slot's eight softmax warps: S read, P written
-  uint64_t o_done[2];        // commit of O += P V
+  float scl[E4M3 ? 2 : 1][C::kScales][E4M3 ? 2 * kTK : 4];
+  float lv[E4M3 ? 2 : 1][C::kScales];   // log2 of the tile's largest value scale
+  uint64_t full[C::kBufs];   // the loader warps of the ring, with K the scale warp (or the TMA's bytes)
+  uint64_t empty[C::kBufs];  // commit of the MMAs that read the buffer (SHARE: of both slots)
   uint64_t tail[C::kBufs];   // bytes of a V tile that is checked before use
-  uint64_t drain;
-  long long scratch[28];
-  Run run[2];
-  Cursor mma_at[2];          // the MMA thread's: the piece that each slot is in
+  uint64_t q_full[2];        // the slot's eight softmax warps
+  uint64_t s_full[2][2];     // the MMA warp (it has seen the tile's scales) and the commit of S
+  uint64_t p_full[2][2];     // the slot's eight softmax warps: S read, P written
+  uint64_t o_done[2][2];     // commit of O += P V (by the tile's parity, as the two above)
+  uint64_t drain[2];
   uint32_t tmem;
+  int starts[C::kBufs];      // the K tile is a piece's first
   int bad_v;                 // a drafted token's V row or scale was not finite
+  int progress[2];           // by slot: V tiles stored
   int abort_flag;
 };
+
+static_assert(sizeof(TilesSmem<128, false>) + 1024 <= 232448 && sizeof(TilesSmem<128, true>) + 1024 <= 232448,
+              "shared memory of a block");
 
 // D[tmem] (+)= A[tmem] * B[smem], 16-bit A (two values a column), fp32 D.
 __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
@@ -88,93 +101,36 @@ __device__ __forceinline__ uint64_t smem_desc_nmajor(const void* p, uint32_t blo
          (static_cast<uint64_t>(2) << 61);
 }
 
-// Byte offset of 16-byte chunk `ch` (of D/8) of row `r` in a 128-row 16-bit tile.
-__device__ __forceinline__ uint32_t tile_off(int r, int ch) {
-  return (ch >> 3) * (kTT * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo, uint32_t hi) {
+  return (static_cast<uint64_t>(hi) << 32) | lo;
+}
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+// Four e4m3 codes to two packed fp16 pairs, exact.
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t& a, uint32_t& b) {
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+      : "=r"(a), "=r"(b)
+      : "r"(w));
+}
+// Lane 0's value, which the compiler then knows to be alike in all lanes.
+template <typename T>
+__device__ __forceinline__ T uniform(T x) {
+  return __shfl_sync(0xffffffffu, x, 0);
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
 }
 
-// The order in which K and V tiles are loaded and used.  A slot's tiles go
-// K(0), V(0), K(1), V(1), ..; with two runs the slots take turns after K(0) of each:
-// V0(t) K0(t+1) V1(t) K1(t+1).
-template <bool SHARE>
-struct Walk {
-  Cursor c[SHARE ? 1 : 2];
-  int t[2], nt[2];
-  bool v, pro, more;
-  int s;
-  __device__ __forceinline__ void start(const TreeArgs& a, const Run* run) {
-    nt[0] = (int)(run[0].t1 - run[0].t0);
-    nt[1] = SHARE ? 0 : (int)(run[1].t1 - run[1].t0);
-    t[0] = t[1] = 0;
-    if (nt[0] > 0) c[0].start(a, run[0], kTT);
-    if (!SHARE && nt[1] > 0) c[SHARE ? 0 : 1].start(a, run[1], kTT);
-    v = false;
-    pro = !SHARE;
-    s = 0;
-    more = nt[0] > 0;      // slot 1 has work only if slot 0 has
-  }
-  __device__ __forceinline__ void step(const TreeArgs& a, int pairs) {
-    if (SHARE) {
-      if (!v) {
-        v = true;
-      } else {
-        v = false;
-        if (++t[0] < nt[0]) c[0].next(a, pairs, kTT);
-        else more = false;
-      }
-      return;
-    }
-    if (pro) {
-      if (s == 0 && nt[1] > 0) {
-        s = 1;
-        return;
-      }
-      pro = false;
-      s = 0;
-      v = true;
-      return;
-    }
-    if (v) {
-      bool k = false;
-      if (s == 0) {
-        if (++t[0] < nt[0]) {
-          c[0].next(a, pairs, kTT);
-          k = true;
-        }
-      } else {
-        if (++t[1] < nt[1]) {
-          c[SHARE ? 0 : 1].next(a, pairs, kTT);
-          k = true;
-        }
-      }
-      if (k) {
-        v = false;
-        return;
-      }
-    }
-    v = true;
-    const bool l0 = t[0] < nt[0], l1 = t[1] < nt[1];
-    if (s == 0) s = l1 ? 1 : 0;
-    else s = l0 ? 0 : 1;
-    more = l0 || l1;
-  }
-  __device__ __forceinline__ Cursor cur() const { return SHARE || s == 0 ? c[0] : c[SHARE ? 0 : 1]; }
-};
-
-// Which of the 32 slots from `key` on a row of drafted token i attends, as bits.
-__device__ __forceinline__ uint32_t allowed32(const TreeArgs& a, const uint8_t* mask, SeqLen s, int i,
-                                              int key) {
-  const int ctx = s.len - key;                 // of them in the context
-  if (ctx >= 32) return 0xffffffffu;
-  uint32_t bits = ctx > 0 ? (1u << ctx) - 1u : 0u;
-  if (key >= s.len + s.n) return bits;
-#pragma unroll
-  for (int c = 0; c < 32; ++c) {
-    const int j = c - ctx;
-    const bool in = j >= 0 && j < s.n;
-    if (in && tree_allows(mask, a.T, i, j)) bits |= 1u << c;
-  }
-  return bits;
+// Byte offset of 16-byte chunk `ch` (of D/8) of row `r` in a 16-bit tile of ROWS rows.
+template <int ROWS>
+__device__ __forceinline__ uint32_t tile_off(int r, int ch) {
+  return (ch >> 3) * (ROWS * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
 }
 
 // Does drafted token i of a sequence attend slot `key`?
@@ -240,6 +196,8 @@ __global__ void __launch_bounds__(kTThreads<E4M3>, 1)
                  const __grid_constant__ TreeArgs a, int rows_unit) {
   using C = TilesCfg<D, E4M3>;
   using Smem = TilesSmem<D, E4M3>;
+  constexpr int kRing = SHARE ? C::kBufs / 2 : C::kBufs / 4;     // buffers of a ring
+  constexpr int kGroup = !E4M3 ? 1 : (SHARE ? 4 : 2);            // loader warps of a ring
   constexpr bool BF = QBF && !E4M3;              // type of the MMA operands
   // log2 of how far P may exceed 1 before the reference moves: fp16 ends at 2^16; a bf16 P of
   // 2^40 leaves its sums and O (fp32) far from their end
@@ -253,195 +211,177 @@ __global__ void __launch_bounds__(kTThreads<E4M3>, 1)
   volatile int* abort_flag = &sm.abort_flag;
   if (tid == 0) {
     for (int i = 0; i < C::kBufs; ++i) {
-      mbar_init(&sm.full[i], 4);
-      mbar_init(&sm.empty[i], 1);
+      mbar_init(&sm.full[i], kGroup + (E4M3 && !((i / kRing) & 1) ? 1 : 0));
+      mbar_init(&sm.empty[i], SHARE ? 2 : 1);
       mbar_init(&sm.tail[i], 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sm.q_full[s], 8);
-      mbar_init(&sm.s_full[s], 2);
-      mbar_init(&sm.p_full[s], 8);
-      mbar_init(&sm.o_done[s], 1);
+      for (int p = 0; p < 2; ++p) {
+        mbar_init(&sm.s_full[s][p], 2);
+        mbar_init(&sm.p_full[s][p], 8);
+        mbar_init(&sm.o_done[s][p], 1);
+      }
     }
-    mbar_init(&sm.drain, 1);
+    mbar_init(&sm.drain[0], 1);
+    mbar_init(&sm.drain[1], 1);
     sm.abort_flag = 0;
     sm.bad_v = 0;
+    sm.progress[0] = sm.progress[1] = 0;
     fence_mbar_init();
   }
   if (warp == kMma) {
     tmem_alloc(&sm.tmem, 512);
     tmem_relinquish();
   }
-  const int vgrid = SHARE ? gridDim.x : 2 * gridDim.x;
-  find_run(a, kTT, pairs, vgrid, SHARE ? blockIdx.x : 2 * blockIdx.x, 1, &sm.run[0], sm.scratch);
-  if (!SHARE) find_run(a, kTT, pairs, vgrid, 2 * blockIdx.x + 1, 1, &sm.run[1], sm.scratch);
+  // slot and ring of this warp
+  const int ring = warp < 16 ? 0 : (warp < kMma ? (warp - 16) / kGroup : (warp - kMma) * 2);
+  const int slot = warp < 16 ? warp >> 3 : (SHARE && warp < kMma ? 0 : ring >> 1);
+  auto run_of_slot = [&](int s) {
+    return warp_run(a, kTK, pairs, SHARE ? gridDim.x : 2 * gridDim.x, SHARE ? blockIdx.x : 2 * blockIdx.x + s, 1);
+  };
+  const Run run = run_of_slot(slot & 1);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
-  const Run& run0 = sm.run[0];
-  const Run& run1 = sm.run[SHARE ? 0 : 1];
 
-  // registers at launch and by role: 768 x 80 = 512 x 96 + 128 x 48 + 128 x 48, and with
-  // e4m3, whose loaders hold a tile, 896 x 72 = 512 x 80 + 256 x 72 + 128 x 40
-  constexpr int kRegSoft = E4M3 ? 80 : 96, kRegMma = E4M3 ? 40 : 48;
+  // registers at launch and by role: 768 x 80 = 512 x 88 + 128 x 64 + 128 x 64, and with e4m3
+  // 896 x 72 = 512 x 80 + 256 x 72 + 128 x 40
+  constexpr int kRegSoft = E4M3 ? 80 : 88, kRegMma = E4M3 ? 40 : 64;
   if (warp >= 16 && warp < 16 + kTLoad<E4M3>) {
     // ------------------------------------------------------------ loaders
-    if (!E4M3) setmaxnreg_dec<48>();
-    Walk<SHARE> w;
-    w.start(a, sm.run);
-    const int lw = (warp - 16) & 3, lgroup = (warp - 16) >> 2;
+    if (!E4M3) setmaxnreg_dec<64>();
+    // One ring of tiles each: (slot 0:) K, V, !SHARE: of slot 1 as well.
+    const bool v = ring & 1;
+    const int n = ring < (SHARE ? 2 : 4) ? run.n : 0, base = ring * kRing;
+    Cursor at;
+    if (n > 0) at.start(run, kTK);
+    // lane j: the page of the slots from key0 + j * (at most 16) on; -1 behind the last key
+    const int chunk = E4M3 ? 16 : min(kTK, 1 << a.c.page_shift);
+    auto page_of = [&]() {
+      const int key = at.tile * kTK + lane * chunk;
+      return lane * chunk < kTK && key < at.s.len + at.s.n
+                 ? __ldg(a.table + (size_t)at.b * a.MP + (key >> a.c.page_shift))
+                 : -1;
+    };
+    int page = n > 0 ? page_of() : -1;
     bool ok = true;
     if (!E4M3) {
-      int e = 0;
       unsigned tails = 0;          // parity of the next phase of each buffer's tail barrier
-      for (; w.more; w.step(a, pairs), ++e) {
-        const Cursor c = w.cur();
-        const int buf = e % C::kBufs;
-        if (e >= C::kBufs && !mbar_wait_warp(&sm.empty[buf], (e / C::kBufs - 1) & 1, abort_flag)) {
+      int t = 0;
+      for (; t < n; ++t) {
+        const int buf = base + t % kRing;
+        const int key0 = at.tile * kTK, len = at.s.len, L = len + at.s.n, h = at.pair / a.RT;
+        const bool starts = t == 0 || at.tile == 0, edge = v && key0 + kTK > len;
+        const bool in = lane * chunk < kTK && key0 + lane * chunk < L;
+        int pg = page;
+        if (in && !page_inside(pg, a.c.pages)) {
+          atomicOr(&g_device_error, DEVERR_BOUNDS);
+          pg = 0;           // any rows: the outputs are not meaningful
+        }
+        if (t + 1 < n) {
+          at.next(a, pairs, kTK);
+          page = page_of();
+        }
+        if (t >= kRing && !mbar_wait_warp(&sm.empty[buf], (t / kRing - 1) & 1, abort_flag)) {
           ok = false;
           break;
         }
-        const int key0 = c.tile * kTT, L = c.s.len + c.s.n, h = c.pair / a.RT;
-        const bool edge = w.v && key0 + kTT > c.s.len;
         uint64_t* bar = edge ? &sm.tail[buf] : &sm.full[buf];
         uint8_t* dst = sm.kv[buf];
-        if (lw == 0) {
-          // lane p: page chunk p of the tile (the pages of rows behind the last key are not read)
-          const int prow = 1 << a.c.page_shift, chunk = key0 + lane * prow;
-          const bool in = lane * prow < kTT && chunk < L;
-          int page = -1;
-          if (in) {
-            page = __ldg(a.table + (size_t)c.b * a.MP + (chunk >> a.c.page_shift));
-            if (!page_inside(page, a.c.pages)) {
-              atomicOr(&g_device_error, DEVERR_BOUNDS);
-              page = 0;     // any rows: the outputs are not meaningful
-            }
-          }
-          const int n = __popc(__ballot_sync(0xffffffffu, in));
-          if (lane == 0) mbar_expect_tx(bar, n * prow * D * 2);
-          __syncwarp();
-          if (in) {
-            const int row = (int)row_of(page, a.c.Hkv, h, a.c.page_shift, chunk);
+        const int cnt = __popc(__ballot_sync(0xffffffffu, in));
+        if (lane == 0) {
+          if (!v) sm.starts[buf] = starts;
+          mbar_expect_tx(bar, cnt * chunk * D * 2);
+        }
+        __syncwarp();
+        if (in) {
+          const int row = (int)row_of(pg, a.c.Hkv, h, a.c.page_shift, key0 + lane * chunk);
 #pragma unroll
-            for (int x = 0; x < C::kBlk; ++x)
-              tma_load_2d(dst + x * kTT * 128 + lane * prow * 128, w.v ? &tm_v : &tm_k, bar, x * 64, row);
-          }
+          for (int x = 0; x < C::kBlk; ++x)
+            tma_load_2d(dst + x * kTK * 128 + lane * chunk * 128, v ? &tm_v : &tm_k, bar, x * 64, row);
         }
         if (edge) {
           // rows behind the last key and drafted rows that are not finite become zeros
-          if (!mbar_wait_warp(&sm.tail[buf], (tails >> buf) & 1, abort_flag)) {
+          if (!mbar_wait_warp(&sm.tail[buf], (tails >> (t % kRing)) & 1, abort_flag)) {
             ok = false;
             break;
           }
-          tails ^= 1u << buf;
-          const int r = tid - 16 * 32;
-          if (key0 + r >= c.s.len) {
+          tails ^= 1u << (t % kRing);
+          for (int r = lane; r < kTK; r += 32) {
+            if (key0 + r < len) continue;
             bool zero = key0 + r >= L;
             if (!zero) {
 #pragma unroll
               for (int ch = 0; ch < D / 8; ++ch)
-                zero = not_finite16<false, QBF>(*reinterpret_cast<const uint4*>(dst + tile_off(r, ch))) || zero;
+                zero = not_finite16<false, QBF>(*reinterpret_cast<const uint4*>(dst + tile_off<kTK>(r, ch))) || zero;
               if (zero) sm.bad_v = 1;
             }
             if (zero)
               for (int ch = 0; ch < D / 8; ++ch)
-                *reinterpret_cast<uint4*>(dst + tile_off(r, ch)) = make_uint4(0u, 0u, 0u, 0u);
+                *reinterpret_cast<uint4*>(dst + tile_off<kTK>(r, ch)) = make_uint4(0u, 0u, 0u, 0u);
           }
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.full[buf]);
-        } else if (lw != 0 && lane == 0) {
-          mbar_arrive(&sm.full[buf]);
         }
       }
-      if (!ok && lw == 0) {
+      if (!ok) {
         // let the copies already issued land before the block exits
-        for (int u = e > C::kBufs ? e - C::kBufs : 0; u < e; ++u)
-          mbar_wait(&sm.full[u % C::kBufs], (u / C::kBufs) & 1, nullptr);
+        for (int u = t > kRing ? t - kRing : 0; u < t; ++u)
+          mbar_wait(&sm.full[base + u % kRing], (u / kRing) & 1, nullptr);
       }
     } else {
-      constexpr int LPR = D / 16, RPP = 128 / LPR, NP = kTT / RPP;   // lanes of a row, rows of a pass
-      const int lt = (tid - 16 * 32) & 127, lr = lt / LPR, lc = lt % LPR;
-      struct Ahead {
-        uint4 u[NP];
-        float ks, vs;
-        int key0, len, n, t, s;
-        bool v, there;
+      // in units of NU passes over the tile's rows (LPR lanes a row): one unit is on its way while
+      // the one before it is stored
+      constexpr int LPR = D / 16, RPP = 32 * kGroup / LPR, NP = kTK / RPP, NU = NP < 4 ? NP : 4;
+      constexpr int kUnits = NP / NU;
+      const int lt = (tid - 16 * 32) % (32 * kGroup), lr = lt / LPR, lc = lt % LPR;
+      const uint8_t* pool = v ? a.c.v : a.c.k;
+      struct Unit {
+        uint4 u[NU];
+        int first, last;           // rows of the tile from which on they are drafted ones, none
+        bool starts;
       };
-      auto fetch = [&](Ahead& x) {
-        x.there = w.more;
-        if (!w.more) return;
-        const Cursor c = w.cur();
-        x.v = w.v;
-        x.s = w.s;
-        x.t = w.s ? w.t[1] : w.t[0];
-        x.key0 = c.tile * kTT;
-        x.len = c.s.len;
-        x.n = c.s.n;
-        const int h = c.pair / a.RT, L = c.s.len + c.s.n;
-        const int* tab = a.table + (size_t)c.b * a.MP;
-        const uint8_t* pool = w.v ? a.c.v : a.c.k;
-        int pg[NP];
-#pragma unroll
-        for (int p = 0; p < NP; ++p) {
-          const int key = x.key0 + p * RPP + lr;
-          pg[p] = key < L ? __ldg(tab + (key >> a.c.page_shift)) : -1;
-        }
-        int spg = -1;
-        const int skey = x.key0 + lt;
-        if (!w.v && skey < L) spg = __ldg(tab + (skey >> a.c.page_shift));
-#pragma unroll
-        for (int p = 0; p < NP; ++p) {
-          const int key = x.key0 + p * RPP + lr;
-          x.u[p] = make_uint4(0u, 0u, 0u, 0u);
-          if (key < L) {
-            if (page_inside(pg[p], a.c.pages)) {
-              const long long row = row_of(pg[p], a.c.Hkv, h, a.c.page_shift, key);
-              x.u[p] = __ldg(reinterpret_cast<const uint4*>(pool + row * D) + lc);
-            } else {
+      int at_t = 0, row16 = -1;    // lane j: row of slot 16 j of the tile
+      auto fetch = [&](Unit& x, int sub) {
+        if (at_t >= n) return;
+        const int key0 = at.tile * kTK, L = at.s.len + at.s.n;
+        if (sub == 0) {
+          row16 = -1;
+          if (lane < kTK / 16 && key0 + 16 * lane < L) {
+            if (page_inside(page, a.c.pages))
+              row16 = (int)row_of(page, a.c.Hkv, at.pair / a.RT, a.c.page_shift, key0 + 16 * lane);
+            else
               atomicOr(&g_device_error, DEVERR_BOUNDS);
-            }
           }
         }
-        x.ks = x.vs = 0.f;
-        if (!w.v && page_inside(spg, a.c.pages)) {
-          const long long row = row_of(spg, a.c.Hkv, h, a.c.page_shift, skey);
-          x.ks = __ldg(a.c.ks + row);
-          x.vs = __ldg(a.c.vs + row);
-        }
-        w.step(a, pairs);
-      };
-      auto put = [&](Ahead& x, int e) -> bool {
-        const int buf = e % C::kBufs;
-        if (e >= C::kBufs && !mbar_wait_warp(&sm.empty[buf], (e / C::kBufs - 1) & 1, abort_flag)) return false;
-        uint8_t* dst = sm.kv[buf];
-        const bool edge = x.key0 + kTT > x.len;
-        if (!x.v) {
-          // the scales of both; slot x.t % kTScales was last read kTScales tiles ago, and a
-          // V tile later than that one has been freed
-          float ks = x.ks, vs = x.vs;
-          if (x.key0 + lt >= x.len) {
-            // masked scores are -inf before the key scale multiplies them, and P is 0 before the
-            // value scale does: the scales of drafted rows become finite, a key's not 0 (a row of
-            // scale 0 has codes 0), those behind the last key are 0
-            if (!(fabsf(vs) < INFINITY) || !(fabsf(ks) < INFINITY)) {
-              if (!(fabsf(vs) < INFINITY)) vs = 0.f;
-              if (!(fabsf(ks) < INFINITY)) ks = 1.f;
-              sm.bad_v = 1;
-            }
-            if (ks == 0.f) ks = 1.f;
-          }
-          float* sc = sm.scl[x.s][x.t % kTScales] + 4 * (lt >> 1) + (lt & 1);
-          sc[0] = ks;
-          sc[2] = vs;
-        }
+        x.first = at.s.len - key0;
+        x.last = L - key0;
+        x.starts = at_t == 0 || at.tile == 0;
 #pragma unroll
-        for (int p = 0; p < NP; ++p) {
-          const int r = p * RPP + lr;
-          if (x.v && edge) {
-            const bool dr = x.key0 + r >= x.len;
-            unsigned bad = dr && not_finite16<true, false>(x.u[p]) ? 1u : 0u;
+        for (int p = 0; p < NU; ++p) {
+          const int r = (sub * NU + p) * RPP + lr, row = __shfl_sync(0xffffffffu, row16, r >> 4);
+          x.u[p] = make_uint4(0u, 0u, 0u, 0u);
+          if (row >= 0 && r < x.last)
+            x.u[p] = __ldg(reinterpret_cast<const uint4*>(pool + (size_t)(row + (r & 15)) * D) + lc);
+        }
+        if (sub == kUnits - 1 && ++at_t < n) {
+          at.next(a, pairs, kTK);
+          page = page_of();
+        }
+      };
+      auto put = [&](Unit& x, int t, int sub) -> bool {
+        const int buf = base + t % kRing;
+        if (sub == 0 && t >= kRing && !mbar_wait_warp(&sm.empty[buf], (t / kRing - 1) & 1, abort_flag)) return false;
+        uint8_t* dst = sm.kv[buf];
+        if (sub == 0 && !v && lt == 0) sm.starts[buf] = x.starts;
+#pragma unroll
+        for (int p = 0; p < NU; ++p) {
+          const int r = (sub * NU + p) * RPP + lr;
+          if (v && x.first < kTK) {
+            unsigned bad = r >= x.first && not_finite16<true, false>(x.u[p]) ? 1u : 0u;
 #pragma unroll
             for (int o = LPR / 2; o; o >>= 1) bad |= __shfl_xor_sync(0xffffffffu, bad, o);
             if (bad) {
@@ -449,143 +389,217 @@ __global__ void __launch_bounds__(kTThreads<E4M3>, 1)
               sm.bad_v = 1;
             }
           }
-          const uint32_t cw[4] = {x.u[p].x, x.u[p].y, x.u[p].z, x.u[p].w};
           uint4 lo, hi;
-          lo.x = e4m3x2_f16x2(cw[0] & 0xffffu);
-          lo.y = e4m3x2_f16x2(cw[0] >> 16);
-          lo.z = e4m3x2_f16x2(cw[1] & 0xffffu);
-          lo.w = e4m3x2_f16x2(cw[1] >> 16);
-          hi.x = e4m3x2_f16x2(cw[2] & 0xffffu);
-          hi.y = e4m3x2_f16x2(cw[2] >> 16);
-          hi.z = e4m3x2_f16x2(cw[3] & 0xffffu);
-          hi.w = e4m3x2_f16x2(cw[3] >> 16);
+          widen4(x.u[p].x, lo.x, lo.y);
+          widen4(x.u[p].y, lo.z, lo.w);
+          widen4(x.u[p].z, hi.x, hi.y);
+          widen4(x.u[p].w, hi.z, hi.w);
           // the two halves of a row store different chunks at a time: no bank conflicts
           const bool sw = D == 128 && (lc >> 2);
-          *reinterpret_cast<uint4*>(dst + tile_off(r, 2 * lc + (sw ? 1 : 0))) = sw ? hi : lo;
-          *reinterpret_cast<uint4*>(dst + tile_off(r, 2 * lc + (sw ? 0 : 1))) = sw ? lo : hi;
+          *reinterpret_cast<uint4*>(dst + tile_off<kTK>(r, 2 * lc + (sw ? 1 : 0))) = sw ? hi : lo;
+          *reinterpret_cast<uint4*>(dst + tile_off<kTK>(r, 2 * lc + (sw ? 0 : 1))) = sw ? lo : hi;
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.full[buf]);
+        if (sub == kUnits - 1) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.full[buf]);
+          if (v && lt == 0) *static_cast<volatile int*>(&sm.progress[slot]) = t;
+        }
         return true;
       };
-      // the two groups take every other tile: one loads while the other stores
-      if (lgroup && w.more) w.step(a, pairs);
-      int e = lgroup;
-      Ahead x;
-      for (fetch(x); x.there; fetch(x)) {
-        if (!put(x, e)) break;
-        e += 2;
-        if (w.more) w.step(a, pairs);
+      Unit x0, x1;
+      fetch(x0, 0);
+      if (kUnits == 1) {
+        for (int t = 0; t < n; t += 2) {
+          fetch(x1, 0);
+          if (!put(x0, t, 0)) break;
+          if (t + 1 == n) break;
+          fetch(x0, 0);
+          if (!put(x1, t + 1, 0)) break;
+        }
+      } else {
+        for (int t = 0; t < n; ++t) {
+          fetch(x1, 1);
+          if (!put(x0, t, 0)) break;
+          fetch(x0, 0);
+          if (!put(x1, t, kUnits - 1)) break;
+        }
       }
     }
   } else if (warp >= 16) {
     // ------------------------------------------------------------ MMA issuer
     setmaxnreg_dec<kRegMma>();
-    if (warp == kMma && lane == 0) {
-      constexpr uint32_t idesc_s = idesc_f16_f32(kTT, kTT, BF);
-      constexpr uint32_t idesc_o = idesc_f16_f32(kTT, D, BF) | (1u << 16);   // B is [k][n]
-      const uint64_t dq = smem_desc_kmajor(sm.q[0], 128);
-      const uint64_t dk = smem_desc_kmajor(sm.kv[0], 128);
-      const uint64_t dv = smem_desc_nmajor(sm.kv[0], kTT * 128);
+    if (warp < kMma + 2) {
+      // One warp a slot.  The whole warp walks the tiles with values that the compiler knows to be
+      // alike in all lanes (shuffled from lane 0), so that descriptors and addresses live in
+      // uniform registers, and one elected lane issues.  This warp's instructions are
+      // on the path of every tile: what it would have to work out (which tile starts a piece)
+      // comes with the tile.
+      constexpr uint32_t idesc_s = idesc_f16_f32(kTR, kTK, BF);
+      constexpr uint32_t idesc_o = idesc_f16_f32(kTR, D, BF) | (1u << 16);   // B is [k][n]
       constexpr uint32_t kBuf16 = C::kTileBytes >> 4;
-      int nt[2] = {(int)(run0.t1 - run0.t0), (int)(run1.t1 - run1.t0)};
-      // tiles of the slot's piece from the current one on; a piece's first tile is next
-      int left0 = 0, left1 = 0;
-      bool new0 = true, new1 = true;
-      if (nt[0] > 0) {
-        sm.mma_at[0].start(a, run0, kTT);
-        left0 = sm.mma_at[0].tiles - sm.mma_at[0].tile;
-      }
-      if (nt[1] > 0) {
-        sm.mma_at[1].start(a, run1, kTT);
-        left1 = sm.mma_at[1].tiles - sm.mma_at[1].tile;
-      }
-      int e = 0;                   // buffers taken
-      int pieces = 0;              // parity of each slot's piece
+      const int s = uniform(warp - kMma);
+      const int kb0 = (SHARE ? 0 : 2 * s) * kRing, vb0 = kb0 + kRing;      // the rings' first buffers
+      const uint64_t dk0 = smem_desc_kmajor(sm.kv[kb0], 128);
+      const uint64_t dv0 = smem_desc_nmajor(sm.kv[vb0], kTK * 128);
+      const uint32_t k_hi = uniform((uint32_t)(dk0 >> 32)), k_lo = uniform((uint32_t)dk0);
+      const uint32_t v_hi = uniform((uint32_t)(dv0 >> 32)), v_lo = uniform((uint32_t)dv0);
+      const uint32_t q_lo = uniform((uint32_t)smem_desc_kmajor(sm.q[s], 128));
+      const uint32_t tm = uniform(tmem) + s * 128, to = uniform(tmem) + 256 + s * 128;
+      const bool leader = elect_one();
+      const int n = uniform(run.n);
+      int first = 0;               // bit p: the last tile of parity p starts a piece
+      int q_ph = 0;
+      // S of tile k, whose K has landed
+      auto scores = [&](int k, int buf, int start) -> bool {
+        const int p = k & 1;
+        if (start) {
+          if (!mbar_wait_warp(&sm.q_full[s], q_ph, abort_flag)) return false;
+          q_ph ^= 1;
+        }
+        first = (first & ~(1 << p)) | (start << p);
+        tc_fence_after();
+        const uint32_t kb = k_lo + buf * kBuf16;
+        if (leader) {
+          mbar_arrive(&sm.s_full[s][p]);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_f16_ss(tm + p * 64, desc_of(q_lo + (kk >> 2) * ((kTR * 128) >> 4) + (kk & 3) * 2, k_hi),
+                       desc_of(kb + (kk >> 2) * ((kTK * 128) >> 4) + (kk & 3) * 2, k_hi), idesc_s, kk > 0);
+          tc_commit(&sm.s_full[s][p]);
+          tc_commit(&sm.empty[kb0 + buf]);
+        }
+        __syncwarp();
+        return true;
+      };
+      // S(t+2) follows P V of t, whose P it overwrites.  A tile that starts a piece waits until every
+      // P V of the piece before is issued (its Q is loaded after that piece's softmax), the ones
+      // behind it wait for it.
+      int ns = 0;
       bool ok = true;
-      auto wait_full = [&](int u) {
-        return mbar_wait(&sm.full[u % C::kBufs], (u / C::kBufs) & 1, abort_flag);
-      };
-      // S of slot s; entry u; `first`: a piece starts with this tile
-      auto scores = [&](int s, int u, bool first, bool release) -> bool {
-        if (first) {
-          if (!mbar_wait(&sm.q_full[s], (pieces >> s) & 1, abort_flag)) return false;
-          pieces ^= 1 << s;
-        }
-        if (!wait_full(u)) return false;
-        mbar_arrive(&sm.s_full[s]);
-        tc_fence_after();
-        const uint64_t qb = dq + s * kBuf16, kb = dk + (u % C::kBufs) * kBuf16;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * ((kTT * 128) >> 4) + (kk & 3) * 2;
-          mma_f16_ss(tmem + s * 128, qb + off, kb + off, idesc_s, kk > 0);
-        }
-        tc_commit(&sm.s_full[s]);
-        if (release) tc_commit(&sm.empty[u % C::kBufs]);
-        return true;
-      };
-      auto values = [&](int s, int t, int u, bool first, bool release) -> bool {
-        if (!mbar_wait(&sm.p_full[s], t & 1, abort_flag)) return false;
-        if (!wait_full(u)) return false;
-        tc_fence_after();
-        const uint64_t vb = dv + (u % C::kBufs) * kBuf16;
-#pragma unroll
-        for (int kk = 0; kk < kTT / 16; ++kk)
-          mma_f16_ts(tmem + 256 + s * 128, tmem + s * 128 + 8 * kk, vb + kk * (16 * 128 >> 4), idesc_o,
-                     !first || kk > 0);
-        tc_commit(&sm.o_done[s]);
-        if (release) tc_commit(&sm.empty[u % C::kBufs]);
-        return true;
-      };
-      // prologue: the first S of both slots
-      if (SHARE) {
-        if (nt[0] > 0) {
-          ok = scores(0, 0, true, false) && scores(1, 0, true, true);
-          e = 1;
-        }
-      } else {
-        if (nt[0] > 0) ok = scores(0, e++, true, true);
-        if (ok && nt[1] > 0) ok = scores(1, e++, true, true);
-      }
-      const int nt0 = nt[0], nt1 = nt[1];
 #pragma unroll 1
-      for (int ts = 0; ok && ts < 2 * nt0; ++ts) {
-        const int t = ts >> 1, s = ts & 1, n = s ? nt1 : nt0;
-        if (t >= n) continue;
-        int left = s ? left1 : left0;
-        bool fresh = s ? new1 : new0;
-        const int u = SHARE ? 2 * t + 1 : e;       // this V; K of the next tile is u + 1
-        const bool more = t + 1 < n;
-        const bool rel = SHARE ? s == 1 : true;
-        ok = values(s, t, u, fresh, rel);
-        fresh = false;
-        if (ok && more) {
-          if (--left == 0) {
-            Cursor c = sm.mma_at[s];
-            c.tile = c.tiles - 1;
-            c.next(a, pairs, kTT);
-            sm.mma_at[s] = c;
-            left = c.tiles;
-            fresh = true;
+      for (int t = -1; ok && t < n; ++t) {
+        if (t >= 0) {
+          const int p = t & 1, buf = t % kRing;
+          if (!mbar_wait_warp(&sm.p_full[s][p], (t >> 1) & 1, abort_flag) ||
+              !mbar_wait_warp(&sm.full[vb0 + buf], (t / kRing) & 1, abort_flag))
+            break;
+          tc_fence_after();
+          const uint32_t vb = v_lo + buf * kBuf16, keep = ((first >> p) & 1) ^ 1;
+          if (leader) {
+#pragma unroll
+            for (int kk = 0; kk < kTK / 16; ++kk)
+              mma_f16_ts(to, tm + p * 64 + 8 * kk, desc_of(vb + kk * (16 * 128 >> 4), v_hi), idesc_o,
+                         kk > 0 ? 1u : keep);
+            tc_commit(&sm.o_done[s][p]);
+            tc_commit(&sm.empty[vb0 + buf]);
           }
-          ok = scores(s, u + 1, fresh, rel);
+          __syncwarp();
         }
-        if (s) {
-          left1 = left;
-          new1 = fresh;
-        } else {
-          left0 = left;
-          new0 = fresh;
+#pragma unroll 1
+        while (ns < n && ns <= t + 2) {
+          const int buf = ns % kRing;
+          if (!mbar_wait_warp(&sm.full[kb0 + buf], (ns / kRing) & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          const int start = uniform(sm.starts[kb0 + buf]);
+          if (start && ns != t + 1) break;
+          if (!scores(ns, buf, start)) {
+            ok = false;
+            break;
+          }
+          ++ns;
         }
-        if (!SHARE) e += more ? 2 : 1;
       }
       // every MMA issued so far completes before the block frees TMEM
-      tc_commit(&sm.drain);
-      mbar_wait(&sm.drain, 0, nullptr);
+      if (leader) tc_commit(&sm.drain[s]);
+      __syncwarp();
+      mbar_wait_warp(&sm.drain[s], 0, nullptr);
+    } else if (E4M3 && warp == kMma + 2) {
+      // the rows of the tiles ahead, to L2: a 128-byte line (D = 64: half of one) a row
+      const Run r0 = run_of_slot(0), r1 = SHARE ? r0 : run_of_slot(1);
+      Cursor c0, c1;
+      if (r0.n > 0) c0.start(r0, kTK);
+      if (!SHARE && r1.n > 0) c1.start(r1, kTK);
+      for (int t = 0; t < max(r0.n, r1.n); ++t) {
+#pragma unroll
+        for (int s = 0; s < (SHARE ? 1 : 2); ++s) {
+          if (t >= (s ? r1.n : r0.n)) continue;
+          Cursor& c = s ? c1 : c0;
+          // no further ahead of the loaders than kTAhead tiles (a bounded wait: running ahead is no fault)
+          for (int x = 0; x < 100000 && !*abort_flag; ++x) {
+            if (*static_cast<volatile int*>(&sm.progress[s]) + kTAhead >= t) break;
+            __nanosleep(100);
+          }
+          __syncwarp();
+          const int L = c.s.len + c.s.n, h = c.pair / a.RT;
+#pragma unroll
+          for (int x = 0; x < kTK; x += 32) {
+            const int key = c.tile * kTK + x + lane;
+            const int page = key < L ? __ldg(a.table + (size_t)c.b * a.MP + (key >> a.c.page_shift)) : -1;
+            if (page_inside(page, a.c.pages)) {
+              const long long row = row_of(page, a.c.Hkv, h, a.c.page_shift, key);
+              prefetch_l2(a.c.k + row * D);
+              prefetch_l2(a.c.v + row * D);
+            }
+          }
+          if (t + 1 < (s ? r1.n : r0.n)) c.next(a, pairs, kTK);
+        }
+      }
+    } else if (E4M3 && warp == kMma + 3) {
+      // the scales, two keys a lane
+      const Run r0 = run_of_slot(0), r1 = SHARE ? r0 : run_of_slot(1);
+      Cursor c0, c1;
+      if (r0.n > 0) c0.start(r0, kTK);
+      if (!SHARE && r1.n > 0) c1.start(r1, kTK);
+      bool go = true;
+      for (int t = 0; go && t < max(r0.n, r1.n); ++t) {
+#pragma unroll
+        for (int s = 0; s < (SHARE ? 1 : 2); ++s) {
+          if (!go || t >= (s ? r1.n : r0.n)) continue;
+          Cursor& c = s ? c1 : c0;
+          const int key = c.tile * kTK + 2 * lane, len = c.s.len, L = len + c.s.n, buf = 2 * s * kRing + t % kRing;
+          float2 ks = make_float2(0.f, 0.f), vs = ks;
+          if (key < L) {
+            const int page = __ldg(a.table + (size_t)c.b * a.MP + (key >> a.c.page_shift));
+            if (page_inside(page, a.c.pages)) {
+              const long long row = row_of(page, a.c.Hkv, c.pair / a.RT, a.c.page_shift, key);
+              ks = __ldg(reinterpret_cast<const float2*>(a.c.ks + row));
+              vs = __ldg(reinterpret_cast<const float2*>(a.c.vs + row));
+            }
+          }
+          // masked scores are -inf before the key scale multiplies them, and P is 0 before the value
+          // scale does: the scales of drafted rows become finite, a key's not 0 (a row of scale 0
+          // has codes 0); those behind the last key are 1 and 0
+          auto clean = [&](float x, bool is_key, int k) {
+            if (k < len) return x;
+            if (k >= L) x = 0.f;
+            if (!(fabsf(x) < INFINITY)) {
+              x = 0.f;
+              sm.bad_v = 1;
+            }
+            return is_key && x == 0.f ? 1.f : x;
+          };
+          ks.x = clean(ks.x, true, key);
+          ks.y = clean(ks.y, true, key + 1);
+          vs.x = clean(vs.x, false, key);
+          vs.y = clean(vs.y, false, key + 1);
+          float m = fmaxf(vs.x, vs.y);
+#pragma unroll
+          for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+          if (t + 1 < (s ? r1.n : r0.n)) c.next(a, pairs, kTK);
+          if (t >= kRing && !mbar_wait_warp(&sm.empty[buf], (t / kRing - 1) & 1, abort_flag)) {
+            go = false;
+            continue;
+          }
+          *reinterpret_cast<float4*>(sm.scl[s][t % C::kScales] + 4 * lane) = make_float4(ks.x, ks.y, vs.x, vs.y);
+          if (lane == 0) sm.lv[s][t % C::kScales] = log2f(fmaxf(m, kVrefLeast));
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.full[buf]);
+        }
+      }
     }
-    __syncwarp();
   } else {
     // ------------------------------------------------------------ softmax
     // Eight warps a slot.  The .16x256b loads give a warp 16 TMEM lanes and each of its
@@ -594,15 +608,14 @@ __global__ void __launch_bounds__(kTThreads<E4M3>, 1)
     // spread evenly over the schedulers.
     setmaxnreg_inc<kRegSoft>();
     const int s = warp >> 3, quad = warp & 3, hf = (warp >> 2) & 1, g = lane & 3;
-    const int lo = (SHARE ? s * kTT : 0) + 64 * hf + 16 * quad + (lane >> 2);   // of the unit's rows: lo, lo + 8
+    const int lo = (SHARE ? s * kTR : 0) + 64 * hf + 16 * quad + (lane >> 2);   // of the unit's rows: lo, lo + 8
     const int ml = 32 * quad + 16 * hf + (lane >> 2);                           // TMEM lane: ml, ml + 8
-    const Run& run = s ? run1 : run0;
-    const int nt = (int)(run.t1 - run.t0);
+    const int nt = run.n;
     const uint32_t lanes = static_cast<uint32_t>(32 * quad + 16 * hf) << 16;
-    const uint32_t tS = tmem + lanes + s * 128, tO = tmem + lanes + 256 + s * 128;
+    const uint32_t tO = tmem + lanes + 256 + s * 128;
     const float kL2E = 1.4426950408889634f;
     Cursor at;
-    if (nt > 0) at.start(a, run, kTT);
+    if (nt > 0) at.start(run, kTK);
     bool ok = true;
     float ref[2], l[2], qs[2];
     int r[2];
@@ -613,18 +626,23 @@ __global__ void __launch_bounds__(kTThreads<E4M3>, 1)
         // a piece starts: the slot's rows of Q.  The last S of the piece before has been waited
         // for, so nothing reads the buffer.
         const int unit0 = (at.pair % a.RT) * rows_unit, h = at.pair / a.RT;
+        uint4 qu[2][D / 32];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           r[e] = lo + 8 * e < rows_unit ? min(unit0 + lo + 8 * e, R) : R;
-          qs[e] = a.sm_scale * kL2E;
-          ref[e] = -INFINITY;
-          l[e] = 0.f;
-          uint4 u[D / 32];
           const uint4* src = reinterpret_cast<const uint4*>(
               static_cast<const uint16_t*>(a.q) + at.b * a.sb + (long long)(h * a.G + r[e] / a.T) * a.sh +
               (long long)(r[e] % a.T) * a.st);
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) u[c] = r[e] < R ? __ldg(src + 4 * c + g) : make_uint4(0u, 0u, 0u, 0u);
+          for (int c = 0; c < D / 32; ++c)
+            qu[e][c] = r[e] < R ? __ldg(src + 4 * c + g) : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          uint4 (&u)[D / 32] = qu[e];
+          qs[e] = a.sm_scale * kL2E;
+          ref[e] = -INFINITY;
+          l[e] = 0.f;
           if (E4M3) {
             float amax = 0.f;
 #pragma unroll
@@ -656,36 +674,32 @@ __global__ void __launch_bounds__(kTThreads<E4M3>, 1)
           }
 #pragma unroll
           for (int c = 0; c < D / 32; ++c)
-            *reinterpret_cast<uint4*>(sm.q[s] + tile_off(ml + 8 * e, 4 * c + g)) = u[c];
+            *reinterpret_cast<uint4*>(sm.q[s] + tile_off<kTR>(ml + 8 * e, 4 * c + g)) = u[c];
         }
         active = __any_sync(0xffffffffu, r[0] < R);
         fence_proxy_async_smem();
         __syncwarp();
         mbar_arrive_lane0(&sm.q_full[s], lane);
       }
-      if (!mbar_wait_warp(&sm.s_full[s], t & 1, abort_flag)) {
+      if (!mbar_wait_warp(&sm.s_full[s][t & 1], (t >> 1) & 1, abort_flag)) {
         ok = false;
         break;
       }
       tc_fence_after();
-      const int key0 = at.tile * kTT;
+      const int key0 = at.tile * kTK;
+      const uint32_t tS = tmem + lanes + s * 128 + (t & 1) * 64;
       if (active) {
-        const float* sc = sm.scl[E4M3 && !SHARE ? s : 0][E4M3 ? t % kTScales : 0];
+        const float* sc = sm.scl[E4M3 && !SHARE ? s : 0][E4M3 ? t % C::kScales : 0];
         float lv = 0.f;
         if (E4M3) {
-          const float4 v0 = *reinterpret_cast<const float4*>(sc + 8 * lane);
-          const float4 v1 = *reinterpret_cast<const float4*>(sc + 8 * lane + 4);
-          float m = fmaxf(fmaxf(v0.z, v0.w), fmaxf(v1.z, v1.w));
-#pragma unroll
-          for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-          lv = log2f(fmaxf(m, kVrefLeast));
+          lv = sm.lv[SHARE ? 0 : s][t % C::kScales];
         }
-        if (key0 + kTT > at.s.len) {
+        if (key0 + kTK > at.s.len) {
           // scores that the mask or the length leaves out become -inf where they lie
           const uint8_t* mask = a.mask ? a.mask + at.b * a.mask_sb : nullptr;
           const int i0 = r[0] % a.T, i1 = r[1] % a.T;
 #pragma unroll 1
-          for (int c = 0; c < kTT; c += 32) {
+          for (int c = 0; c < kTK; c += 32) {
             uint32_t x[16];
             tmem_ld16x256_16(tS + c, x);
             tmem_ld_wait();
@@ -698,9 +712,7 @@ __global__ void __launch_bounds__(kTThreads<E4M3>, 1)
           }
           tmem_st_wait();
         }
-        // P of chunk c (64 keys, 32 columns) goes over scores that have been read
-#pragma unroll 1
-        for (int c = 0; c < 2; ++c) {
+        {
           uint32_t p[16];
           float2 sum[2];
           while (true) {
@@ -710,7 +722,7 @@ __global__ void __launch_bounds__(kTThreads<E4M3>, 1)
             float mx[2] = {-INFINITY, -INFINITY};
             sum[0] = sum[1] = make_float2(0.f, 0.f);
             uint32_t x[32];
-            tmem_ld16x256_32(tS + 64 * c, x);
+            tmem_ld16x256_32(tS, x);
             tmem_ld_wait();
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
@@ -719,7 +731,7 @@ __global__ void __launch_bounds__(kTThreads<E4M3>, 1)
               float4 f4;
               if (E4M3) {
                 // two key scales and two value scales
-                f4 = *reinterpret_cast<const float4*>(sc + 2 * (64 * c + 8 * k + 2 * g));
+                f4 = *reinterpret_cast<const float4*>(sc + 2 * (8 * k + 2 * g));
                 x0 = __fmul2_rn(x0, make_float2(f4.x, f4.y));
                 x1 = __fmul2_rn(x1, make_float2(f4.x, f4.y));
               }
@@ -742,8 +754,8 @@ __global__ void __launch_bounds__(kTThreads<E4M3>, 1)
             const bool over = (mx[0] > -INFINITY && mx[0] * qs[0] + lv > ref[0] + kGrow) ||
                               (mx[1] > -INFINITY && mx[1] * qs[1] + lv > ref[1] + kGrow);
             if (!__any_sync(0xffffffffu, over)) break;
-            // the references move to the largest scores so far: the sums, O (at rest once P V of the
-            // tile before is done) and the P of chunk 0 follow, and this chunk is done again
+            // the references move to the largest scores so far: the sums and O (at rest once P V of
+            // the tile before is done) follow, and the tile is done again
             float f[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -755,7 +767,7 @@ __global__ void __launch_bounds__(kTThreads<E4M3>, 1)
               l[e] *= f[e];
             }
             if (!first) {
-              if (!mbar_wait_warp(&sm.o_done[s], (t - 1) & 1, abort_flag)) {
+              if (!mbar_wait_warp(&sm.o_done[s][(t - 1) & 1], ((t - 1) >> 1) & 1, abort_flag)) {
                 ok = false;
                 break;
               }
@@ -771,33 +783,21 @@ __global__ void __launch_bounds__(kTThreads<E4M3>, 1)
               }
             }
             tmem_st_wait();
-            if (c == 1) {
-              uint32_t y[16];
-              tmem_ld16x128_16(tS, y);
-              tmem_ld_wait();
-#pragma unroll
-              for (int z = 0; z < 16; ++z) {
-                const float2 w2 = halves<BF>(y[z]);
-                y[z] = pack2<BF>(w2.x * f[z & 1], w2.y * f[z & 1]);
-              }
-              tmem_st16x128_16(tS, y);
-            }
           }
           if (!ok) break;
-          tmem_st16x128_16(tS + 32 * c, p);
+          tmem_st16x128_16(tS, p);
           l[0] += sum[0].x + sum[0].y;
           l[1] += sum[1].x + sum[1].y;
         }
-        if (!ok) break;
         tmem_st_wait();
       }
       tc_fence_before();
       __syncwarp();
-      mbar_arrive_lane0(&sm.p_full[s], lane);
+      mbar_arrive_lane0(&sm.p_full[s][t & 1], lane);
 
       if (at.tile + 1 == at.tiles || t + 1 == nt) {
         // ---- the piece ends
-        if (!mbar_wait_warp(&sm.o_done[s], t & 1, abort_flag)) {
+        if (!mbar_wait_warp(&sm.o_done[s][t & 1], (t >> 1) & 1, abort_flag)) {
           ok = false;
           break;
         }
@@ -848,7 +848,7 @@ __global__ void __launch_bounds__(kTThreads<E4M3>, 1)
           }
         }
       }
-      if (t + 1 < nt) at.next(a, pairs, kTT);
+      if (t + 1 < nt) at.next(a, pairs, kTK);
     }
   }
   tc_fence_before();
@@ -862,7 +862,7 @@ __global__ void __launch_bounds__(kTThreads<E4M3>, 1)
 template <int D, bool E4M3, bool QBF, bool SHARE>
 static cudaError_t launch_tiles(TreeArgs a, int dev, cudaMemPool_t pool, cudaStream_t st) {
   using C = TilesCfg<D, E4M3>;
-  const int R = a.G * a.T, most = SHARE ? 2 * kTT : kTT;
+  const int R = a.G * a.T, most = SHARE ? 2 * kTR : kTR;
   a.RT = (R + most - 1) / most;
   const int unit = (R + a.RT - 1) / a.RT;          // rows of a unit
   const int grid = sm_count(dev), vgrid = SHARE ? grid : 2 * grid;
@@ -872,7 +872,7 @@ static cudaError_t launch_tiles(TreeArgs a, int dev, cudaMemPool_t pool, cudaStr
     const uint64_t rows = (uint64_t)a.c.pages * a.c.Hkv << a.c.page_shift;
     const uint64_t dims[2] = {(uint64_t)D, rows};
     const uint64_t strides[1] = {(uint64_t)D * 2};
-    const uint32_t box[2] = {64, 1u << a.c.page_shift};
+    const uint32_t box[2] = {64, min(1u << a.c.page_shift, (unsigned)kTK)};
     e = make_tmap(&tk, a.c.k, 2, dims, strides, box, 2, 128);
     if (e == cudaSuccess) e = make_tmap(&tv, a.c.v, 2, dims, strides, box, 2, 128);
     if (e != cudaSuccess) return e;
@@ -891,7 +891,7 @@ static cudaError_t launch_tiles(TreeArgs a, int dev, cudaMemPool_t pool, cudaStr
     e = cudaGetLastError();
   }
   if (e == cudaSuccess) {
-    k_tree_join<D><<<dim3((R + 3) / 4, a.c.Hkv, a.B), 128, 0, st>>>(a, kTT, unit, vgrid, 1);
+    k_tree_join<D><<<dim3((R + 3) / 4, a.c.Hkv, a.B), 128, 0, st>>>(a, kTK, unit, vgrid, 1);
     e = cudaGetLastError();
   }
   const cudaError_t e2 = cudaFreeAsync(ws, st);

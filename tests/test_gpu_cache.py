@@ -110,6 +110,41 @@ def test_tree(qa, case, masked):
         check_tree(c, o, lse, want, odt)
 
 
+def attend_gpu(c, x):
+    """(o, lse, mag) as cache_ref.attend gives them, in 64 bits with torch on the GPU."""
+    B, Hq = c.B, c.Hkv * c.G
+    o = torch.zeros(B, Hq, c.T, c.d, dtype=torch.float64, device="cuda")
+    lse, mag = torch.full((B, Hq, c.T), -math.inf, dtype=torch.float64, device="cuda"), torch.zeros_like(o)
+    for b in range(B):
+        ln, n = c.lens[b], c.n[b]
+        bar = torch.zeros(n, ln + n, dtype=torch.float64, device="cuda")
+        bar[:, ln:][~x["mask"][b, :n, :n]] = -math.inf
+        for h in range(c.Hkv):
+            K, V = (c.dense(w, b, h, ln + n).cuda() for w in "kv")
+            for g in range(c.G):
+                s = x["q"][b, h * c.G + g, :n].double() @ K.T * c.sm + bar
+                z = torch.logsumexp(s, -1)
+                w = torch.exp(s - z[:, None])
+                o[b, h * c.G + g, :n], mag[b, h * c.G + g, :n] = w @ V, w @ V.abs()
+                lse[b, h * c.G + g, :n] = z
+    return o.cpu(), lse.cpu(), mag.cpu()
+
+
+@pytest.mark.parametrize("kv", ["same", "e4m3"])
+@pytest.mark.parametrize("T, G, d, dtype", [(1, 1, 128, "bf16"), (3, 7, 64, "fp16"), (9, 4, 128, "fp16"),
+                                            (33, 3, 64, "bf16"), (48, 4, 128, "bf16"), (64, 8, 64, "fp16")])
+def test_tree_long_runs(qa, T, G, d, dtype, kv):
+    """Enough keys that every block walks many tiles and crosses from one sequence's to the next's."""
+    lens = [9000, 1, 3333, 6400, 0, 777, 8191, 2048, 5, 4095]
+    c = R.Case(17, lens, T, 4, G, d, 64, dtype, kv, [T - (b % T) // 2 for b in range(len(lens))], junk=False)
+    x = c.cuda()
+    o, lse = qa.sage2_attn_tree(out_dtype=torch.float32, **x)
+    assert qa.sage2_check_device_error() == 0
+    check_tree(c, o, lse, attend_gpu(c, x), torch.float32)
+    o2, lse2 = qa.sage2_attn_tree(out_dtype=torch.float32, **x)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
 @pytest.mark.parametrize("kv", ["same", "e4m3"])
 @pytest.mark.parametrize("T, G, d", [(5, 3, 128), (7, 4, 64), (40, 2, 128), (40, 4, 64), (33, 6, 128)])
 def test_not_finite_in_masked_places(qa, T, G, d, kv):
