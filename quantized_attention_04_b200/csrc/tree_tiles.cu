@@ -133,6 +133,27 @@ __device__ __forceinline__ uint32_t tile_off(int r, int ch) {
   return (ch >> 3) * (ROWS * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
 }
 
+// A warp waits for the phase with the given parity, with no more than a poll and a branch a try: the
+// waiting warps share the issue slots with those that work.  Gives up as mbar_wait does.
+__device__ __forceinline__ bool tile_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  bool ok = mbar_try_wait(bar, parity);
+  if (!__all_sync(0xffffffffu, ok)) {
+    const uint64_t t0 = globaltimer_ns();
+    while (!ok) {
+#pragma unroll 1
+      for (int i = 0; i < 256 && !ok; ++i) ok = mbar_try_wait(bar, parity);
+      if (ok || (abort_flag && *abort_flag)) break;
+      if (globaltimer_ns() - t0 > kWaitLimitNs) {
+        atomicOr(&g_device_error, DEVERR_TIMEOUT);
+        if (abort_flag) *abort_flag = 1;
+        break;
+      }
+    }
+    ok = __all_sync(0xffffffffu, ok);
+  }
+  return ok;
+}
+
 // Does drafted token i of a sequence attend slot `key`?
 __device__ __forceinline__ bool slot_allowed(const TreeArgs& a, const uint8_t* mask, SeqLen s, int i, int key) {
   const int j = key - s.len;
@@ -188,6 +209,22 @@ __device__ __noinline__ bool v_row_bad(const TreeArgs& a, int b, int h, int slot
     bad = bad || not_finite16<E4M3, BF>(
                      __ldg(reinterpret_cast<const uint4*>(a.c.v + row * D * (E4M3 ? 1 : 2)) + i));
   return bad;
+}
+
+// The two rows of a thread (.16x256b) of O times f0, f1.  Rare: not inlined, so that the loop that
+// calls it keeps its registers.
+template <int D>
+__device__ __noinline__ void scale_rows(uint32_t o, float f0, float f1) {
+#pragma unroll 1
+  for (int d0 = 0; d0 < D; d0 += 32) {
+    uint32_t y[16];
+    tmem_ld16x256_16(o + d0, y);
+    tmem_ld_wait();
+#pragma unroll
+    for (int z = 0; z < 16; ++z) y[z] = __float_as_uint(__uint_as_float(y[z]) * ((z & 2) ? f1 : f0));
+    tmem_st16x256_16(o + d0, y);
+  }
+  tmem_st_wait();
 }
 
 template <int D, bool E4M3, bool QBF, bool SHARE>
@@ -284,7 +321,7 @@ __global__ void __launch_bounds__(kTThreads<E4M3>, 1)
           at.next(a, pairs, kTK);
           page = page_of();
         }
-        if (t >= kRing && !mbar_wait_warp(&sm.empty[buf], (t / kRing - 1) & 1, abort_flag)) {
+        if (t >= kRing && !tile_wait(&sm.empty[buf], (t / kRing - 1) & 1, abort_flag)) {
           ok = false;
           break;
         }
@@ -304,7 +341,7 @@ __global__ void __launch_bounds__(kTThreads<E4M3>, 1)
         }
         if (edge) {
           // rows behind the last key and drafted rows that are not finite become zeros
-          if (!mbar_wait_warp(&sm.tail[buf], (tails >> (t % kRing)) & 1, abort_flag)) {
+          if (!tile_wait(&sm.tail[buf], (tails >> (t % kRing)) & 1, abort_flag)) {
             ok = false;
             break;
           }
@@ -333,15 +370,16 @@ __global__ void __launch_bounds__(kTThreads<E4M3>, 1)
           mbar_wait(&sm.full[base + u % kRing], (u / kRing) & 1, nullptr);
       }
     } else {
-      // in units of NU passes over the tile's rows (LPR lanes a row): one unit is on its way while
-      // the one before it is stored
-      constexpr int LPR = D / 16, RPP = 32 * kGroup / LPR, NP = kTK / RPP, NU = NP < 4 ? NP : 4;
+      // A row is 8 lanes with 8 bytes each (D = 128: and 8 more 64 codes on), so that they store the 8
+      // chunks of a 128-byte line.  In units of NU passes over the tile's rows; one unit is on its way
+      // while the one before it is stored.
+      constexpr int RPP = 4 * kGroup, NP = kTK / RPP, NU = kGroup == 4 || D == 64 ? NP : NP / 2;
       constexpr int kUnits = NP / NU;
-      const int lt = (tid - 16 * 32) % (32 * kGroup), lr = lt / LPR, lc = lt % LPR;
-      const uint8_t* pool = v ? a.c.v : a.c.k;
+      const int lt = (tid - 16 * 32) % (32 * kGroup), lr = lt >> 3, lc = lt & 7;
+      const uint8_t* pool = (v ? a.c.v : a.c.k) + 8 * lc;
       struct Unit {
-        uint4 u[NU];
-        int first, last;           // rows of the tile from which on they are drafted ones, none
+        uint2 u[NU][C::kBlk];
+        int first;                 // row of the tile from which on they are drafted ones
         bool starts;
       };
       int at_t = 0, row16 = -1;    // lane j: row of slot 16 j of the tile
@@ -358,47 +396,56 @@ __global__ void __launch_bounds__(kTThreads<E4M3>, 1)
           }
         }
         x.first = at.s.len - key0;
-        x.last = L - key0;
         x.starts = at_t == 0 || at.tile == 0;
+        const bool full = key0 + kTK <= L && __all_sync(0xffffffffu, lane >= kTK / 16 || row16 >= 0);
 #pragma unroll
         for (int p = 0; p < NU; ++p) {
           const int r = (sub * NU + p) * RPP + lr, row = __shfl_sync(0xffffffffu, row16, r >> 4);
-          x.u[p] = make_uint4(0u, 0u, 0u, 0u);
-          if (row >= 0 && r < x.last)
-            x.u[p] = __ldg(reinterpret_cast<const uint4*>(pool + (size_t)(row + (r & 15)) * D) + lc);
+          const uint2* src = reinterpret_cast<const uint2*>(pool + (size_t)(uint32_t)(row + (r & 15)) * D);
+#pragma unroll
+          for (int c = 0; c < C::kBlk; ++c) {
+            if (full) x.u[p][c] = __ldg(src + 8 * c);
+            else x.u[p][c] = row >= 0 && key0 + r < L ? __ldg(src + 8 * c) : make_uint2(0u, 0u);
+          }
         }
         if (sub == kUnits - 1 && ++at_t < n) {
           at.next(a, pairs, kTK);
           page = page_of();
         }
       };
+      const uint32_t off = tile_off<kTK>(lr, lc);      // of row r + 8 i: 1024 i more
       auto put = [&](Unit& x, int t, int sub) -> bool {
         const int buf = base + t % kRing;
-        if (sub == 0 && t >= kRing && !mbar_wait_warp(&sm.empty[buf], (t / kRing - 1) & 1, abort_flag)) return false;
-        uint8_t* dst = sm.kv[buf];
+        if (sub == 0 && t >= kRing && !tile_wait(&sm.empty[buf], (t / kRing - 1) & 1, abort_flag)) return false;
+        uint8_t* dst = sm.kv[buf] + off;
         if (sub == 0 && !v && lt == 0) sm.starts[buf] = x.starts;
+        if (v && x.first < kTK) {
+          // drafted rows that are not finite become zeros
 #pragma unroll
-        for (int p = 0; p < NU; ++p) {
-          const int r = (sub * NU + p) * RPP + lr;
-          if (v && x.first < kTK) {
-            unsigned bad = r >= x.first && not_finite16<true, false>(x.u[p]) ? 1u : 0u;
+          for (int p = 0; p < NU; ++p) {
+            const int r = (sub * NU + p) * RPP + lr;
+            unsigned bad = 0;
 #pragma unroll
-            for (int o = LPR / 2; o; o >>= 1) bad |= __shfl_xor_sync(0xffffffffu, bad, o);
-            if (bad) {
-              x.u[p] = make_uint4(0u, 0u, 0u, 0u);
+            for (int c = 0; c < C::kBlk; ++c)
+              bad |= not_finite16<true, false>(make_uint4(x.u[p][c].x, x.u[p][c].y, 0u, 0u)) ? 1u : 0u;
+#pragma unroll
+            for (int o = 4; o; o >>= 1) bad |= __shfl_xor_sync(0xffffffffu, bad, o);
+            if (bad && r >= x.first) {
+#pragma unroll
+              for (int c = 0; c < C::kBlk; ++c) x.u[p][c] = make_uint2(0u, 0u);
               sm.bad_v = 1;
             }
           }
-          uint4 lo, hi;
-          widen4(x.u[p].x, lo.x, lo.y);
-          widen4(x.u[p].y, lo.z, lo.w);
-          widen4(x.u[p].z, hi.x, hi.y);
-          widen4(x.u[p].w, hi.z, hi.w);
-          // the two halves of a row store different chunks at a time: no bank conflicts
-          const bool sw = D == 128 && (lc >> 2);
-          *reinterpret_cast<uint4*>(dst + tile_off<kTK>(r, 2 * lc + (sw ? 1 : 0))) = sw ? hi : lo;
-          *reinterpret_cast<uint4*>(dst + tile_off<kTK>(r, 2 * lc + (sw ? 0 : 1))) = sw ? lo : hi;
         }
+#pragma unroll
+        for (int p = 0; p < NU; ++p)
+#pragma unroll
+          for (int c = 0; c < C::kBlk; ++c) {
+            uint4 w;
+            widen4(x.u[p][c].x, w.x, w.y);
+            widen4(x.u[p][c].y, w.z, w.w);
+            *reinterpret_cast<uint4*>(dst + (sub * NU + p) * RPP * 128 + c * (kTK * 128)) = w;
+          }
         if (sub == kUnits - 1) {
           fence_proxy_async_smem();
           __syncwarp();
@@ -454,7 +501,7 @@ __global__ void __launch_bounds__(kTThreads<E4M3>, 1)
       auto scores = [&](int k, int buf, int start) -> bool {
         const int p = k & 1;
         if (start) {
-          if (!mbar_wait_warp(&sm.q_full[s], q_ph, abort_flag)) return false;
+          if (!tile_wait(&sm.q_full[s], q_ph, abort_flag)) return false;
           q_ph ^= 1;
         }
         first = (first & ~(1 << p)) | (start << p);
@@ -481,8 +528,8 @@ __global__ void __launch_bounds__(kTThreads<E4M3>, 1)
       for (int t = -1; ok && t < n; ++t) {
         if (t >= 0) {
           const int p = t & 1, buf = t % kRing;
-          if (!mbar_wait_warp(&sm.p_full[s][p], (t >> 1) & 1, abort_flag) ||
-              !mbar_wait_warp(&sm.full[vb0 + buf], (t / kRing) & 1, abort_flag))
+          if (!tile_wait(&sm.p_full[s][p], (t >> 1) & 1, abort_flag) ||
+              !tile_wait(&sm.full[vb0 + buf], (t / kRing) & 1, abort_flag))
             break;
           tc_fence_after();
           const uint32_t vb = v_lo + buf * kBuf16, keep = ((first >> p) & 1) ^ 1;
@@ -499,7 +546,7 @@ __global__ void __launch_bounds__(kTThreads<E4M3>, 1)
 #pragma unroll 1
         while (ns < n && ns <= t + 2) {
           const int buf = ns % kRing;
-          if (!mbar_wait_warp(&sm.full[kb0 + buf], (ns / kRing) & 1, abort_flag)) {
+          if (!tile_wait(&sm.full[kb0 + buf], (ns / kRing) & 1, abort_flag)) {
             ok = false;
             break;
           }
@@ -515,7 +562,7 @@ __global__ void __launch_bounds__(kTThreads<E4M3>, 1)
       // every MMA issued so far completes before the block frees TMEM
       if (leader) tc_commit(&sm.drain[s]);
       __syncwarp();
-      mbar_wait_warp(&sm.drain[s], 0, nullptr);
+      tile_wait(&sm.drain[s], 0, nullptr);
     } else if (E4M3 && warp == kMma + 2) {
       // the rows of the tiles ahead, to L2: a 128-byte line (D = 64: half of one) a row
       const Run r0 = run_of_slot(0), r1 = SHARE ? r0 : run_of_slot(1);
@@ -542,58 +589,90 @@ __global__ void __launch_bounds__(kTThreads<E4M3>, 1)
               const long long row = row_of(page, a.c.Hkv, h, a.c.page_shift, key);
               prefetch_l2(a.c.k + row * D);
               prefetch_l2(a.c.v + row * D);
+              if (lane % 16 == 0) {
+                prefetch_l2(a.c.ks + row);
+                prefetch_l2(a.c.vs + row);
+              }
             }
           }
           if (t + 1 < (s ? r1.n : r0.n)) c.next(a, pairs, kTK);
         }
       }
     } else if (E4M3 && warp == kMma + 3) {
-      // the scales, two keys a lane
+      // the scales, two keys a lane; those of the next tile are on their way while these are stored
       const Run r0 = run_of_slot(0), r1 = SHARE ? r0 : run_of_slot(1);
       Cursor c0, c1;
-      if (r0.n > 0) c0.start(r0, kTK);
-      if (!SHARE && r1.n > 0) c1.start(r1, kTK);
+      struct Ahead {
+        float2 ks, vs;
+        int page, key, len, L;
+      };
+      Ahead x0, x1;
+      auto page_at = [&](const Cursor& c, Ahead& x) {       // the page of the cursor's tile
+        x.key = c.tile * kTK + 2 * lane;
+        x.len = c.s.len;
+        x.L = x.len + c.s.n;
+        x.page = x.key < x.L ? __ldg(a.table + (size_t)c.b * a.MP + (x.key >> a.c.page_shift)) : -1;
+      };
+      auto fetch = [&](const Cursor& c, Ahead& x) {
+        x.ks = x.vs = make_float2(0.f, 0.f);
+        if (page_inside(x.page, a.c.pages)) {
+          const long long row = row_of(x.page, a.c.Hkv, c.pair / a.RT, a.c.page_shift, x.key);
+          x.ks = __ldg(reinterpret_cast<const float2*>(a.c.ks + row));
+          x.vs = __ldg(reinterpret_cast<const float2*>(a.c.vs + row));
+        }
+      };
+      if (r0.n > 0) {
+        c0.start(r0, kTK);
+        page_at(c0, x0);
+        fetch(c0, x0);
+      }
+      if (!SHARE && r1.n > 0) {
+        c1.start(r1, kTK);
+        page_at(c1, x1);
+        fetch(c1, x1);
+      }
       bool go = true;
       for (int t = 0; go && t < max(r0.n, r1.n); ++t) {
 #pragma unroll
         for (int s = 0; s < (SHARE ? 1 : 2); ++s) {
-          if (!go || t >= (s ? r1.n : r0.n)) continue;
+          const int n = s ? r1.n : r0.n;
+          if (!go || t >= n) continue;
           Cursor& c = s ? c1 : c0;
-          const int key = c.tile * kTK + 2 * lane, len = c.s.len, L = len + c.s.n, buf = 2 * s * kRing + t % kRing;
-          float2 ks = make_float2(0.f, 0.f), vs = ks;
-          if (key < L) {
-            const int page = __ldg(a.table + (size_t)c.b * a.MP + (key >> a.c.page_shift));
-            if (page_inside(page, a.c.pages)) {
-              const long long row = row_of(page, a.c.Hkv, c.pair / a.RT, a.c.page_shift, key);
-              ks = __ldg(reinterpret_cast<const float2*>(a.c.ks + row));
-              vs = __ldg(reinterpret_cast<const float2*>(a.c.vs + row));
-            }
+          Ahead& x = s ? x1 : x0;
+          const int buf = 2 * s * kRing + t % kRing;
+          Ahead y = x;
+          if (t + 1 < n) {
+            c.next(a, pairs, kTK);
+            page_at(c, x);
           }
           // masked scores are -inf before the key scale multiplies them, and P is 0 before the value
           // scale does: the scales of drafted rows become finite, a key's not 0 (a row of scale 0
           // has codes 0); those behind the last key are 1 and 0
-          auto clean = [&](float x, bool is_key, int k) {
-            if (k < len) return x;
-            if (k >= L) x = 0.f;
-            if (!(fabsf(x) < INFINITY)) {
-              x = 0.f;
+          auto clean = [&](float w, bool is_key, int k) {
+            if (k < y.len) return w;
+            if (k >= y.L) w = 0.f;
+            if (!(fabsf(w) < INFINITY)) {
+              w = 0.f;
               sm.bad_v = 1;
             }
-            return is_key && x == 0.f ? 1.f : x;
+            return is_key && w == 0.f ? 1.f : w;
           };
-          ks.x = clean(ks.x, true, key);
-          ks.y = clean(ks.y, true, key + 1);
-          vs.x = clean(vs.x, false, key);
-          vs.y = clean(vs.y, false, key + 1);
-          float m = fmaxf(vs.x, vs.y);
+          if (y.key + 2 > y.len) {
+            y.ks.x = clean(y.ks.x, true, y.key);
+            y.ks.y = clean(y.ks.y, true, y.key + 1);
+            y.vs.x = clean(y.vs.x, false, y.key);
+            y.vs.y = clean(y.vs.y, false, y.key + 1);
+          }
+          float m = fmaxf(y.vs.x, y.vs.y);
 #pragma unroll
           for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-          if (t + 1 < (s ? r1.n : r0.n)) c.next(a, pairs, kTK);
-          if (t >= kRing && !mbar_wait_warp(&sm.empty[buf], (t / kRing - 1) & 1, abort_flag)) {
+          if (t + 1 < n) fetch(c, x);
+          if (t >= kRing && !tile_wait(&sm.empty[buf], (t / kRing - 1) & 1, abort_flag)) {
             go = false;
             continue;
           }
-          *reinterpret_cast<float4*>(sm.scl[s][t % C::kScales] + 4 * lane) = make_float4(ks.x, ks.y, vs.x, vs.y);
+          *reinterpret_cast<float4*>(sm.scl[s][t % C::kScales] + 4 * lane) =
+              make_float4(y.ks.x, y.ks.y, y.vs.x, y.vs.y);
           if (lane == 0) sm.lv[s][t % C::kScales] = log2f(fmaxf(m, kVrefLeast));
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.full[buf]);
@@ -626,20 +705,16 @@ __global__ void __launch_bounds__(kTThreads<E4M3>, 1)
         // a piece starts: the slot's rows of Q.  The last S of the piece before has been waited
         // for, so nothing reads the buffer.
         const int unit0 = (at.pair % a.RT) * rows_unit, h = at.pair / a.RT;
-        uint4 qu[2][D / 32];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
+          uint4 u[D / 32];
           r[e] = lo + 8 * e < rows_unit ? min(unit0 + lo + 8 * e, R) : R;
           const uint4* src = reinterpret_cast<const uint4*>(
               static_cast<const uint16_t*>(a.q) + at.b * a.sb + (long long)(h * a.G + r[e] / a.T) * a.sh +
               (long long)(r[e] % a.T) * a.st);
 #pragma unroll
           for (int c = 0; c < D / 32; ++c)
-            qu[e][c] = r[e] < R ? __ldg(src + 4 * c + g) : make_uint4(0u, 0u, 0u, 0u);
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          uint4 (&u)[D / 32] = qu[e];
+            u[c] = r[e] < R ? __ldg(src + 4 * c + g) : make_uint4(0u, 0u, 0u, 0u);
           qs[e] = a.sm_scale * kL2E;
           ref[e] = -INFINITY;
           l[e] = 0.f;
@@ -681,7 +756,7 @@ __global__ void __launch_bounds__(kTThreads<E4M3>, 1)
         __syncwarp();
         mbar_arrive_lane0(&sm.q_full[s], lane);
       }
-      if (!mbar_wait_warp(&sm.s_full[s][t & 1], (t >> 1) & 1, abort_flag)) {
+      if (!tile_wait(&sm.s_full[s][t & 1], (t >> 1) & 1, abort_flag)) {
         ok = false;
         break;
       }
@@ -700,14 +775,17 @@ __global__ void __launch_bounds__(kTThreads<E4M3>, 1)
           const int i0 = r[0] % a.T, i1 = r[1] % a.T;
 #pragma unroll 1
           for (int c = 0; c < kTK; c += 32) {
+            uint32_t bits = 0;
+#pragma unroll 4
+            for (int y = 0; y < 16; ++y)
+              if (slot_allowed(a, mask, at.s, y & 2 ? i1 : i0, key0 + c + 8 * (y >> 2) + 2 * g + (y & 1)))
+                bits |= 1u << y;
             uint32_t x[16];
             tmem_ld16x256_16(tS + c, x);
             tmem_ld_wait();
 #pragma unroll
-            for (int y = 0; y < 16; ++y) {
-              const int key = key0 + c + 8 * (y >> 2) + 2 * g + (y & 1);
-              if (!slot_allowed(a, mask, at.s, y & 2 ? i1 : i0, key)) x[y] = 0xff800000u;
-            }
+            for (int y = 0; y < 16; ++y)
+              if (!((bits >> y) & 1u)) x[y] = 0xff800000u;
             tmem_st16x256_16(tS + c, x);
           }
           tmem_st_wait();
@@ -721,35 +799,38 @@ __global__ void __launch_bounds__(kTThreads<E4M3>, 1)
             const float2 m0 = make_float2(n0, n0), m1 = make_float2(n1, n1);
             float mx[2] = {-INFINITY, -INFINITY};
             sum[0] = sum[1] = make_float2(0.f, 0.f);
-            uint32_t x[32];
-            tmem_ld16x256_32(tS, x);
-            tmem_ld_wait();
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              float2 x0 = make_float2(__uint_as_float(x[4 * k]), __uint_as_float(x[4 * k + 1]));
-              float2 x1 = make_float2(__uint_as_float(x[4 * k + 2]), __uint_as_float(x[4 * k + 3]));
-              float4 f4;
-              if (E4M3) {
-                // two key scales and two value scales
-                f4 = *reinterpret_cast<const float4*>(sc + 2 * (8 * k + 2 * g));
-                x0 = __fmul2_rn(x0, make_float2(f4.x, f4.y));
-                x1 = __fmul2_rn(x1, make_float2(f4.x, f4.y));
+            for (int c = 0; c < 2; ++c) {
+              uint32_t x[16];
+              tmem_ld16x256_16(tS + 32 * c, x);
+              tmem_ld_wait();
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                float2 x0 = make_float2(__uint_as_float(x[4 * k]), __uint_as_float(x[4 * k + 1]));
+                float2 x1 = make_float2(__uint_as_float(x[4 * k + 2]), __uint_as_float(x[4 * k + 3]));
+                float4 f4;
+                if (E4M3) {
+                  // two key scales and two value scales
+                  f4 = *reinterpret_cast<const float4*>(sc + 2 * (32 * c + 8 * k + 2 * g));
+                  x0 = __fmul2_rn(x0, make_float2(f4.x, f4.y));
+                  x1 = __fmul2_rn(x1, make_float2(f4.x, f4.y));
+                }
+                mx[0] = max3f(mx[0], x0.x, x0.y);
+                mx[1] = max3f(mx[1], x1.x, x1.y);
+                float2 e0 = __ffma2_rn(x0, q0, m0), e1 = __ffma2_rn(x1, q1, m1);
+                e0.x = ex2(e0.x);
+                e0.y = ex2(e0.y);
+                e1.x = ex2(e1.x);
+                e1.y = ex2(e1.y);
+                sum[0] = __fadd2_rn(sum[0], e0);
+                sum[1] = __fadd2_rn(sum[1], e1);
+                if (E4M3) {
+                  e0 = __fmul2_rn(e0, make_float2(f4.z, f4.w));
+                  e1 = __fmul2_rn(e1, make_float2(f4.z, f4.w));
+                }
+                p[8 * c + 2 * k] = pack2<BF>(e0.x, e0.y);
+                p[8 * c + 2 * k + 1] = pack2<BF>(e1.x, e1.y);
               }
-              mx[0] = max3f(mx[0], x0.x, x0.y);
-              mx[1] = max3f(mx[1], x1.x, x1.y);
-              float2 e0 = __ffma2_rn(x0, q0, m0), e1 = __ffma2_rn(x1, q1, m1);
-              e0.x = ex2(e0.x);
-              e0.y = ex2(e0.y);
-              e1.x = ex2(e1.x);
-              e1.y = ex2(e1.y);
-              sum[0] = __fadd2_rn(sum[0], e0);
-              sum[1] = __fadd2_rn(sum[1], e1);
-              if (E4M3) {
-                e0 = __fmul2_rn(e0, make_float2(f4.z, f4.w));
-                e1 = __fmul2_rn(e1, make_float2(f4.z, f4.w));
-              }
-              p[2 * k] = pack2<BF>(e0.x, e0.y);
-              p[2 * k + 1] = pack2<BF>(e1.x, e1.y);
             }
             const bool over = (mx[0] > -INFINITY && mx[0] * qs[0] + lv > ref[0] + kGrow) ||
                               (mx[1] > -INFINITY && mx[1] * qs[1] + lv > ref[1] + kGrow);
@@ -767,22 +848,13 @@ __global__ void __launch_bounds__(kTThreads<E4M3>, 1)
               l[e] *= f[e];
             }
             if (!first) {
-              if (!mbar_wait_warp(&sm.o_done[s][(t - 1) & 1], ((t - 1) >> 1) & 1, abort_flag)) {
+              if (!tile_wait(&sm.o_done[s][(t - 1) & 1], ((t - 1) >> 1) & 1, abort_flag)) {
                 ok = false;
                 break;
               }
               tc_fence_after();
-#pragma unroll 1
-              for (int d0 = 0; d0 < D; d0 += 32) {
-                uint32_t y[16];
-                tmem_ld16x256_16(tO + d0, y);
-                tmem_ld_wait();
-#pragma unroll
-                for (int z = 0; z < 16; ++z) y[z] = __float_as_uint(__uint_as_float(y[z]) * f[(z >> 1) & 1]);
-                tmem_st16x256_16(tO + d0, y);
-              }
+              scale_rows<D>(tO, f[0], f[1]);
             }
-            tmem_st_wait();
           }
           if (!ok) break;
           tmem_st16x128_16(tS, p);
@@ -797,7 +869,7 @@ __global__ void __launch_bounds__(kTThreads<E4M3>, 1)
 
       if (at.tile + 1 == at.tiles || t + 1 == nt) {
         // ---- the piece ends
-        if (!mbar_wait_warp(&sm.o_done[s][t & 1], (t >> 1) & 1, abort_flag)) {
+        if (!tile_wait(&sm.o_done[s][t & 1], (t >> 1) & 1, abort_flag)) {
           ok = false;
           break;
         }
