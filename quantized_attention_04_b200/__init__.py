@@ -423,80 +423,88 @@ def sage2_cache_alloc(pages: int, Hkv: int, page_size: int, d: int, dtype=torch.
 
 
 def _cache_of(cache: dict):
-    """(sage2_cache, k): the checked cache of a dict."""
+    """(sage2_cache, index of its device): the checked cache of a dict."""
     k, v = cache["k"], cache["v"]
-    if k.dim() != 4 or not k.is_cuda or not k.is_contiguous():
+    dev = k.get_device()
+    shape, dtype = k.shape, k.dtype
+    if len(shape) != 4 or dev < 0 or not k.is_contiguous():
         raise ValueError("a cache holds contiguous CUDA tensors [pages, Hkv, page_size, d]")
-    if v.shape != k.shape or v.dtype != k.dtype or v.device != k.device or not v.is_contiguous():
+    if v.shape != shape or v.dtype != dtype or v.get_device() != dev or not v.is_contiguous():
         raise ValueError("the cache's k and v must be alike")
-    ty = _KV.get(k.dtype)
+    ty = _KV.get(dtype)
     if ty is None:
         raise ValueError("a cache is float16, bfloat16 or float8_e4m3fn")
-    pages, Hkv, page, d = k.shape
     ks = vs = 0
     if ty == E4M3:
-        for t in (cache["k_scale"], cache["v_scale"]):
-            if t.shape != k.shape[:3] or t.dtype != torch.float32 or t.device != k.device \
+        ks, vs = cache["k_scale"], cache["v_scale"]
+        for t in (ks, vs):
+            if t.shape != shape[:3] or t.dtype != torch.float32 or t.get_device() != dev \
                     or not t.is_contiguous():
                 raise ValueError("k_scale and v_scale must be contiguous float32 "
                                  "[pages, Hkv, page_size] on the cache's device")
-        ks, vs = cache["k_scale"].data_ptr(), cache["v_scale"].data_ptr()
-    return _Cache(k.data_ptr(), v.data_ptr(), ks, vs, ty, pages, Hkv, page, d), k
+        ks, vs = ks.data_ptr(), vs.data_ptr()
+    return _Cache(k.data_ptr(), v.data_ptr(), ks, vs, ty, *shape), dev
 
 
-def _ints(t: torch.Tensor | None, shape, dev, what: str) -> int:
-    """Address of a contiguous int32 tensor of that shape (0 for None)."""
+def _ints(t: torch.Tensor | None, n: int, dev: int, what: str) -> int:
+    """Address of a contiguous int32 tensor [n] (0 for None)."""
     if t is None:
         return 0
-    if t.dtype != torch.int32 or t.device != dev or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous int32 tensor {list(shape)} on the cache's device")
+    if t.dtype != torch.int32 or t.get_device() != dev or t.dim() != 1 or t.shape[0] != n \
+            or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous int32 tensor [{n}] on the cache's device")
     return t.data_ptr()
 
 
-def _table(t: torch.Tensor, dev, B: int | None = None):
-    if t.dim() != 2 or t.dtype != torch.int32 or t.device != dev or not t.is_contiguous() \
-            or (B is not None and t.shape[0] != B):
+def _table(t: torch.Tensor, dev: int, B: int):
+    if t.dim() != 2 or t.dtype != torch.int32 or t.get_device() != dev or not t.is_contiguous() \
+            or t.shape[0] != B:
         raise ValueError("a page table is a contiguous int32 tensor [B, max_pages] on the cache's device")
     return t.data_ptr(), t.shape[1]
 
 
-def _bhtd(t: torch.Tensor, dev, d: int, what: str):
-    """Strides of a [B, H, T, d] tensor whose rows are contiguous."""
-    if t.dim() != 4 or t.device != dev or t.shape[3] != d or (d > 1 and t.stride(3) != 1):
+def _bhtd(t: torch.Tensor, dev: int, d: int, what: str):
+    """Strides of a [B, H, T, d] tensor whose rows are contiguous (None: all of it is)."""
+    if t.dim() != 4 or t.get_device() != dev or t.shape[3] != d:
         raise ValueError(f"{what} must be [B, H, T, {d}] on the cache's device, its last dimension contiguous")
-    if t.dtype not in (torch.float16, torch.bfloat16):
+    if t.dtype != torch.float16 and t.dtype != torch.bfloat16:
         raise ValueError(f"{what} must be float16 or bfloat16")
+    if t.is_contiguous():
+        return None
+    if t.stride(3) != 1:
+        raise ValueError(f"{what} must be [B, H, T, {d}] on the cache's device, its last dimension contiguous")
     # the stride of a dimension of one element says nothing
-    return _S3(*(t.stride(i) if t.shape[i] > 1 else 0 for i in range(3)))
+    return _S3(*(st if n > 1 else 0 for n, st in zip(t.shape[:3], t.stride())))
 
 
-def _tally(t: torch.Tensor, dev, B: int, H: int, what: str):
-    if t.dim() != 3 or t.dtype != torch.float32 or t.device != dev or t.shape[0] != B \
+def _tally(t: torch.Tensor, dev: int, B: int, H: int, what: str):
+    if t.dim() != 3 or t.dtype != torch.float32 or t.get_device() != dev or t.shape[0] != B \
             or t.shape[1] != H or (t.shape[2] > 1 and t.stride(2) != 1):
         raise ValueError(f"{what} must be float32 [B, Hkv, slots] on the cache's device, slots contiguous")
     return _S2(t.stride(0), t.stride(1))
 
 
-def _mask(mask: torch.Tensor | None, dev, B: int, T: int):
+def _mask(mask: torch.Tensor | None, dev: int, B: int, T: int):
     """(address, bytes between sequences) of a tree mask."""
     if mask is None:
         return 0, 0
-    if mask.dtype not in (torch.bool, torch.uint8) or mask.device != dev \
-            or tuple(mask.shape) not in ((T, T), (B, T, T)):
+    if (mask.dtype != torch.bool and mask.dtype != torch.uint8) or mask.get_device() != dev \
+            or mask.shape not in ((T, T), (B, T, T)):
         raise ValueError("mask must be bool [T, T] or [B, T, T] on the cache's device")
     if T > 1 and (mask.stride(-1) != 1 or mask.stride(-2) != T):
         raise ValueError("mask must be contiguous in its last two dimensions")
-    return mask.data_ptr(), mask.stride(0) if mask.dim() == 3 and B > 1 else 0
+    return mask.data_ptr(), mask.stride(0) if B > 1 and mask.dim() == 3 else 0
 
 
-def _run(name: str, dev: torch.device, *args):
-    """The call on torch's current stream of `dev`, with that device current."""
+def _run(name: str, dev: int, *args):
+    """The call on torch's current stream of device `dev`, with that device current."""
     fn = getattr(lib(), name)
-    if torch.cuda.current_device() == dev.index:
-        st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    stream = torch._C._cuda_getCurrentRawStream(dev)
+    if torch._C._cuda_getDevice() == dev:
+        st = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+            st = fn(*args, stream)
     if st != 0:
         raise Sage2Error(name, st)
 
@@ -505,8 +513,7 @@ def sage2_cache_append(k: torch.Tensor, v: torch.Tensor, cache: dict, table: tor
                        lens: torch.Tensor, n: torch.Tensor | None = None) -> dict:
     """Writes k, v [B, Hkv, T, d] behind the lens[b] tokens in the cache (n[b] of
     the T tokens; None: all), in the cache's type.  `lens` is not changed."""
-    cs, pool = _cache_of(cache)
-    dev = pool.device
+    cs, dev = _cache_of(cache)
     if k.shape != v.shape or k.dtype != v.dtype:
         raise ValueError("k and v must have the same shape and dtype")
     sk, sv = _bhtd(k, dev, cs.d, "k"), _bhtd(v, dev, cs.d, "v")
@@ -515,7 +522,7 @@ def sage2_cache_append(k: torch.Tensor, v: torch.Tensor, cache: dict, table: tor
         raise ValueError("k and v must have the cache's heads")
     tp, mp = _table(table, dev, B)
     _run("sage2_cache_append", dev, k.data_ptr(), v.data_ptr(), _DT[k.dtype], sk, sv,
-         ctypes.byref(cs), tp, mp, _ints(lens, (B,), dev, "lens"), _ints(n, (B,), dev, "n"), B, T)
+         ctypes.byref(cs), tp, mp, _ints(lens, B, dev, "lens"), _ints(n, B, dev, "n"), B, T)
     return cache
 
 
@@ -528,23 +535,22 @@ def sage2_attn_tree(q: torch.Tensor, cache: dict, table: torch.Tensor, lens: tor
     cache).  mask [T, T] or [B, T, T]: row i marks the drafted tokens that token
     i attends (None: those up to itself).  n[b] of the T tokens are in use (None:
     all).  Returns (o [B, Hq, T, d], lse [B, Hq, T])."""
-    cs, pool = _cache_of(cache)
-    dev = pool.device
+    cs, dev = _cache_of(cache)
     sq = _bhtd(q, dev, cs.d, "q")
     B, Hq, T, d = q.shape
     tp, mp = _table(table, dev, B)
     mptr, mstride = _mask(mask, dev, B, T)
     if out is None:
-        out = torch.empty(B, Hq, T, d, dtype=out_dtype or q.dtype, device=dev)
-    elif out.shape != q.shape or out.device != dev or not out.is_contiguous() or out.dtype not in _DT:
+        out = torch.empty((B, Hq, T, d), dtype=out_dtype or q.dtype, device=q.device)
+    elif out.shape != q.shape or out.get_device() != dev or not out.is_contiguous() or out.dtype not in _DT:
         raise ValueError("out must be contiguous, of q's shape and on its device")
     if lse is None:
-        lse = torch.empty(B, Hq, T, dtype=torch.float32, device=dev)
-    elif lse.shape != (B, Hq, T) or lse.dtype != torch.float32 or lse.device != dev \
+        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=q.device)
+    elif lse.shape != (B, Hq, T) or lse.dtype != torch.float32 or lse.get_device() != dev \
             or not lse.is_contiguous():
         raise ValueError("lse must be contiguous float32 [B, Hq, T]")
     _run("sage2_attn_tree", dev, q.data_ptr(), _DT[q.dtype], sq, ctypes.byref(cs), tp, mp,
-         _ints(lens, (B,), dev, "lens"), _ints(n, (B,), dev, "n"), mptr, mstride, out.data_ptr(),
+         _ints(lens, B, dev, "lens"), _ints(n, B, dev, "n"), mptr, mstride, out.data_ptr(),
          _DT[out.dtype], lse.data_ptr(), B, Hq, T,
          1.0 / math.sqrt(d) if sm_scale is None else sm_scale)
     return out, lse
@@ -556,18 +562,17 @@ def sage2_cache_weights(q: torch.Tensor, lse: torch.Tensor, cache: dict, table: 
     """Adds to acc [B, Hkv, slots] (float32) the attention weight that each cached
     token received from q, over all its heads and drafted tokens; the arguments
     are those of sage2_attn_tree and the lse it returned."""
-    cs, pool = _cache_of(cache)
-    dev = pool.device
+    cs, dev = _cache_of(cache)
     sq = _bhtd(q, dev, cs.d, "q")
     B, Hq, T, d = q.shape
     tp, mp = _table(table, dev, B)
     mptr, mstride = _mask(mask, dev, B, T)
-    if lse.shape != (B, Hq, T) or lse.dtype != torch.float32 or lse.device != dev \
+    if lse.shape != (B, Hq, T) or lse.dtype != torch.float32 or lse.get_device() != dev \
             or not lse.is_contiguous():
         raise ValueError("lse must be contiguous float32 [B, Hq, T]")
     sa = _tally(acc, dev, B, cs.Hkv, "acc")
     _run("sage2_cache_weights", dev, q.data_ptr(), _DT[q.dtype], sq, lse.data_ptr(),
-         ctypes.byref(cs), tp, mp, _ints(lens, (B,), dev, "lens"), _ints(n, (B,), dev, "n"), mptr,
+         ctypes.byref(cs), tp, mp, _ints(lens, B, dev, "lens"), _ints(n, B, dev, "n"), mptr,
          mstride, acc.data_ptr(), sa, acc.shape[2], B, Hq, T,
          1.0 / math.sqrt(d) if sm_scale is None else sm_scale)
     return acc
@@ -589,9 +594,8 @@ def sage2_cache_compact(cache: dict, table: torch.Tensor, idx: torch.Tensor,
     place, rows moving towards the front only.  For an accepted path of a tree:
     idx = lens + path, base = lens, the same for every head (an expanded idx).  With
     acc [B, Hkv, slots] its values move along, to acc_out (None: in place)."""
-    cs, pool = _cache_of(cache)
-    dev = pool.device
-    if idx.dim() != 3 or idx.dtype != torch.int32 or idx.device != dev or idx.shape[1] != cs.Hkv \
+    cs, dev = _cache_of(cache)
+    if idx.dim() != 3 or idx.dtype != torch.int32 or idx.get_device() != dev or idx.shape[1] != cs.Hkv \
             or (idx.shape[2] > 1 and idx.stride(2) != 1):
         raise ValueError("idx must be int32 [B, Hkv, M] on the cache's device, M contiguous")
     B, _, M = idx.shape
@@ -608,7 +612,7 @@ def sage2_cache_compact(cache: dict, table: torch.Tensor, idx: torch.Tensor,
         sa, so = _tally(acc, dev, B, cs.Hkv, "acc"), _tally(acc_out, dev, B, cs.Hkv, "acc_out")
         S, SO, ap, aop = acc.shape[2], acc_out.shape[2], acc.data_ptr(), acc_out.data_ptr()
     _run("sage2_cache_compact", dev, ctypes.byref(cs), tp, mp, op, om, idx.data_ptr(),
-         _S2(idx.stride(0), idx.stride(1)), _ints(n, (B,), dev, "n"), _ints(base, (B,), dev, "base"),
+         _S2(idx.stride(0), idx.stride(1)), _ints(n, B, dev, "n"), _ints(base, B, dev, "base"),
          ap, sa, S, aop, so, SO, B, M)
     return cache
 
@@ -621,8 +625,7 @@ def sage2_cache_evict(cache: dict, table: torch.Tensor, lens: torch.Tensor, acc:
     rows move to the slots 0.. of out_table (None: in place), their tallies to
     acc_out (None: a new tensor [B, Hkv, keep]).  Returns (idx int32 [B, Hkv, keep]:
     the kept slots, ascending, -1 behind the last; lens int32 [B]; acc_out)."""
-    cs, pool = _cache_of(cache)
-    dev = pool.device
+    cs, dev = _cache_of(cache)
     B = lens.shape[0] if lens.dim() == 1 else -1
     tp, mp = _table(table, dev, B)
     op, om = _out_table(table, out_table, dev, B)
@@ -630,13 +633,13 @@ def sage2_cache_evict(cache: dict, table: torch.Tensor, lens: torch.Tensor, acc:
     if keep <= 0:
         raise ValueError("keep must be positive")
     if acc_out is None:
-        acc_out = torch.zeros(B, cs.Hkv, keep, dtype=torch.float32, device=dev)
+        acc_out = torch.zeros((B, cs.Hkv, keep), dtype=torch.float32, device=lens.device)
     elif op and acc_out.data_ptr() == acc.data_ptr():
         raise ValueError("acc_out must be another tensor than acc when out_table is another table")
     so = _tally(acc_out, dev, B, cs.Hkv, "acc_out")
-    idx = torch.empty(B, cs.Hkv, keep, dtype=torch.int32, device=dev)
-    new = torch.empty(B, dtype=torch.int32, device=dev)
-    _run("sage2_cache_evict", dev, ctypes.byref(cs), tp, mp, op, om, _ints(lens, (B,), dev, "lens"),
+    idx = torch.empty((B, cs.Hkv, keep), dtype=torch.int32, device=lens.device)
+    new = torch.empty(B, dtype=torch.int32, device=lens.device)
+    _run("sage2_cache_evict", dev, ctypes.byref(cs), tp, mp, op, om, _ints(lens, B, dev, "lens"),
          acc.data_ptr(), sa, acc.shape[2], acc_out.data_ptr(), so, acc_out.shape[2], B, keep, sinks,
          recent, idx.data_ptr(), new.data_ptr())
     return idx, new, acc_out

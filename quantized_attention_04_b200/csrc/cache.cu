@@ -9,6 +9,8 @@
 // Device-side integers (table, lens, n, idx) are checked where they are used:
 // one that points outside the pools or the table sets DEVERR_BOUNDS and the
 // row it names is skipped.
+#include <type_traits>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -36,9 +38,29 @@ __device__ __forceinline__ long long cache_row(const CacheView& c, const int* ta
   return row_of(page, c.Hkv, h, c.page_shift, slot);
 }
 
+// The 16-bit value with these bits.
+template <typename T>
+__device__ __forceinline__ float to_float(uint32_t bits);
+template <>
+__device__ __forceinline__ float to_float<__half>(uint32_t bits) {
+  return __half2float(__ushort_as_half(static_cast<unsigned short>(bits)));
+}
+template <>
+__device__ __forceinline__ float to_float<__nv_bfloat16>(uint32_t bits) {
+  return __uint_as_float(bits << 16);
+}
+
+// Data that this kernel alone reads, and once: not kept in L1.
+__device__ __forceinline__ uint4 ld_once(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
 // ---------------------------------------------------------------------------
-// Append.  D/8 lanes own one row of K or V (16 bytes each); a warp holds 2 or 4
-// rows.  e4m3: scale = amax/448, code = e4m3(x * (448/amax)), all fp32 RN, the
+// Append.  D/16 lanes own one row of K or V (32 bytes each) and have kAppendRows of them in
+// flight; a block works for one head of one sequence.  e4m3: scale = amax/448, code = e4m3(x * (448/amax)), all fp32 RN, the
 // same rounding as the quantized V; a row of zeros has scale 0, a row with an
 // infinity or NaN has scale NaN, so that whatever reads it sees NaN.
 struct AppendArgs {
@@ -51,21 +73,14 @@ struct AppendArgs {
   int B, T, MP;
 };
 
+constexpr int kAppendRows = 2;           // rows that a thread has in flight
+
 template <typename T, int D, bool E4M3>
 __global__ void __launch_bounds__(256) k_cache_append(AppendArgs a) {
-  constexpr int LPR = D / 8;            // lanes of a row
-  constexpr int RPB = 256 / LPR;        // rows of a block
-  const int kv = blockIdx.y;
-  const long long row = (long long)blockIdx.x * RPB + threadIdx.x / LPR;
+  constexpr int LPR = D / 16;           // lanes of a row, two 16-byte pieces each
+  constexpr int RPB = 256 / LPR;        // rows of a pass
+  const int kv = blockIdx.z, h = blockIdx.x % a.c.Hkv, b = blockIdx.x / a.c.Hkv;
   const int lane = threadIdx.x % LPR;
-  const long long rows = (long long)a.B * a.c.Hkv * a.T;
-  if (row >= rows) return;              // whole rows, and the shuffles stay inside a row
-  const int t = (int)(row % a.T);
-  const long long bh = row / a.T;
-  const int h = (int)(bh % a.c.Hkv), b = (int)(bh / a.c.Hkv);
-  const uint4 u = __ldg(reinterpret_cast<const uint4*>(
-                            static_cast<const T*>(a.x[kv]) + b * a.sb[kv] + h * a.sh[kv] +
-                            (long long)t * a.st[kv]) + lane);
   const int len = __ldg(a.lens + b);
   int n = a.T;
   if (a.n) {
@@ -75,60 +90,81 @@ __global__ void __launch_bounds__(256) k_cache_append(AppendArgs a) {
       return;
     }
   }
-  if (t >= n) return;
   if (len < 0 || len > INT_MAX - a.T) {
-    atomicOr(&g_device_error, DEVERR_BOUNDS);
+    if (n > 0) atomicOr(&g_device_error, DEVERR_BOUNDS);
     return;
   }
-  const long long dst = cache_row(a.c, a.table, a.MP, b, h, len + t);
-  if (dst < 0) return;
+  const T* x0 = static_cast<const T*>(a.x[kv]) + b * a.sb[kv] + h * a.sh[kv];
   uint8_t* pool = kv ? a.c.v : a.c.k;
-  if (!E4M3) {
-    reinterpret_cast<uint4*>(pool + dst * D * 2)[lane] = u;
-  } else {
-    float x[8];
-    unpack8<T>(u, x);
-    float amax = 0.f;
-    bool fin = true;
+  // whole rows take part, so that the shuffles stay among lanes that are there
+  const unsigned act = ((1u << LPR) - 1u) << (threadIdx.x % 32 / LPR * LPR);
+  const int step = gridDim.y * RPB * kAppendRows;
+  for (int t0 = blockIdx.y * RPB * kAppendRows + threadIdx.x / LPR; t0 < n; t0 += step) {
+    uint4 u[kAppendRows][2];
+    long long dst[kAppendRows];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      amax = fmaxf(amax, fabsf(x[i]));
-      fin = fin && fabsf(x[i]) < __int_as_float(0x7f800000);
+    for (int r = 0; r < kAppendRows; ++r) {
+      const int t = t0 + r * RPB;
+      dst[r] = -1;
+      if (t < n) {
+        const uint4* src = reinterpret_cast<const uint4*>(x0 + (long long)t * a.st[kv]) + lane;
+        u[r][0] = ld_once(src);
+        u[r][1] = ld_once(src + LPR);
+        dst[r] = cache_row(a.c, a.table, a.MP, b, h, len + t);
+      }
     }
-    // the lanes of this row, which are all here: whole rows leave above
-    const unsigned act = (LPR == 32 ? 0xffffffffu : ((1u << LPR) - 1u)) << (threadIdx.x % 32 / LPR * LPR);
-    float bad = fin ? 0.f : 1.f;
 #pragma unroll
-    for (int o = LPR / 2; o; o >>= 1) {
-      amax = fmaxf(amax, __shfl_xor_sync(act, amax, o));
-      bad = fmaxf(bad, __shfl_xor_sync(act, bad, o));
+    for (int r = 0; r < kAppendRows; ++r) {
+      if (t0 + r * RPB >= n || dst[r] < 0) continue;
+      if (!E4M3) {
+        uint4* to = reinterpret_cast<uint4*>(pool + dst[r] * D * 2) + lane;
+        to[0] = u[r][0];
+        to[LPR] = u[r][1];
+        continue;
+      }
+      // largest magnitude as integers, two 16-bit values a word (their order is that of the bits; an
+      // infinity or NaN is the largest of all)
+      uint32_t m2 = 0;
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+        m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(u[r][p].x & 0x7fff7fffu, u[r][p].y & 0x7fff7fffu),
+                                   __vmaxu2(u[r][p].z & 0x7fff7fffu, u[r][p].w & 0x7fff7fffu)));
+#pragma unroll
+      for (int o = LPR / 2; o; o >>= 1) m2 = __vmaxu2(m2, __shfl_xor_sync(act, m2, o));
+      const uint32_t mb = max(m2 & 0xffffu, m2 >> 16);
+      const bool bad = mb >= (std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u);
+      const float amax = to_float<T>(mb);
+      // below 2^-100 the inverse would pass fp32's range: such a row is zero
+      const bool nz = amax >= 7.8886e-31f;
+      // one division a lane: the even ones' 448 / amax goes into the codes, the odd ones' amax / 448
+      // is the scale
+      const float q = nz ? __fdiv_rn(lane & 1 ? amax : 448.f, lane & 1 ? 448.f : amax) : 0.f;
+      const float inv = __shfl_sync(act, q, 0, LPR);
+      const float2 inv2 = make_float2(inv, inv);
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        float x[8];
+        unpack8<T>(u[r][p], x);
+        uint32_t w[2];
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const float2 lo = __fmul2_rn(make_float2(x[4 * g], x[4 * g + 1]), inv2);
+          const float2 hi = __fmul2_rn(make_float2(x[4 * g + 2], x[4 * g + 3]), inv2);
+          w[g] = static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(lo, __NV_SATFINITE, __NV_E4M3)) |
+                 static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(hi, __NV_SATFINITE, __NV_E4M3)) << 16;
+        }
+        reinterpret_cast<uint2*>(pool + dst[r] * D)[lane + p * LPR] = make_uint2(w[0], w[1]);
+      }
+      if (lane == 1) (kv ? a.c.vs : a.c.ks)[dst[r]] = bad ? __int_as_float(0x7fffffff) : q;
     }
-    // below 2^-100 the inverse would pass fp32's range: such a row is zero
-    const bool nz = amax >= 7.8886e-31f;
-    const float inv = nz ? __fdiv_rn(448.f, amax) : 0.f;
-    uint32_t w[2];
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      w[g] = 0;
-#pragma unroll
-      for (int i = 0; i < 4; i += 2)
-        w[g] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(
-                    make_float2(__fmul_rn(x[4 * g + i], inv), __fmul_rn(x[4 * g + i + 1], inv)),
-                    __NV_SATFINITE, __NV_E4M3))
-                << (8 * i);
-    }
-    reinterpret_cast<uint2*>(pool + dst * D)[lane] = make_uint2(w[0], w[1]);
-    if (lane == 0)
-      (kv ? a.c.vs : a.c.ks)[dst] = bad > 0.f ? __int_as_float(0x7fffffff)
-                                              : (nz ? __fdiv_rn(amax, 448.f) : 0.f);
   }
 }
 
 template <typename T, int D, bool E>
 static cudaError_t append_go(const AppendArgs& a, cudaStream_t st) {
-  const long long rows = (long long)a.B * a.c.Hkv * a.T;
-  const long long blocks = (rows + 256 / (D / 8) - 1) / (256 / (D / 8));
-  k_cache_append<T, D, E><<<dim3((unsigned)blocks, 2), 256, 0, st>>>(a);
+  const int rows = 256 / (D / 16) * kAppendRows;
+  const int blocks = (a.T + rows - 1) / rows;
+  k_cache_append<T, D, E><<<dim3((unsigned)(a.B * a.c.Hkv), blocks < 65535 ? blocks : 65535, 2), 256, 0, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -141,10 +177,12 @@ static cudaError_t append_pick(const AppendArgs& a, int d, bool e4m3, cudaStream
 // ---------------------------------------------------------------------------
 // Choice of the tokens to keep.  One block per (sequence, head).  The tallies
 // of the middle (neither among the first `sinks` nor the last `recent`) are
-// mapped to integers of the same order (NaN lowest, -0 like +0), the
-// (keep - sinks - recent)-th largest is found by four 8-bit radix passes, and one
-// pass in slot order writes the chosen slots ascending, the equal ones from the
-// lowest slot on.
+// mapped to integers of the same order (NaN lowest, -0 like +0) and kept in shared
+// memory while they fit there (SMEM: one pass over the tally).  The
+// (keep - sinks - recent)-th largest is found by three radix passes of 11, 11 and 10
+// bits; then each thread counts its run of consecutive slots, a scan over the block gives
+// where its choices go, and the chosen slots are written ascending, the equal ones
+// from the lowest slot on.
 struct SelectArgs {
   const float* acc;
   long long sb, sh;        // strides of acc in elements
@@ -161,14 +199,49 @@ __device__ __forceinline__ uint32_t tally_key(float x) {
 }
 
 constexpr int kSelThreads = 1024;
+constexpr int kSelBins = 2048;
+constexpr int kSelKeys = 54000;          // of the middle that fit beside the rest (227 KB)
 
+// Exclusive sums over the block (1024 threads); *all: the total.
+__device__ __forceinline__ uint2 scan_block(uint2 v, uint2 (&part)[32], uint2* all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint2 incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t x = __shfl_up_sync(0xffffffffu, incl.x, o), y = __shfl_up_sync(0xffffffffu, incl.y, o);
+    if (lane >= o) {
+      incl.x += x;
+      incl.y += y;
+    }
+  }
+  __syncthreads();                       // part is free
+  if (lane == 31) part[warp] = incl;
+  __syncthreads();
+  uint2 w = part[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t x = __shfl_up_sync(0xffffffffu, w.x, o), y = __shfl_up_sync(0xffffffffu, w.y, o);
+    if (lane >= o) {
+      w.x += x;
+      w.y += y;
+    }
+  }
+  all->x = __shfl_sync(0xffffffffu, w.x, 31);
+  all->y = __shfl_sync(0xffffffffu, w.y, 31);
+  uint2 before = make_uint2(__shfl_sync(0xffffffffu, w.x, (warp + 31) & 31),
+                            __shfl_sync(0xffffffffu, w.y, (warp + 31) & 31));
+  if (warp == 0) before = make_uint2(0u, 0u);
+  return make_uint2(before.x + incl.x - v.x, before.y + incl.y - v.y);
+}
+
+template <bool SMEM>
 __global__ void __launch_bounds__(kSelThreads) k_cache_select(SelectArgs a) {
-  __shared__ uint32_t hist[256];
+  extern __shared__ uint32_t keys[];     // SMEM: the middle
+  __shared__ uint32_t hist[kSelBins];
+  __shared__ uint2 part[32];
   __shared__ uint32_t s_prefix;
   __shared__ int s_need;
-  __shared__ int wsum[2][kSelThreads / 32];
   const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
-  const int lane = tid & 31, warp = tid >> 5;
   int len = __ldg(a.lens + b);
   if (len < 0 || len > a.S) {
     if (tid == 0) atomicOr(&g_device_error, DEVERR_BOUNDS);
@@ -182,90 +255,95 @@ __global__ void __launch_bounds__(kSelThreads) k_cache_select(SelectArgs a) {
     for (int i = tid; i < m; i += kSelThreads) out[i] = i;
     return;
   }
-  const float* acc = a.acc + b * a.sb + h * a.sh;
-  const int lo = a.sinks, hi = len - a.recent;     // the middle: [lo, hi), longer than `want`
+  const int lo = a.sinks, n = len - a.recent - lo;   // the middle: n slots from lo on, more than `want`
   const int want = a.keep - a.sinks - a.recent;
   for (int i = tid; i < lo; i += kSelThreads) out[i] = i;
-  for (int i = tid; i < a.recent; i += kSelThreads) out[lo + want + i] = hi + i;
+  for (int i = tid; i < a.recent; i += kSelThreads) out[lo + want + i] = lo + n + i;
   if (want == 0) return;
+  const float* acc = a.acc + b * a.sb + h * a.sh + lo;
+  auto key = [&](int i) { return SMEM ? keys[i] : tally_key(__ldg(acc + i)); };
+  for (int i = tid; i < kSelBins; i += kSelThreads) hist[i] = 0;
+  __syncthreads();
   uint32_t prefix = 0;
-  int need = want;                                  // still to take among those with the prefix
-  for (int pass = 0; pass < 4; ++pass) {
-    const int shift = 24 - 8 * pass;
-    for (int i = tid; i < 256; i += kSelThreads) hist[i] = 0;
-    __syncthreads();
-    for (int s = lo + tid; s < hi; s += kSelThreads) {
-      const uint32_t key = tally_key(__ldg(acc + s));
-      if (pass == 0 || (key >> (shift + 8)) == prefix) atomicAdd(&hist[(key >> shift) & 255], 1u);
+  int need = want;                       // still to take among those with the prefix
+#pragma unroll
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+    if (pass == 0 && SMEM) {
+#pragma unroll 8
+      for (int i = tid; i < n; i += kSelThreads) {
+        const uint32_t k = tally_key(__ldg(acc + i));
+        keys[i] = k;
+        atomicAdd(&hist[k >> 21], 1u);
+      }
+    } else {
+#pragma unroll 4
+      for (int i = tid; i < n; i += kSelThreads) {
+        const uint32_t k = key(i);
+        if (pass == 0 || (k >> (shift + bits)) == prefix) atomicAdd(&hist[(k >> shift) & ((1 << bits) - 1)], 1u);
+      }
     }
     __syncthreads();
-    if (tid < 32) {
-      // lane L sums bins 255-8L .. 248-8L; the largest bins come first
-      uint32_t v[8], sum = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        v[i] = hist[255 - 8 * lane - i];
-        sum += v[i];
-      }
-      uint32_t incl = sum;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-      }
-      uint32_t before = incl - sum;
-      if (before < (uint32_t)need && incl >= (uint32_t)need) {
-        int i = 0;
-        while (before + v[i] < (uint32_t)need) before += v[i++];
-        s_prefix = (prefix << 8) | (255 - 8 * lane - i);
-        s_need = need - (int)before;
-      }
+    // the bins from the largest on, two a thread
+    const int top = kSelBins - 1 - 2 * tid;
+    const uint32_t v0 = hist[top], v1 = hist[top - 1];
+    uint2 all;
+    const uint32_t before = scan_block(make_uint2(v0 + v1, 0u), part, &all).x;
+    if (before < (uint32_t)need && before + v0 + v1 >= (uint32_t)need) {
+      const bool first = before + v0 >= (uint32_t)need;
+      s_prefix = (prefix << bits) | (uint32_t)(first ? top : top - 1);
+      s_need = need - (int)(before + (first ? 0u : v0));
     }
+    hist[top] = 0;
+    hist[top - 1] = 0;
     __syncthreads();
     prefix = s_prefix;
     need = s_need;
-    __syncthreads();
   }
-  // prefix is now the threshold key; `need` of the equal ones are kept
-  int taken = 0, ties = 0;
-  for (int s0 = lo; s0 < hi; s0 += kSelThreads) {
-    const int s = s0 + tid;
-    const uint32_t key = s < hi ? tally_key(__ldg(acc + s)) : 0u;
-    const bool gt = s < hi && key > prefix, eq = s < hi && key == prefix;
-    const unsigned bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq);
-    if (lane == 0) {
-      wsum[0][warp] = __popc(bg);
-      wsum[1][warp] = __popc(be);
-    }
-    __syncthreads();
-    int g0 = 0, e0 = 0, gall = 0, eall = 0;
-    for (int w = 0; w < kSelThreads / 32; ++w) {
-      const int cg = wsum[0][w], ce = wsum[1][w];
-      if (w < warp) {
-        g0 += cg;
-        e0 += ce;
-      }
-      gall += cg;
-      eall += ce;
-    }
-    const unsigned below = (1u << lane) - 1u;
-    const int eqs = ties + e0 + __popc(be & below);        // equal ones before this slot
-    const int gts = taken + g0 + __popc(bg & below);       // larger ones before this slot
-    if (gt || (eq && eqs < need)) out[lo + gts + min(eqs, need)] = s;
-    taken += gall;
-    ties += eall;
-    __syncthreads();
+  // prefix is now the threshold key; `need` of the equal ones are kept.  An odd run of slots a
+  // thread: the threads of a warp read different banks.
+  const int per = ((n + kSelThreads - 1) / kSelThreads) | 1;
+  const int i0 = tid * per < n ? tid * per : n, i1 = min(n, i0 + per);
+  uint2 mine = make_uint2(0u, 0u);       // larger, equal
+  for (int i = i0; i < i1; ++i) {
+    const uint32_t k = key(i);
+    mine.x += k > prefix;
+    mine.y += k == prefix;
   }
+  uint2 all;
+  uint2 at = scan_block(mine, part, &all);
+  for (int i = i0; i < i1; ++i) {
+    const uint32_t k = key(i);
+    if (k > prefix) out[lo + at.x++ + min(at.y, (uint32_t)need)] = lo + i;
+    else if (k == prefix) {
+      if (at.y < (uint32_t)need) out[lo + at.x + at.y] = lo + i;
+      ++at.y;
+    }
+  }
+}
+
+static cudaError_t launch_select(const SelectArgs& a, int B, cudaStream_t st) {
+  // the longest middle that the tally's extent allows
+  const long long n = (long long)a.S - a.sinks - a.recent;
+  if (n <= kSelKeys) {
+    const int smem = (int)(n > 0 ? n : 0) * 4;
+    const cudaError_t e =
+        cudaFuncSetAttribute(k_cache_select<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelKeys * 4);
+    if (e != cudaSuccess) return e;
+    k_cache_select<true><<<dim3(a.Hkv, B), kSelThreads, smem, st>>>(a);
+  } else {
+    k_cache_select<false><<<dim3(a.Hkv, B), kSelThreads, 0, st>>>(a);
+  }
+  return cudaGetLastError();
 }
 
 // ---------------------------------------------------------------------------
 // Row moves: slot base[b]+i of out_table <- slot idx[b][h][i] of table, i < n[b].
 //
-// In place (out_table is table) a row may only move towards the front
-// (idx[i] >= base + i).  A block then owns one slice of the rows' bytes and walks
-// all its rows in order, a chunk at a time: a chunk is read whole before any of
-// it is written, and what a chunk writes lies before everything that the later
-// chunks read.  Slices do not touch each other, so they run side by side.
+// In place (out_table is table) a row may only move towards the front (idx[i] >= base + i).
+// A block then owns one slice (64 bytes) of the rows of one head and walks them in order, a chunk at a time.  What chunk j writes lies before everything
+// that the chunks after it read, so chunk j + 1 is read before chunk j is written, with
+// one barrier between: all of chunk j has been read by then.  Slices do not touch each other.
 // Otherwise the pages do not overlap and every chunk has its own block.
 struct MoveArgs {
   CacheView c;
@@ -283,103 +361,176 @@ struct MoveArgs {
   int S, SO;               // extent of acc and acc_out along the slots
   int M, row_bytes;        // row_bytes: bytes of one cached row of K or V
   int slice_bytes;         // bytes of a row that one block moves
+  int piece_blocks;        // blocks that move them; the others move the 4-byte values
   int in_place;
 };
 
 constexpr int kMoveThreads = 256;
-constexpr int kMovePer = 4;              // 16-byte pieces of a thread and chunk
+constexpr int kMovePieces = 4;           // 16-byte pieces of a row that one thread moves
+// Rows of a thread and chunk; in place a thread holds two chunks.
+template <bool INPLACE>
+constexpr int kMoveRows = INPLACE ? 1 : 2;
 
-__global__ void __launch_bounds__(kMoveThreads) k_cache_move(MoveArgs a) {
-  const int slices = a.row_bytes / a.slice_bytes;
+// A block's part of a head's rows: one slice of K or V, or the 4-byte values (scales, tally; a row a
+// thread).  A slice's row is slice/64 lanes with four pieces each, so that the look-up of a row (its
+// index and two pages) is shared by 64 bytes a lane.  Four things follow one another, each a chunk
+// behind: the indices, the pages they name, the data, the writing; none waits for what it has just
+// asked for.
+template <bool INPLACE>
+__global__ void __launch_bounds__(kMoveThreads, 4) k_cache_move(MoveArgs a) {
+  constexpr int NR = kMoveRows<INPLACE>;
   const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
-  int what = blockIdx.x % (2 * slices + 1);      // K slices, V slices, the 4-byte values
-  const int chunk0 = blockIdx.x / (2 * slices + 1);
-  int n = a.n ? __ldg(a.n + b) : a.M;
+  // blocks: the slices of K and of V chunk by chunk, then the words
+  const int slices = a.row_bytes / a.slice_bytes;
+  const bool words = (int)blockIdx.x >= a.piece_blocks;
+  const int what = words ? 0 : blockIdx.x % (2 * slices);
+  const int chunk0 = words ? blockIdx.x - a.piece_blocks : blockIdx.x / (2 * slices);
+  const int n = a.n ? __ldg(a.n + b) : a.M;
   const int base = a.base ? __ldg(a.base + b) : 0;
   if (static_cast<unsigned>(n) > static_cast<unsigned>(a.M) || base < 0 || base > INT_MAX - a.M) {
     if (tid == 0) atomicOr(&g_device_error, DEVERR_BOUNDS);
     return;
   }
   const int* idx = a.idx + b * a.ib + h * a.ih;
-  if (what < 2 * slices) {
-    uint8_t* pool = what < slices ? a.c.k : a.c.v;
-    const int off = (what % slices) * a.slice_bytes;
-    const int ppr = a.slice_bytes / 16;              // pieces of a row
-    const int rpc = kMoveThreads * kMovePer / ppr;   // rows of a chunk
-    const int step = a.in_place ? rpc : rpc * (gridDim.x / (2 * slices + 1));
-    for (int i0 = chunk0 * rpc; i0 < n; i0 += step) {
-      uint4 v[kMovePer];
-      long long dst[kMovePer];
-#pragma unroll
-      for (int u = 0; u < kMovePer; ++u) {
-        const int p = u * kMoveThreads + tid;
-        const int i = i0 + p / ppr;
-        dst[u] = -1;
-        if (i < n) {
-          const int s = __ldg(idx + i);
-          if (a.in_place && s < base + i) {
-            atomicOr(&g_device_error, DEVERR_BOUNDS);
-          } else if (!(a.in_place && s == base + i)) {
-            const long long src = cache_row(a.c, a.table, a.MP, b, h, s);
-            const long long to = cache_row(a.c, a.out_table, a.MO, b, h, base + i);
-            if (src >= 0 && to >= 0) {
-              dst[u] = to * a.row_bytes + off + 16 * (p % ppr);
-              v[u] = *reinterpret_cast<const uint4*>(pool + src * a.row_bytes + off + 16 * (p % ppr));
-            }
-          }
-        }
-      }
-      if (a.in_place) __syncthreads();
-#pragma unroll
-      for (int u = 0; u < kMovePer; ++u)
-        if (dst[u] >= 0) *reinterpret_cast<uint4*>(pool + dst[u]) = v[u];
-    }
-    return;
-  }
-  // the scales and the tally: one block walks all rows
-  if (chunk0 != 0) return;
+  const int* table = a.table + (size_t)b * a.MP;
+  const int* out_table = a.out_table + (size_t)b * a.MO;
+  const int lanes = words ? 1 : a.slice_bytes / (16 * kMovePieces), shift = 31 - __clz(lanes);
+  const int pass = kMoveThreads >> shift, rpc = pass * NR;       // rows of a pass, of a chunk
+  const int lane = tid & (lanes - 1), row0 = tid >> shift;
+  uint8_t* pool = (what < slices ? a.c.k : a.c.v) + (size_t)(what % slices) * a.slice_bytes + 16 * lane;
   const float* acc = a.acc ? a.acc + b * a.ab + h * a.ah : nullptr;
   float* acc_out = a.acc_out ? a.acc_out + b * a.ob + h * a.oh : nullptr;
-  for (int i0 = 0; i0 < n; i0 += kMoveThreads) {
-    const int i = i0 + tid;
-    long long to = -1;
-    int s = -1;
-    float ks = 0.f, vs = 0.f, t = 0.f;
-    if (i < n) {
-      s = __ldg(idx + i);
-      if (s < 0 || (a.in_place && s < base + i)) {
+  const int last = INPLACE ? n : min(n, (chunk0 + 1) * rpc);
+  auto ask_idx = [&](int (&s)[NR], int i0) {
+#pragma unroll
+    for (int u = 0; u < NR; ++u) {
+      const int i = i0 + u * pass + row0;
+      s[u] = i < last ? __ldg(idx + i) : 0;
+    }
+  };
+  struct Pages {
+    int slot[NR];                        // -1: nothing to move
+    int src[NR], dst[NR];
+  };
+  auto ask_pages = [&](Pages& p, const int (&s)[NR], int i0) {
+#pragma unroll
+    for (int u = 0; u < NR; ++u) {
+      const int i = i0 + u * pass + row0, to = base + i;
+      p.slot[u] = -1;
+      if (i >= last) continue;
+      if (!slot_inside(s[u], a.c.page_shift, a.MP) || !slot_inside(to, a.c.page_shift, a.MO) ||
+          (INPLACE && s[u] < to)) {
         atomicOr(&g_device_error, DEVERR_BOUNDS);
-        s = -1;
+        continue;
+      }
+      p.slot[u] = s[u];
+      p.src[u] = __ldg(table + (s[u] >> a.c.page_shift));
+      p.dst[u] = __ldg(out_table + (to >> a.c.page_shift));
+    }
+  };
+  struct Data {
+    uint4 v[NR][kMovePieces];            // words: key scale, value scale, tally in the first
+    int to[NR];                          // row written (rows over the pool are 31-bit); -1: none
+  };
+  auto ask_data = [&](Data& x, const Pages& p, int i0) {
+#pragma unroll
+    for (int u = 0; u < NR; ++u) {
+      x.to[u] = -1;
+      if (p.slot[u] < 0) continue;
+      if (!page_inside(p.src[u], a.c.pages) || !page_inside(p.dst[u], a.c.pages)) {
+        atomicOr(&g_device_error, DEVERR_BOUNDS);
+        continue;
+      }
+      const int to = base + i0 + u * pass + row0;
+      const long long src = row_of(p.src[u], a.c.Hkv, h, a.c.page_shift, p.slot[u]);
+      x.to[u] = (int)row_of(p.dst[u], a.c.Hkv, h, a.c.page_shift, to);
+      if (!words) {
+        if (INPLACE && p.slot[u] == to) {
+          x.to[u] = -1;                                           // it stays
+        } else {
+          const uint8_t* from = pool + src * a.row_bytes;
+#pragma unroll
+          for (int y = 0; y < kMovePieces; ++y)
+            x.v[u][y] = *reinterpret_cast<const uint4*>(from + ((16 * y) << shift));
+        }
       } else {
         if (a.c.ks) {
-          const long long src = cache_row(a.c, a.table, a.MP, b, h, s);
-          to = cache_row(a.c, a.out_table, a.MO, b, h, base + i);
-          if (src < 0) to = -1;
-          if (to >= 0) {
-            ks = a.c.ks[src];
-            vs = a.c.vs[src];
-          }
+          x.v[u][0].x = __float_as_uint(a.c.ks[src]);
+          x.v[u][0].y = __float_as_uint(a.c.vs[src]);
         }
-        if (acc && s < a.S) t = acc[s];
+        if (acc) x.v[u][0].z = p.slot[u] < a.S ? __float_as_uint(acc[p.slot[u]]) : 0u;
       }
     }
-    __syncthreads();
-    if (to >= 0) {
-      a.c.ks[to] = ks;
-      a.c.vs[to] = vs;
+  };
+  auto write = [&](const Data& x, int i0) {
+#pragma unroll
+    for (int u = 0; u < NR; ++u) {
+      if (x.to[u] < 0) continue;
+      if (!words) {
+        uint8_t* into = pool + (long long)x.to[u] * a.row_bytes;
+#pragma unroll
+        for (int y = 0; y < kMovePieces; ++y)
+          *reinterpret_cast<uint4*>(into + ((16 * y) << shift)) = x.v[u][y];
+      } else {
+        if (a.c.ks) {
+          a.c.ks[x.to[u]] = __uint_as_float(x.v[u][0].x);
+          a.c.vs[x.to[u]] = __uint_as_float(x.v[u][0].y);
+        }
+        const int to = base + i0 + u * pass + row0;
+        if (acc_out && to < a.SO) acc_out[to] = __uint_as_float(x.v[u][0].z);
+      }
     }
-    if (acc_out && s >= 0 && base + i < a.SO) acc_out[base + i] = t;
+  };
+  int s[NR];
+  Pages p;
+  Data x0;
+  if (!INPLACE) {
+    const int i0 = chunk0 * rpc;
+    ask_idx(s, i0);
+    ask_pages(p, s, i0);
+    ask_data(x0, p, i0);
+    write(x0, i0);
+    return;
+  }
+  Data x1;
+  ask_idx(s, 0);
+  ask_pages(p, s, 0);
+  ask_idx(s, rpc);
+  ask_data(x0, p, 0);
+  ask_pages(p, s, rpc);
+  ask_idx(s, 2 * rpc);
+  // the data of chunk i0 is on its way, with the pages of the one after it and the indices of the next
+  for (int i0 = 0; i0 < n; i0 += 2 * rpc) {
+    ask_data(x1, p, i0 + rpc);
+    ask_pages(p, s, i0 + 2 * rpc);
+    ask_idx(s, i0 + 3 * rpc);
     __syncthreads();
+    write(x0, i0);
+    if (i0 + rpc >= n) break;
+    ask_data(x0, p, i0 + 2 * rpc);
+    ask_pages(p, s, i0 + 3 * rpc);
+    ask_idx(s, i0 + 4 * rpc);
+    __syncthreads();
+    write(x1, i0 + rpc);
   }
 }
 
 static cudaError_t launch_move(MoveArgs a, int B, cudaStream_t st) {
   if (a.M == 0) return cudaSuccess;
-  a.slice_bytes = a.in_place ? (a.row_bytes >= 64 ? 64 : a.row_bytes) : a.row_bytes;
+  // In place a block walks all rows of its slice: whole rows where the heads fill the SMs twice, else
+  // slices down to 64 bytes.
+  a.slice_bytes = a.row_bytes;
+  while (a.in_place && a.slice_bytes > 64 &&
+         (int64_t)B * a.c.Hkv * 2 * (a.row_bytes / a.slice_bytes) < 2 * 148)
+    a.slice_bytes /= 2;
   const int slices = a.row_bytes / a.slice_bytes;
-  const int rpc = kMoveThreads * kMovePer / (a.slice_bytes / 16);
-  const int chunks = a.in_place ? 1 : (a.M + rpc - 1) / rpc;
-  k_cache_move<<<dim3((unsigned)(chunks * (2 * slices + 1)), a.c.Hkv, B), kMoveThreads, 0, st>>>(a);
+  const int per = kMoveThreads * (a.in_place ? kMoveRows<true> : kMoveRows<false>);
+  const int rpc = per / (a.slice_bytes / (16 * kMovePieces));
+  a.piece_blocks = (a.in_place ? 1 : (a.M + rpc - 1) / rpc) * 2 * slices;
+  const int word_blocks = a.c.ks || a.acc ? (a.in_place ? 1 : (a.M + per - 1) / per) : 0;
+  const dim3 grid((unsigned)(a.piece_blocks + word_blocks), a.c.Hkv, B);
+  if (a.in_place) k_cache_move<true><<<grid, kMoveThreads, 0, st>>>(a);
+  else k_cache_move<false><<<grid, kMoveThreads, 0, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -474,7 +625,7 @@ sage2_status sage2_cache_append(const void* k, const void* v, int dtype, const i
   if (!e4m3 && dtype != a.c.kv_dtype) return SAGE2_ERR_INVALID_ARG;
   if (T <= 0) return SAGE2_ERR_INVALID_ARG;
   if (T > (max_pages << a.c.page_shift)) return SAGE2_ERR_INVALID_ARG;
-  if ((int64_t)B * a.c.Hkv * T > (int64_t)INT32_MAX * 8) return SAGE2_ERR_UNSUPPORTED;
+  if ((int64_t)B * a.c.Hkv > INT32_MAX) return SAGE2_ERR_UNSUPPORTED;
   s = check_ptrs(k, v);
   if (s != SAGE2_OK) return s;
   s = check_words(table, lens);
@@ -594,8 +745,7 @@ sage2_status sage2_cache_evict(const sage2_cache* cache, const int* table, int m
   a.base = nullptr;
   SelectArgs sel{acc, a.ab, a.ah, lens, idx, new_lens, a.c.Hkv, S, keep, sinks, recent};
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  k_cache_select<<<dim3(a.c.Hkv, B), kSelThreads, 0, st>>>(sel);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_select(sel, B, st);
   if (e == cudaSuccess) e = launch_move(a, B, st);
   return from_cuda(e);
 }

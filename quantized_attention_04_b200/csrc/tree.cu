@@ -39,6 +39,7 @@ struct TreeArgs {
   int RT;                   // row tiles of a (sequence, head) pair
   float* part;              // [2*grid][rows of a tile][d]
   float2* part_ml;          // [2*grid][rows of a tile]: (max in log2 units, sum)
+  long long* before;        // [B + 1]: tiles of the sequences before b; the last: of all
 };
 
 // Context length and drafted tokens of sequence b, held to what the table can hold.
@@ -132,6 +133,26 @@ __device__ __forceinline__ Run warp_run(const TreeArgs& a, int tile, int pairs, 
     before += __shfl_sync(0xffffffffu, incl, 31);
   }
   return r;
+}
+
+// What the join needs of the split: the tiles before each sequence.  By one warp of the launch.
+__device__ __forceinline__ void write_before(const TreeArgs& a, int tile, int pairs) {
+  const int lane = threadIdx.x & 31;
+  long long before = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    long long incl = 0;
+    if (b0 + lane < a.B)
+      incl = (long long)pair_tiles(seq_len(a.lens, a.n, b0 + lane, a.T, a.MP, a.c.page_shift), tile) * pairs;
+    const long long mine = incl;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (b0 + lane < a.B) a.before[b0 + lane] = before + incl - mine;
+    before += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  if (lane == 0) a.before[a.B] = before;
 }
 
 // Walks the tiles of a run.
@@ -236,6 +257,11 @@ __device__ __forceinline__ void store4(void* out, int dtype, size_t idx, const f
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + idx) = w;
   }
 }
+// Two consecutive values (index of the first, even) in the output type.
+__device__ __forceinline__ void store2(void* out, int dtype, size_t idx, float x, float y) {
+  if (dtype == 2) *reinterpret_cast<float2*>(static_cast<float*>(out) + idx) = make_float2(x, y);
+  else *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(out) + idx) = dtype == 1 ? pack2<true>(x, y) : pack2<false>(x, y);
+}
 // ln of a row's sum of exponentials from its maximum (log2 units) and the sum relative to it.
 __device__ __forceinline__ float row_lse(float m, float sum) {
   return (m + log2f(sum)) * 0.6931471805599453f;
@@ -312,6 +338,7 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 2)
     fence_mbar_init();
   }
   const Run run = warp_run(a, kRowsTile, pairs, gridDim.x, blockIdx.x, kRowsLeast);
+  if (blockIdx.x == gridDim.x - 1 && warp == 0) write_before(a, kRowsTile, pairs);
   __syncthreads();
   const int nt = run.n;
   if (nt == 0) return;
@@ -723,73 +750,140 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 2)
 }
 
 // ------------------------------------------------------------ adding pieces
-// One warp per row.  Rows of a pair that one block covered are done; the others
-// (and the pairs without any tile) are written here.
+// Rows of a pair that one block covered are done; the others (and the pairs without any tile) are
+// written here.  The pieces' maxima and sums are read at once, then the channels of all pieces with
+// loads that do not wait for one another (a warp that went from piece to piece took 23 us for
+// the 37 pieces of one token's heads).  k_tree_join: a block a row, thread d for channel d; for
+// rows of many pieces.  k_tree_join_few: a warp a row.
+constexpr int kMostBlocks = 1024;       // of a split
+constexpr int kJoinFew = 8;             // blocks a pair from which on a row has a block
 template <int D>
-__global__ void __launch_bounds__(128) k_tree_join(const __grid_constant__ TreeArgs a, int tile,
-                                                   int rows_tile, int grid, int least) {
-  __shared__ long long scratch[4];
-  const int pairs = a.c.Hkv * a.RT;
-  const int b = blockIdx.z, h = blockIdx.y;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+__global__ void __launch_bounds__(128) k_tree_join_few(const __grid_constant__ TreeArgs a, int tile,
+                                                       int rows_tile, int grid, int least) {
+  const int b = blockIdx.z, h = blockIdx.y, lane = threadIdx.x & 31;
+  const int R = a.G * a.T, r = blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (r >= R) return;
   const SeqLen s = seq_len(a.lens, a.n, b, a.T, a.MP, a.c.page_shift);
   const int tiles = pair_tiles(s, tile);
-  // tiles before this sequence, and in all
-  long long before = 0, total = 0;
-  for (int x = tid; x < a.B; x += 128) {
-    const long long v =
-        (long long)pair_tiles(seq_len(a.lens, a.n, x, a.T, a.MP, a.c.page_shift), tile) * pairs;
-    total += v;
-    if (x < b) before += v;
-  }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    before += __shfl_xor_sync(0xffffffffu, before, o);
-    total += __shfl_xor_sync(0xffffffffu, total, o);
-  }
-  if (lane == 0) scratch[warp] = before;
-  __syncthreads();
-  before = scratch[0] + scratch[1] + scratch[2] + scratch[3];
-  __syncthreads();
-  if (lane == 0) scratch[warp] = total;
-  __syncthreads();
-  total = scratch[0] + scratch[1] + scratch[2] + scratch[3];
-  const int gr = run_blocks(total, grid, least);
-  const int R = a.G * a.T;
-  const int r = blockIdx.x * 4 + warp;
-  if (r >= R) return;
   const int i = r % a.T;
   const size_t orow = ((size_t)b * a.Hq + h * a.G + r / a.T) * a.T + i;
   constexpr int PER = D / 32;
   float o[PER] = {};
   float M = -INFINITY, sum = 0.f;
   if (tiles > 0) {
-    const long long P0 = before + (long long)(h * a.RT + r / rows_tile) * tiles, P1 = P0 + tiles;
-    const int c0 = run_of(P0, total, gr), c1 = run_of(P1 - 1, total, gr);
-    if (c0 == c1) return;
-    for (int x = c0; x <= c1; ++x) {
-      const size_t prow = (size_t)(2 * x + (x == c0 ? 1 : 0)) * rows_tile + r % rows_tile;
-      const float2 ml = a.part_ml[prow];
-      const float mn = fmaxf(M, ml.x), mb = mn == -INFINITY ? 0.f : mn;
-      const float f0 = ex2(M - mb), f1 = ex2(ml.x - mb);
-      const float* src = a.part + prow * D + lane * PER;
+    const long long total = a.before[a.B];
+    const int gr = run_blocks(total, grid, least);
+    const long long P0 = a.before[b] + (long long)(h * a.RT + r / rows_tile) * tiles;
+    const int c0 = run_of(P0, total, gr), np = run_of(P0 + tiles - 1, total, gr) - c0 + 1;
+    if (np == 1) return;
+    const size_t prow0 = (size_t)2 * c0 * rows_tile + r % rows_tile;
+    for (int x0 = 0; x0 < np; x0 += 32) {
+      const int x = x0 + lane, m = min(32, np - x0);
+      const float2 ml = x < np ? a.part_ml[prow0 + (size_t)(2 * x + (x == 0 ? 1 : 0)) * rows_tile]
+                               : make_float2(-INFINITY, 0.f);
+      float mn = ml.x;
 #pragma unroll
-      for (int y = 0; y < PER; ++y) o[y] = o[y] * f0 + src[y] * f1;
-      sum = sum * f0 + ml.y * f1;
+      for (int k = 16; k; k >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, k));
+      mn = fmaxf(mn, M);
+      const float mb = mn == -INFINITY ? 0.f : mn;
+      const float f0 = ex2(M - mb), f1 = ex2(ml.x - mb);
+      float part = f1 * ml.y;
+#pragma unroll
+      for (int k = 16; k; k >>= 1) part += __shfl_xor_sync(0xffffffffu, part, k);
+      sum = sum * f0 + part;
       M = mn;
+#pragma unroll
+      for (int y = 0; y < PER; ++y) o[y] *= f0;
+#pragma unroll 4
+      for (int z = 0; z < m; ++z) {
+        const int xx = x0 + z;
+        const float f = __shfl_sync(0xffffffffu, f1, z);
+        const float* src = a.part + (prow0 + (size_t)(2 * xx + (xx == 0 ? 1 : 0)) * rows_tile) * D + lane * PER;
+        if (PER == 4) {
+          const float4 v = *reinterpret_cast<const float4*>(src);
+          o[0] += f * v.x;
+          o[1] += f * v.y;
+          o[PER - 2] += f * v.z;
+          o[PER - 1] += f * v.w;
+        } else {
+          const float2 v = *reinterpret_cast<const float2*>(src);
+          o[0] += f * v.x;
+          o[1] += f * v.y;
+        }
+      }
     }
   }
   const bool none = i >= s.n || sum == 0.f;
   const float inv = none ? 0.f : 1.f / sum;
 #pragma unroll
-  for (int y = 0; y < PER; ++y) {
-    const float v = none ? 0.f : o[y] * inv;
-    const size_t idx = orow * D + lane * PER + y;
-    if (a.o_dtype == 0) static_cast<__half*>(a.o)[idx] = __float2half_rn(v);
-    else if (a.o_dtype == 1) static_cast<__nv_bfloat16*>(a.o)[idx] = __float2bfloat16_rn(v);
-    else static_cast<float*>(a.o)[idx] = v;
+  for (int y = 0; y < PER; ++y) o[y] = none ? 0.f : o[y] * inv;
+  const size_t idx = orow * D + lane * PER;
+  if (PER == 4) {
+    const float f4[4] = {o[0], o[1], o[PER - 2], o[PER - 1]};
+    store4(a.o, a.o_dtype, idx, f4);
+  } else {
+    store2(a.o, a.o_dtype, idx, o[0], o[1]);
   }
   if (a.lse && lane == 0) a.lse[orow] = none ? -INFINITY : row_lse(M, sum);
+}
+
+template <int D>
+__global__ void __launch_bounds__(128) k_tree_join(const __grid_constant__ TreeArgs a, int tile,
+                                                   int rows_tile, int grid, int least) {
+  __shared__ float fac[kMostBlocks];
+  __shared__ float red[2][4];
+  __shared__ float half[D];
+  const int b = blockIdx.z, h = blockIdx.y, r = blockIdx.x;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const SeqLen s = seq_len(a.lens, a.n, b, a.T, a.MP, a.c.page_shift);
+  const int tiles = pair_tiles(s, tile);
+  const int i = r % a.T;
+  const size_t orow = ((size_t)b * a.Hq + h * a.G + r / a.T) * a.T + i;
+  float M = -INFINITY, sum = 0.f, o = 0.f;
+  if (tiles > 0) {
+    const long long total = a.before[a.B];
+    const int gr = run_blocks(total, grid, least);
+    const long long P0 = a.before[b] + (long long)(h * a.RT + r / rows_tile) * tiles;
+    const int c0 = run_of(P0, total, gr), np = run_of(P0 + tiles - 1, total, gr) - c0 + 1;
+    if (np == 1) return;
+    const size_t prow0 = (size_t)2 * c0 * rows_tile + r % rows_tile;
+    auto prow = [&](int x) { return prow0 + (size_t)(2 * x + (x == 0 ? 1 : 0)) * rows_tile; };
+    for (int x = tid; x < np; x += 128) M = fmaxf(M, a.part_ml[prow(x)].x);
+#pragma unroll
+    for (int k = 16; k; k >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, k));
+    if (lane == 0) red[0][warp] = M;
+    __syncthreads();
+    M = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+    const float mb = M == -INFINITY ? 0.f : M;
+    for (int x = tid; x < np; x += 128) {
+      const float2 ml = a.part_ml[prow(x)];
+      fac[x] = ex2(ml.x - mb);
+      sum += fac[x] * ml.y;
+    }
+#pragma unroll
+    for (int k = 16; k; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+    if (lane == 0) red[1][warp] = sum;
+    __syncthreads();
+    sum = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
+    // D = 64: the two halves of the block take every other piece
+    constexpr int kStep = 128 / D;
+    const float* src = a.part + tid % D;
+#pragma unroll 8
+    for (int x = tid / D; x < np; x += kStep) o += fac[x] * src[prow(x) * D];
+    if (kStep == 2) {
+      if (tid >= D) half[tid - D] = o;
+      __syncthreads();
+      if (tid < D) o += half[tid];
+    }
+  }
+  if (tid >= D) return;
+  const bool none = i >= s.n || sum == 0.f;
+  const float v = none ? 0.f : o / sum;
+  const size_t idx = orow * D + tid;
+  if (a.o_dtype == 0) static_cast<__half*>(a.o)[idx] = __float2half_rn(v);
+  else if (a.o_dtype == 1) static_cast<__nv_bfloat16*>(a.o)[idx] = __float2bfloat16_rn(v);
+  else static_cast<float*>(a.o)[idx] = v;
+  if (a.lse && tid == 0) a.lse[orow] = none ? -INFINITY : row_lse(M, sum);
 }
 
 // ------------------------------------------------------------ weights
@@ -935,9 +1029,32 @@ static int sm_count(int dev) {
     int v = 0;
     if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0)
       v = 148;
-    n[dev] = v;
+    n[dev] = v < kMostBlocks / 2 ? v : kMostBlocks / 2;
   }
   return n[dev];
+}
+
+// Workspace of a split: partial rows, their maxima and sums, the tiles before each sequence.
+static cudaError_t split_workspace(TreeArgs* a, size_t prow, int D, cudaMemPool_t pool, cudaStream_t st) {
+  const size_t p = up256(prow * D * 4), m = up256(prow * 8);
+  uint8_t* ws = nullptr;
+  const cudaError_t e = cudaMallocFromPoolAsync(reinterpret_cast<void**>(&ws), p + m + (size_t)(a->B + 1) * 8,
+                                                pool, st);
+  if (e != cudaSuccess) return e;
+  a->part = reinterpret_cast<float*>(ws);
+  a->part_ml = reinterpret_cast<float2*>(ws + p);
+  a->before = reinterpret_cast<long long*>(ws + p + m);
+  return cudaSuccess;
+}
+
+template <int D>
+static cudaError_t launch_join(const TreeArgs& a, int tile, int rows_tile, int grid, int least, cudaStream_t st) {
+  const int R = a.G * a.T;
+  if ((int64_t)a.B * a.c.Hkv * a.RT * kJoinFew <= grid)
+    k_tree_join<D><<<dim3(R, a.c.Hkv, a.B), 128, 0, st>>>(a, tile, rows_tile, grid, least);
+  else
+    k_tree_join_few<D><<<dim3((R + 3) / 4, a.c.Hkv, a.B), 128, 0, st>>>(a, tile, rows_tile, grid, least);
+  return cudaGetLastError();
 }
 
 template <int D, bool E4M3, bool QBF, int MT>
@@ -955,11 +1072,8 @@ static cudaError_t launch_rows(TreeArgs a, int dev, cudaMemPool_t pool, cudaStre
   if (e == cudaSuccess) e = make_tmap(&tv, a.c.v, 2, dims, strides, box, eb, C::kBoxBytes);
   if (e != cudaSuccess) return e;
   const size_t prow = (size_t)2 * grid * 16 * MT;
-  uint8_t* ws = nullptr;
-  e = cudaMallocFromPoolAsync(reinterpret_cast<void**>(&ws), up256(prow * D * 4) + prow * 8, pool, st);
+  e = split_workspace(&a, prow, D, pool, st);
   if (e != cudaSuccess) return e;
-  a.part = reinterpret_cast<float*>(ws);
-  a.part_ml = reinterpret_cast<float2*>(ws + up256(prow * D * 4));
   auto kern = k_tree_rows<D, E4M3, QBF, MT>;
   const int smem = sizeof(RowsSmem<D, E4M3>) + 1024;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -968,11 +1082,9 @@ static cudaError_t launch_rows(TreeArgs a, int dev, cudaMemPool_t pool, cudaStre
     e = cudaGetLastError();
   }
   if (e == cudaSuccess) {
-    k_tree_join<D><<<dim3((a.G * a.T + 3) / 4, a.c.Hkv, a.B), 128, 0, st>>>(a, kRowsTile, 16 * MT, grid,
-                                                                          kRowsLeast);
-    e = cudaGetLastError();
+    e = launch_join<D>(a, kRowsTile, 16 * MT, grid, kRowsLeast, st);
   }
-  const cudaError_t e2 = cudaFreeAsync(ws, st);
+  const cudaError_t e2 = cudaFreeAsync(a.part, st);
   return e != cudaSuccess ? e : e2;
 }
 

@@ -192,12 +192,6 @@ __device__ __forceinline__ void tmem_ld16x128_16(uint32_t taddr, uint32_t (&r)[1
       : "r"(taddr));
 }
 
-// Two consecutive values (index of the first, even) in the output type.
-__device__ __forceinline__ void store2(void* out, int dtype, size_t idx, float x, float y) {
-  if (dtype == 2) *reinterpret_cast<float2*>(static_cast<float*>(out) + idx) = make_float2(x, y);
-  else *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(out) + idx) = dtype == 1 ? pack2<true>(x, y) : pack2<false>(x, y);
-}
-
 // Does the V row of slot `slot`, or one of its scales, hold an infinity or NaN?
 template <int D, bool E4M3, bool BF>
 __device__ __noinline__ bool v_row_bad(const TreeArgs& a, int b, int h, int slot) {
@@ -278,6 +272,7 @@ __global__ void __launch_bounds__(kTThreads<E4M3>, 1)
     return warp_run(a, kTK, pairs, SHARE ? gridDim.x : 2 * gridDim.x, SHARE ? blockIdx.x : 2 * blockIdx.x + s, 1);
   };
   const Run run = run_of_slot(slot & 1);
+  if (blockIdx.x == gridDim.x - 1 && warp == kMma + 2) write_before(a, kTK, pairs);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -950,11 +945,8 @@ static cudaError_t launch_tiles(TreeArgs a, int dev, cudaMemPool_t pool, cudaStr
     if (e != cudaSuccess) return e;
   }
   const size_t prow = (size_t)2 * vgrid * unit;
-  uint8_t* ws = nullptr;
-  e = cudaMallocFromPoolAsync(reinterpret_cast<void**>(&ws), up256(prow * D * 4) + prow * 8, pool, st);
+  e = split_workspace(&a, prow, D, pool, st);
   if (e != cudaSuccess) return e;
-  a.part = reinterpret_cast<float*>(ws);
-  a.part_ml = reinterpret_cast<float2*>(ws + up256(prow * D * 4));
   auto kern = k_tree_tiles<D, E4M3, QBF, SHARE>;
   const int smem = sizeof(TilesSmem<D, E4M3>) + 1024;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -963,10 +955,9 @@ static cudaError_t launch_tiles(TreeArgs a, int dev, cudaMemPool_t pool, cudaStr
     e = cudaGetLastError();
   }
   if (e == cudaSuccess) {
-    k_tree_join<D><<<dim3((R + 3) / 4, a.c.Hkv, a.B), 128, 0, st>>>(a, kTK, unit, vgrid, 1);
-    e = cudaGetLastError();
+    e = launch_join<D>(a, kTK, unit, vgrid, 1, st);
   }
-  const cudaError_t e2 = cudaFreeAsync(ws, st);
+  const cudaError_t e2 = cudaFreeAsync(a.part, st);
   return e != cudaSuccess ? e : e2;
 }
 
