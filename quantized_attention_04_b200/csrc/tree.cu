@@ -1090,6 +1090,7 @@ static cudaError_t launch_rows(TreeArgs a, int dev, cudaMemPool_t pool, cudaStre
 
 }  // namespace sage2
 #include "tree_tiles.cu"
+#include "weights_tiles.cu"
 namespace sage2 {
 
 template <int D, bool E4M3, bool QBF>
@@ -1103,7 +1104,8 @@ static cudaError_t tree_pick(const TreeArgs& a, int dev, cudaMemPool_t pool, cud
 
 template <int D, bool E4M3, bool QBF>
 static cudaError_t launch_weights(const TreeArgs& a, const float* lse, float* acc, long long ab,
-                                  long long ah, int S, cudaStream_t st) {
+                                  long long ah, int S, int dev, cudaStream_t st) {
+  return launch_weights_tiles<D, E4M3, QBF>(a, lse, acc, ab, ah, S, dev, st);
   const int cap = a.MP << a.c.page_shift;
   k_cache_weights<D, E4M3, QBF><<<dim3((cap + kWKeys - 1) / kWKeys, a.c.Hkv, a.B), 128, 0, st>>>(
       a, lse, acc, ab, ah, S);
@@ -1202,20 +1204,22 @@ sage2_status sage2_cache_weights(const void* q, int dtype, const int64_t* q_stri
   s = check_words(lse, acc);
   if (s != SAGE2_OK) return s;
   if (S <= 0 || !acc_strides || acc_strides[0] < 0 || acc_strides[1] < 0) return SAGE2_ERR_INVALID_ARG;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return SAGE2_ERR_CUDA;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const long long ab = acc_strides[0], ah = acc_strides[1];
   const bool bf = dtype == SAGE2_BF16, e4 = a.c.kv_dtype == SAGE2_E4M3;
   cudaError_t e;
   if (a.c.d == 64)
-    e = e4 ? (bf ? launch_weights<64, true, true>(a, lse, acc, ab, ah, S, st)
-                 : launch_weights<64, true, false>(a, lse, acc, ab, ah, S, st))
-           : (bf ? launch_weights<64, false, true>(a, lse, acc, ab, ah, S, st)
-                 : launch_weights<64, false, false>(a, lse, acc, ab, ah, S, st));
+    e = e4 ? (bf ? launch_weights<64, true, true>(a, lse, acc, ab, ah, S, dev, st)
+                 : launch_weights<64, true, false>(a, lse, acc, ab, ah, S, dev, st))
+           : (bf ? launch_weights<64, false, true>(a, lse, acc, ab, ah, S, dev, st)
+                 : launch_weights<64, false, false>(a, lse, acc, ab, ah, S, dev, st));
   else
-    e = e4 ? (bf ? launch_weights<128, true, true>(a, lse, acc, ab, ah, S, st)
-                 : launch_weights<128, true, false>(a, lse, acc, ab, ah, S, st))
-           : (bf ? launch_weights<128, false, true>(a, lse, acc, ab, ah, S, st)
-                 : launch_weights<128, false, false>(a, lse, acc, ab, ah, S, st));
+    e = e4 ? (bf ? launch_weights<128, true, true>(a, lse, acc, ab, ah, S, dev, st)
+                 : launch_weights<128, true, false>(a, lse, acc, ab, ah, S, dev, st))
+           : (bf ? launch_weights<128, false, true>(a, lse, acc, ab, ah, S, dev, st)
+                 : launch_weights<128, false, false>(a, lse, acc, ab, ah, S, dev, st));
   return from_cuda(e);
 }
 

@@ -160,6 +160,16 @@ __device__ __forceinline__ bool slot_allowed(const TreeArgs& a, const uint8_t* m
   return j < 0 || (j < s.n && tree_allows(mask, a.T, i, j));
 }
 
+// 32 lanes x 16 consecutive columns: thread t gets lane (base + t).
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
 // .16x256b.x4: 16 lanes x 32 columns.  Thread t gets, for k = 0..3, the columns 8k + 2(t%4) + {0,1}
 // of lane t/4 (registers 4k, 4k+1) and of lane t/4 + 8 (4k+2, 4k+3).
 __device__ __forceinline__ void tmem_ld16x256_16(uint32_t taddr, uint32_t (&r)[16]) {

@@ -194,6 +194,34 @@ def test_weights(qa, case):
     assert (got[want == 0] == 0.5).all()
 
 
+@pytest.mark.parametrize("kv", ["same", "e4m3"])
+@pytest.mark.parametrize("T, G, d, dtype", [(1, 1, 128, "bf16"), (9, 4, 64, "fp16"), (48, 4, 128, "bf16"),
+                                            (64, 8, 64, "bf16"), (37, 7, 128, "fp16")])
+def test_weights_long_runs(qa, T, G, d, dtype, kv):
+    """Many tiles a block, pieces that end inside a block's run, more rows than one unit holds; each
+    weight in 64 bits on the GPU."""
+    lens = [9000, 1, 3333, 0, 777, 8191]
+    c = R.Case(18, lens, T, 3, G, d, 16, dtype, kv, [T - (b % T) // 2 for b in range(len(lens))], junk=False)
+    x = c.cuda()
+    lse = attend_gpu(c, x)[1].float()
+    acc = torch.full((c.B, 3, c.MP * 16), 0.25, device="cuda")
+    qa.sage2_cache_weights(x["q"], lse.cuda(), x["cache"], x["table"], x["lens"], acc, mask=x["mask"], n=x["n"])
+    assert qa.sage2_check_device_error() == 0
+    want = torch.zeros(acc.shape, dtype=torch.float64, device="cuda")
+    for b in range(c.B):
+        ln, n = c.lens[b], c.n[b]
+        bar = torch.zeros(n, ln + n, dtype=torch.float64, device="cuda")
+        bar[:, ln:][~x["mask"][b, :n, :n]] = -math.inf
+        for h in range(3):
+            K = c.dense("k", b, h, ln + n).cuda()
+            for g in range(G):
+                s = x["q"][b, h * G + g, :n].double() @ K.T * c.sm + bar
+                want[b, h, :ln + n] += torch.exp(s - lse[b, h * G + g, :n, None].double().cuda()).sum(0)
+    e = logit_error(c) + 2.0 ** -22 * (lse[lse > -math.inf].abs().max().item() + 1)
+    tol = want * (math.expm1(e) + (G * T + 4) * 2.0 ** -24) + 2.0 ** -24 * (want + 0.25)
+    assert ((acc.double() - 0.25 - want).abs() <= tol).all(), ((acc.double() - 0.25 - want).abs() / tol).max()
+
+
 def pools_after_append(c, k, v):
     """The pools after writing k, v [B, Hkv, T, d] behind lens, by the definition."""
     out = {n: t.clone() for n, t in c.pool.items()}
