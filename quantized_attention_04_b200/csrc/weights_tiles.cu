@@ -3,8 +3,9 @@
 //   acc[b][h][s] += sum over the rows r that attend slot s of exp2(c_s q_r . K_s - z_r),
 // z = lse / ln 2.  S^T = K Q^T: 128 keys are the MMA's rows (TMEM lanes) and up to 256 rows of Q
 // its columns, so that a thread owns a key and adds up its own columns: no sum crosses
-// lanes, and a slot's sum has a fixed order.  S^T is double-buffered in TMEM; sixteen warps take
-// chunks of 16 columns in turn (four warps a lane quadrant) and meet once a tile.
+// lanes, and a slot's sum has a fixed order.  S^T is double-buffered in TMEM; eight warps take the even
+// tiles and eight the odd ones, each half of the columns in chunks of 16, and the two that share a key
+// meet once a tile.
 // Bound by the exponentials (16 a cycle and SM) where rows are many, by the bytes of K where few.
 //
 // e4m3 caches go to the tensor cores as they are (kind::f8f6f4).  The rows of Q, scaled
@@ -45,9 +46,9 @@ struct __align__(1024) WeightsSmem {
   using C = WeightsCfg<D, E4M3, QBF>;
   uint8_t q[C::kTerms][C::kTermBytes];
   uint8_t k[kWStages][C::kTileBytes];
-  float z[kWR];              // lse in log2 units; +inf: the row does not count
+  float z[kWR];              // -lse in log2 units; -inf: the row does not count
   int tok[kWR];              // drafted token of the row
-  float red[2][3][kWK];      // sums of the other three quarters of the columns, by tile parity
+  float red[2][2][kWK];      // sums of the second half of the columns, by tile parity and its turn
   float amax[kWExp];
   uint64_t full[kWStages], empty[kWStages];
   uint64_t q_full;           // the exponential warps
@@ -64,6 +65,9 @@ __device__ __forceinline__ uint32_t line_off(int r, int ch) {
   return r * 64 + ((ch ^ ((r >> 1) & 3)) << 4);
 }
 __device__ __forceinline__ void bar_exp() { asm volatile("bar.sync 1, %0;" ::"n"(kWExp * 32) : "memory"); }
+__device__ __forceinline__ void bar_half(int group) {      // the eight warps of a tile parity
+  asm volatile("bar.sync %0, %1;" ::"r"(2 + group), "n"(kWExp * 16) : "memory");
+}
 __host__ __device__ constexpr uint32_t idesc_e4m3_e5m2(int M, int N) {
   return (1u << 4) | (0u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) |
          (static_cast<uint32_t>(M >> 4) << 24);
@@ -90,7 +94,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
     mbar_init(&sm.q_full, kWExp);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.d_full[i], 1);
-      mbar_init(&sm.d_empty[i], kWExp);
+      mbar_init(&sm.d_empty[i], kWExp / 2);
     }
     mbar_init(&sm.drain, 1);
     sm.abort_flag = 0;
@@ -207,7 +211,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
   } else {
     // ------------------------------------------------------------ exponentials
     // After a wait that gave up every barrier is still passed, so that no warp is left waiting.
-    const int quad = warp & 3, part = warp >> 2, key_l = 32 * quad + lane;
+    const int quad = warp & 3, part = (warp >> 2) & 1, group = warp >> 3, key_l = 32 * quad + lane;
     const uint32_t tD = tmem + (static_cast<uint32_t>(32 * quad) << 16);
     const float kL2E = 1.4426950408889634f;
     while (left > 0) {
@@ -292,45 +296,50 @@ __global__ void __launch_bounds__(kWThreads, 1)
           }
         }
         if (half == 0) {
-          sm.z[rl] = z;
+          sm.z[rl] = -z;
           sm.tok[rl] = i;
         }
         fence_proxy_async_smem();
         bar_exp();
         if (lane == 0) mbar_arrive(&sm.q_full);
 
-        // the key scale of this thread's key, a tile ahead
-        auto scale_of = [&](int key) {
-          if (!E4M3 || key >= L) return 0.f;
-          const int page = __ldg(a.table + (size_t)at.b * a.MP + (key >> a.c.page_shift));
-          return page_inside(page, a.c.pages) ? __ldg(a.c.ks + row_of(page, a.c.Hkv, h, a.c.page_shift, key)) : 0.f;
+        // this group's tiles: every other one; the page of the thread's key two of them ahead, the key
+        // scale one
+        const int k0 = (t & 1) == group ? 0 : 1;
+        auto page_of = [&](int k) {
+          const int key = (at.tile + k) * kWK + key_l;
+          return E4M3 && k < cnt && key < L ? __ldg(a.table + (size_t)at.b * a.MP + (key >> a.c.page_shift)) : -1;
         };
-        float ks = scale_of(at.tile * kWK + key_l);
-        for (int k = 0; k < cnt; ++k, ++t) {
-          const int p = t & 1, key0 = (at.tile + k) * kWK, key = key0 + key_l;
+        auto scale_of = [&](int k, int page) {
+          const int key = (at.tile + k) * kWK + key_l;
+          return E4M3 && page_inside(page, a.c.pages)
+                     ? __ldg(a.c.ks + row_of(page, a.c.Hkv, h, a.c.page_shift, key)) : 0.f;
+        };
+        float ks = scale_of(k0, page_of(k0));
+        int page = page_of(k0 + 2);
+        for (int k = k0; k < cnt; k += 2) {
+          const int tt = t + k, key0 = (at.tile + k) * kWK, key = key0 + key_l, p = group;
           const float c1 = E4M3 ? qs * ks : qs;
-          if (k + 1 < cnt) ks = scale_of(key + kWK);
-          const bool edge = key0 + kWK > at.s.len;
+          ks = scale_of(k + 2, page);
+          page = page_of(k + 4);
+          const bool edge = key0 + kWK > at.s.len, mine = part == 0 && key < L && key < S;
           float* out = tally + at.b * ab + h * ah + key;
           float old = 0.f;
-          if (part == 0 && key < L && key < S) old = *out;
-          ok = ok && tile_wait(&sm.d_full[p], (t >> 1) & 1, abort_flag);
+          if (mine) old = *out;
+          ok = ok && tile_wait(&sm.d_full[p], (tt >> 1) & 1, abort_flag);
           tc_fence_after();
           float2 sum = make_float2(0.f, 0.f), sum2 = sum;
           const float2 c2 = make_float2(c1, c1);
-#pragma unroll 1
-          for (int c = ok ? 16 * part : cols; c < cols; c += 64) {
-            uint32_t x[16];
-            tmem_ld16(tD + p * 256 + c, x);
-            tmem_ld_wait();
-            if (!edge) {
+          const uint32_t d = tD + p * 256;
+          if (!edge && ok) {
+            auto add = [&](const uint32_t (&x)[16], int c) {
 #pragma unroll
               for (int y = 0; y < 16; y += 4) {
                 const float4 zz = *reinterpret_cast<const float4*>(sm.z + c + y);
                 float2 e0 = __ffma2_rn(make_float2(__uint_as_float(x[y]), __uint_as_float(x[y + 1])), c2,
-                                       make_float2(-zz.x, -zz.y));
+                                       make_float2(zz.x, zz.y));
                 float2 e1 = __ffma2_rn(make_float2(__uint_as_float(x[y + 2]), __uint_as_float(x[y + 3])), c2,
-                                       make_float2(-zz.z, -zz.w));
+                                       make_float2(zz.z, zz.w));
                 e0.x = ex2(e0.x);
                 e0.y = ex2(e0.y);
                 e1.x = ex2(e1.x);
@@ -338,12 +347,33 @@ __global__ void __launch_bounds__(kWThreads, 1)
                 sum = __fadd2_rn(sum, e0);
                 sum2 = __fadd2_rn(sum2, e1);
               }
-            } else {
+            };
+            uint32_t xa[16], xb[16];
+            int c = 16 * part;
+            if (c < cols) tmem_ld16(d + c, xa);
+#pragma unroll 1
+            while (c < cols) {
+              tmem_ld_wait();
+              if (c + 32 < cols) tmem_ld16(d + c + 32, xb);
+              add(xa, c);
+              c += 32;
+              if (c >= cols) break;
+              tmem_ld_wait();
+              if (c + 32 < cols) tmem_ld16(d + c + 32, xa);
+              add(xb, c);
+              c += 32;
+            }
+          } else if (ok) {
+#pragma unroll 1
+            for (int c = 16 * part; c < cols; c += 32) {
+              uint32_t x[16];
+              tmem_ld16(d + c, x);
+              tmem_ld_wait();
 #pragma unroll 4
               for (int y = 0; y < 16; ++y) {
                 const float zz = sm.z[c + y];
-                const bool in = zz < INFINITY && key < L && slot_allowed(a, mask, at.s, sm.tok[c + y], key);
-                const float e = ex2(__uint_as_float(x[y]) * c1 - zz);
+                const bool in = zz > -INFINITY && key < L && slot_allowed(a, mask, at.s, sm.tok[c + y], key);
+                const float e = ex2(fmaf(__uint_as_float(x[y]), c1, zz));
                 if (in) sum.x += e;
               }
             }
@@ -351,12 +381,13 @@ __global__ void __launch_bounds__(kWThreads, 1)
           tc_fence_before();
           __syncwarp();
           mbar_arrive_lane0(&sm.d_empty[p], lane);
-          const float mine = (sum.x + sum.y) + (sum2.x + sum2.y);
-          if (part > 0) sm.red[p][part - 1][key_l] = mine;
-          bar_exp();
-          if (part == 0 && key < L && key < S)
-            *out = old + ((mine + sm.red[p][0][key_l]) + (sm.red[p][1][key_l] + sm.red[p][2][key_l]));
+          const float half_sum = (sum.x + sum.y) + (sum2.x + sum2.y);
+          const int turn = (tt >> 1) & 1;
+          if (part == 1) sm.red[p][turn][key_l] = half_sum;
+          bar_half(group);
+          if (mine) *out = old + (half_sum + sm.red[p][turn][key_l]);
         }
+        t += cnt;
       }
       next_piece(cnt);
     }
