@@ -84,13 +84,43 @@ struct __align__(1024) TilesSmem {
 static_assert(sizeof(TilesSmem<128, false>) + 1024 <= 232448 && sizeof(TilesSmem<128, true>) + 1024 <= 232448,
               "shared memory of a block");
 
+// MMAs and commits of one elected lane as predicated instructions: the whole converged warp passes them, so
+// that descriptors stay in uniform registers (inside a branch of one lane each operand costs moves).
 // D[tmem] (+)= A[tmem] * B[smem], 16-bit A (two values a column), fp32 D.
-__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
-                                           uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_f16_ts_if(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                              uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-      ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate));
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead));
+}
+// D[tmem] (+)= A[smem] * B[smem]^T, 16-bit floats.
+__device__ __forceinline__ void mma_f16_ss_if(uint32_t lead, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                              uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+      ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead));
+}
+// The same of 8-bit floats.
+__device__ __forceinline__ void mma_f8_ss_if(uint32_t lead, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                             uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+      ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead));
+}
+__device__ __forceinline__ void tc_commit_if(uint32_t lead, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+      ::"r"(smem_u32(bar)), "r"(lead) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_if(uint32_t lead, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}"
+      ::"r"(smem_u32(bar)), "r"(lead) : "memory");
 }
 // Descriptor of a [k][n] operand (n contiguous): 128-byte rows of 64 n, 128-byte
 // swizzle, 8-row groups 1024 bytes apart, the next 64 n `block` bytes on.
@@ -119,12 +149,12 @@ template <typename T>
 __device__ __forceinline__ T uniform(T x) {
   return __shfl_sync(0xffffffffu, x, 0);
 }
-__device__ __forceinline__ bool elect_one() {
+__device__ __forceinline__ uint32_t elect_one() {
   uint32_t p;
   asm volatile(
       "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(p));
-  return p != 0;
+  return p;
 }
 
 // Byte offset of 16-byte chunk `ch` (of D/8) of row `r` in a 16-bit tile of ROWS rows.
@@ -498,7 +528,7 @@ __global__ void __launch_bounds__(kTThreads<E4M3>, 1)
       const uint32_t v_hi = uniform((uint32_t)(dv0 >> 32)), v_lo = uniform((uint32_t)dv0);
       const uint32_t q_lo = uniform((uint32_t)smem_desc_kmajor(sm.q[s], 128));
       const uint32_t tm = uniform(tmem) + s * 128, to = uniform(tmem) + 256 + s * 128;
-      const bool leader = elect_one();
+      const uint32_t leader = elect_one();
       const int n = uniform(run.n);
       int first = 0;               // bit p: the last tile of parity p starts a piece
       int q_ph = 0;
@@ -511,16 +541,14 @@ __global__ void __launch_bounds__(kTThreads<E4M3>, 1)
         }
         first = (first & ~(1 << p)) | (start << p);
         tc_fence_after();
-        const uint32_t kb = k_lo + buf * kBuf16;
-        if (leader) {
-          mbar_arrive(&sm.s_full[s][p]);
+        const uint32_t kb = uniform(k_lo + buf * kBuf16);
+        mbar_arrive_if(leader, &sm.s_full[s][p]);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_f16_ss(tm + p * 64, desc_of(q_lo + (kk >> 2) * ((kTR * 128) >> 4) + (kk & 3) * 2, k_hi),
-                       desc_of(kb + (kk >> 2) * ((kTK * 128) >> 4) + (kk & 3) * 2, k_hi), idesc_s, kk > 0);
-          tc_commit(&sm.s_full[s][p]);
-          tc_commit(&sm.empty[kb0 + buf]);
-        }
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_f16_ss_if(leader, tm + p * 64, desc_of(q_lo + (kk >> 2) * ((kTR * 128) >> 4) + (kk & 3) * 2, k_hi),
+                        desc_of(kb + (kk >> 2) * ((kTK * 128) >> 4) + (kk & 3) * 2, k_hi), idesc_s, kk > 0);
+        tc_commit_if(leader, &sm.s_full[s][p]);
+        tc_commit_if(leader, &sm.empty[kb0 + buf]);
         __syncwarp();
         return true;
       };
@@ -537,15 +565,13 @@ __global__ void __launch_bounds__(kTThreads<E4M3>, 1)
               !tile_wait(&sm.full[vb0 + buf], (t / kRing) & 1, abort_flag))
             break;
           tc_fence_after();
-          const uint32_t vb = v_lo + buf * kBuf16, keep = ((first >> p) & 1) ^ 1;
-          if (leader) {
+          const uint32_t vb = uniform(v_lo + buf * kBuf16), keep = ((first >> p) & 1) ^ 1;
 #pragma unroll
-            for (int kk = 0; kk < kTK / 16; ++kk)
-              mma_f16_ts(to, tm + p * 64 + 8 * kk, desc_of(vb + kk * (16 * 128 >> 4), v_hi), idesc_o,
-                         kk > 0 ? 1u : keep);
-            tc_commit(&sm.o_done[s][p]);
-            tc_commit(&sm.empty[vb0 + buf]);
-          }
+          for (int kk = 0; kk < kTK / 16; ++kk)
+            mma_f16_ts_if(leader, to, tm + p * 64 + 8 * kk, desc_of(vb + kk * (16 * 128 >> 4), v_hi), idesc_o,
+                          kk > 0 ? 1u : keep);
+          tc_commit_if(leader, &sm.o_done[s][p]);
+          tc_commit_if(leader, &sm.empty[vb0 + buf]);
           __syncwarp();
         }
 #pragma unroll 1
@@ -565,7 +591,7 @@ __global__ void __launch_bounds__(kTThreads<E4M3>, 1)
         }
       }
       // every MMA issued so far completes before the block frees TMEM
-      if (leader) tc_commit(&sm.drain[s]);
+      tc_commit_if(leader, &sm.drain[s]);
       __syncwarp();
       tile_wait(&sm.drain[s], 0, nullptr);
     } else if (E4M3 && warp == kMma + 2) {

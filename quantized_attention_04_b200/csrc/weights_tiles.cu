@@ -52,7 +52,7 @@ struct __align__(1024) WeightsSmem {
   float amax[kWExp];
   uint64_t full[kWStages], empty[kWStages];
   uint64_t q_full;           // the exponential warps
-  uint64_t d_full[2], d_empty[2];
+  uint64_t d_full[2][2], d_empty[2][2];     // by tile parity, half of the columns
   uint64_t drain;
   uint32_t tmem;
   int abort_flag;
@@ -85,6 +85,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
                                       ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int R = a.G * a.T, cols = (rows_unit + 15) & ~15;
+  const int cols0 = ((cols >> 4) + 1) / 2 * 16;      // columns of the first half
   volatile int* abort_flag = &sm.abort_flag;
   if (tid == 0) {
     for (int i = 0; i < kWStages; ++i) {
@@ -92,9 +93,9 @@ __global__ void __launch_bounds__(kWThreads, 1)
       mbar_init(&sm.empty[i], 1);
     }
     mbar_init(&sm.q_full, kWExp);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sm.d_full[i], 1);
-      mbar_init(&sm.d_empty[i], kWExp / 2);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&sm.d_full[i >> 1][i & 1], 1);
+      mbar_init(&sm.d_empty[i >> 1][i & 1], kWExp / 4);
     }
     mbar_init(&sm.drain, 1);
     sm.abort_flag = 0;
@@ -165,11 +166,12 @@ __global__ void __launch_bounds__(kWThreads, 1)
     }
   } else if (warp == kWExp + 1) {
     // ------------------------------------------------------------ MMA issuer (values alike in all lanes)
-    const uint32_t idesc = E4M3 ? idesc_e4m3_e5m2(kWK, cols) : idesc_f16_f32(kWK, cols, QBF);
+    auto idesc_of = [&](int n) { return E4M3 ? idesc_e4m3_e5m2(kWK, n) : idesc_f16_f32(kWK, n, QBF); };
     const uint64_t dk0 = smem_desc_kmajor(sm.k[0], C::kLine), dq0 = smem_desc_kmajor(sm.q[0], C::kLine);
     const uint32_t hi = uniform((uint32_t)(dk0 >> 32)), k_lo = uniform((uint32_t)dk0), q_lo = uniform((uint32_t)dq0);
-    const uint32_t tm = uniform(tmem), id = uniform(idesc);
-    const bool leader = elect_one();
+    const uint32_t tm = uniform(tmem), id0 = uniform(idesc_of(cols0)), id1 = uniform(idesc_of(cols - cols0));
+    const int halves_used = cols > cols0 ? 2 : 1;
+    const uint32_t leader = elect_one();
     int units = 0;
     while (ok && left > 0) {
       const int cnt = piece_tiles();
@@ -180,32 +182,39 @@ __global__ void __launch_bounds__(kWThreads, 1)
         }
         for (int k = 0; k < cnt; ++k, ++t) {
           const int st = t % kWStages, p = t & 1;
-          if ((t >= 2 && !tile_wait(&sm.d_empty[p], ((t >> 1) - 1) & 1, abort_flag)) ||
-              !tile_wait(&sm.full[st], (t / kWStages) & 1, abort_flag)) {
+          if (!tile_wait(&sm.full[st], (t / kWStages) & 1, abort_flag)) {
             ok = false;
             break;
           }
-          tc_fence_after();
-          const uint32_t kb = uniform(k_lo + st * (C::kTileBytes >> 4)), d = uniform(tm + p * 256);
-          if (leader) {
+          const uint32_t kb = uniform(k_lo + st * (C::kTileBytes >> 4));
+#pragma unroll 1
+          for (int hf = 0; hf < halves_used; ++hf) {
+            if (t >= 2 && !tile_wait(&sm.d_empty[p][hf], ((t >> 1) - 1) & 1, abort_flag)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t d = uniform(tm + p * 256 + hf * 128), id = uniform(hf ? id1 : id0);
+            const uint32_t qb = uniform(q_lo + (hf ? cols0 * (C::kLine >> 4) : 0));
 #pragma unroll
             for (int x = 0; x < C::kTerms; ++x)
 #pragma unroll
               for (int kk = 0; kk < C::kRowBytes / 32; ++kk) {
                 const uint32_t qo = (kk >> 2) * ((kWR * 128) >> 4) + (kk & 3) * 2 + x * (C::kTermBytes >> 4);
                 const uint32_t ko = (kk >> 2) * ((kWK * 128) >> 4) + (kk & 3) * 2;
-                if (E4M3) mma_f8_ss(d, desc_of(kb + ko, hi), desc_of(q_lo + qo, hi), id, x > 0 || kk > 0);
-                else mma_f16_ss(d, desc_of(kb + ko, hi), desc_of(q_lo + qo, hi), id, kk > 0);
+                if (E4M3) mma_f8_ss_if(leader, d, desc_of(kb + ko, hi), desc_of(qb + qo, hi), id, x > 0 || kk > 0);
+                else mma_f16_ss_if(leader, d, desc_of(kb + ko, hi), desc_of(qb + qo, hi), id, kk > 0);
               }
-            tc_commit(&sm.d_full[p]);
-            tc_commit(&sm.empty[st]);
+            tc_commit_if(leader, &sm.d_full[p][hf]);
+            if (hf == halves_used - 1) tc_commit_if(leader, &sm.empty[st]);
+            __syncwarp();
           }
-          __syncwarp();
+          if (!ok) break;
         }
       }
       next_piece(cnt);
     }
-    if (leader) tc_commit(&sm.drain);
+    tc_commit_if(leader, &sm.drain);
     __syncwarp();
     tile_wait(&sm.drain, 0, nullptr);
   } else {
@@ -315,8 +324,13 @@ __global__ void __launch_bounds__(kWThreads, 1)
           return E4M3 && page_inside(page, a.c.pages)
                      ? __ldg(a.c.ks + row_of(page, a.c.Hkv, h, a.c.page_shift, key)) : 0.f;
         };
-        float ks = scale_of(k0, page_of(k0));
+        auto old_of = [&](int k) {
+          const int key = (at.tile + k) * kWK + key_l;
+          return part == 0 && k < cnt && key < L && key < S ? tally[at.b * ab + h * ah + key] : 0.f;
+        };
+        float ks = scale_of(k0, page_of(k0)), next_old = old_of(k0);
         int page = page_of(k0 + 2);
+        const int c0 = part ? cols0 : 0, c1st = part ? cols : cols0;      // this warp's columns
         for (int k = k0; k < cnt; k += 2) {
           const int tt = t + k, key0 = (at.tile + k) * kWK, key = key0 + key_l, p = group;
           const float c1 = E4M3 ? qs * ks : qs;
@@ -324,13 +338,13 @@ __global__ void __launch_bounds__(kWThreads, 1)
           page = page_of(k + 4);
           const bool edge = key0 + kWK > at.s.len, mine = part == 0 && key < L && key < S;
           float* out = tally + at.b * ab + h * ah + key;
-          float old = 0.f;
-          if (mine) old = *out;
-          ok = ok && tile_wait(&sm.d_full[p], (tt >> 1) & 1, abort_flag);
+          const float old = next_old;
+          next_old = old_of(k + 2);
+          if (c0 < c1st) ok = ok && tile_wait(&sm.d_full[p][part], (tt >> 1) & 1, abort_flag);
           tc_fence_after();
           float2 sum = make_float2(0.f, 0.f), sum2 = sum;
           const float2 c2 = make_float2(c1, c1);
-          const uint32_t d = tD + p * 256;
+          const uint32_t d = tD + p * 256 + part * 128 - c0;
           if (!edge && ok) {
             auto add = [&](const uint32_t (&x)[16], int c) {
 #pragma unroll
@@ -349,38 +363,42 @@ __global__ void __launch_bounds__(kWThreads, 1)
               }
             };
             uint32_t xa[16], xb[16];
-            int c = 16 * part;
-            if (c < cols) tmem_ld16(d + c, xa);
+            int c = c0;
+            if (c < c1st) tmem_ld16(d + c, xa);
 #pragma unroll 1
-            while (c < cols) {
+            while (c < c1st) {
               tmem_ld_wait();
-              if (c + 32 < cols) tmem_ld16(d + c + 32, xb);
+              if (c + 16 < c1st) tmem_ld16(d + c + 16, xb);
               add(xa, c);
-              c += 32;
-              if (c >= cols) break;
+              c += 16;
+              if (c >= c1st) break;
               tmem_ld_wait();
-              if (c + 32 < cols) tmem_ld16(d + c + 32, xa);
+              if (c + 16 < c1st) tmem_ld16(d + c + 16, xa);
               add(xb, c);
-              c += 32;
+              c += 16;
             }
           } else if (ok) {
 #pragma unroll 1
-            for (int c = 16 * part; c < cols; c += 32) {
+            for (int c = c0; c < c1st; c += 16) {
+              // which rows attend this key: 16 bytes of the mask on their way at a time
+              uint32_t in = 0;
+#pragma unroll
+              for (int y = 0; y < 16; ++y)
+                in |= (slot_allowed(a, mask, at.s, sm.tok[c + y], key) ? 1u : 0u) << y;
+              if (key >= L) in = 0;
               uint32_t x[16];
               tmem_ld16(d + c, x);
               tmem_ld_wait();
-#pragma unroll 4
+#pragma unroll
               for (int y = 0; y < 16; ++y) {
-                const float zz = sm.z[c + y];
-                const bool in = zz > -INFINITY && key < L && slot_allowed(a, mask, at.s, sm.tok[c + y], key);
-                const float e = ex2(fmaf(__uint_as_float(x[y]), c1, zz));
-                if (in) sum.x += e;
+                const float zz = sm.z[c + y], e = ex2(fmaf(__uint_as_float(x[y]), c1, zz));
+                if (((in >> y) & 1u) && zz > -INFINITY) sum.x += e;
               }
             }
           }
           tc_fence_before();
           __syncwarp();
-          mbar_arrive_lane0(&sm.d_empty[p], lane);
+          mbar_arrive_lane0(&sm.d_empty[p][part], lane);
           const float half_sum = (sum.x + sum.y) + (sum2.x + sum2.y);
           const int turn = (tt >> 1) & 1;
           if (part == 1) sm.red[p][turn][key_l] = half_sum;
