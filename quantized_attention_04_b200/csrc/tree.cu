@@ -209,10 +209,12 @@ __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
                : "r"(addr)
                : "memory");
 }
-// Two e4m3 codes (bits 15:0) to two fp16 values, exact.
-__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t two) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3);
-  return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
+// Four e4m3 codes to two packed fp16 pairs, exact.
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t& a, uint32_t& b) {
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+      : "=r"(a), "=r"(b)
+      : "r"(w));
 }
 template <bool BF>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -280,26 +282,30 @@ __device__ __forceinline__ float row_lse(float m, float sum) {
 // e4m3 cache: codes become fp16 in registers (exact).  Q (fp16 or bf16) enters as
 // fp16 scaled by a power of two that puts the row's largest value at 2^13 (what
 // falls below fp16's range is under 2^-37 of it).  The key scales multiply the
-// scores; the value scales multiply P relative to the largest one seen
-// (vref, carried like the running maximum), so P stays within [0, 1].
+// scores; the value scales multiply P, whose reference includes the tile's largest value scale.
 constexpr int kRowsWarps = 4;
 constexpr float kVrefLeast = 1e-30f;   // value scales below it count as part of it
 constexpr int kRowsTile = 16 * kRowsWarps;
 constexpr int kRowsLeast = 2;          // tiles that a block takes at least
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, int MT>
 struct RowsCfg {
   static constexpr int kRowBytes = D * (E4M3 ? 1 : 2);
   static constexpr int kBoxBytes = kRowBytes < 128 ? kRowBytes : 128;   // swizzle span
   static constexpr int kBoxes = kRowBytes / kBoxBytes;
   static constexpr int kTileBytes = 16 * kRowBytes;                     // K or V of a warp's 16 keys
   static constexpr int kStageBytes = 2 * kTileBytes;
-  static constexpr int kStages = E4M3 ? (D == 128 ? 6 : 8) : (D == 128 ? 3 : 6);
+  // Blocks of an SM, and stages of a warp in the shared memory that leaves them.  A warp's chain of
+  // waits, products and exponentials is long: more warps, not deeper rings, keep the bytes coming
+  // (one token over 32768 e4m3 slots x 8 heads: 2 blocks of 6 stages 35 us, see the launch for 4 of 2).
+  static constexpr int kBlocks = MT == 2 ? 2 : (D == 64 ? 4 : 3);
+  static constexpr int kStages = MT == 2 ? (E4M3 ? (D == 128 ? 6 : 8) : (D == 128 ? 3 : 6))
+                                         : (E4M3 ? (D == 64 ? 4 : 3) : 2);
 };
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, int MT>
 struct __align__(1024) RowsSmem {
-  using C = RowsCfg<D, E4M3>;
+  using C = RowsCfg<D, E4M3, MT>;
   uint8_t kv[kRowsWarps][C::kStages][C::kStageBytes];
   float sc[kRowsWarps][C::kStages][E4M3 ? 32 : 4];  // key scales, value scales
   float red[kRowsWarps][16][36];                    // 32 columns of the rows of an m-tile
@@ -312,21 +318,21 @@ struct __align__(1024) RowsSmem {
 // Byte offset of 16-byte chunk `ch` of row `r` in a tile of 16 rows.
 template <int D, bool E4M3>
 __device__ __forceinline__ uint32_t rows_off(int r, int ch) {
-  using C = RowsCfg<D, E4M3>;
+  using C = RowsCfg<D, E4M3, 1>;
   if (C::kBoxBytes == 128)
     return (ch >> 3) * (16 * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
   return r * 64 + ((ch ^ ((r >> 1) & 3)) << 4);
 }
 
 template <int D, bool E4M3, bool QBF, int MT>
-__global__ void __launch_bounds__(32 * kRowsWarps, 2)
+__global__ void __launch_bounds__(32 * kRowsWarps, (RowsCfg<D, E4M3, MT>::kBlocks))
     k_tree_rows(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                 const __grid_constant__ TreeArgs a) {
-  using C = RowsCfg<D, E4M3>;
+  using C = RowsCfg<D, E4M3, MT>;
   constexpr bool BF = QBF && !E4M3;           // type of the MMA operands
   constexpr int NT = D / 8;                   // n-tiles of O
   extern __shared__ uint8_t smem_raw[];
-  RowsSmem<D, E4M3>& sm = *reinterpret_cast<RowsSmem<D, E4M3>*>(
+  RowsSmem<D, E4M3, MT>& sm = *reinterpret_cast<RowsSmem<D, E4M3, MT>*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, c = lane & 3;
@@ -346,49 +352,54 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 2)
   in.start(run, kRowsTile);
   at = in;
   int issued = 0, used = 0, in_t = 0;         // tiles with keys of this warp
-  // Issues the loads of the next tile in which this warp has keys, if the run has one.
-  auto issue = [&]() {
+  int page = -1;                              // of the tile to be issued next, asked for one tile ahead
+  // On to the next tile in which this warp has keys.
+  auto seek = [&]() {
     while (in_t < nt) {
       const int key0 = in.tile * kRowsTile + warp * 16;
-      const bool here = key0 < in.s.len + in.s.n;
-      if (here && lane == 0) {
-        const int st = issued % C::kStages;
-        int page = __ldg(a.table + (size_t)in.b * a.MP + (key0 >> a.c.page_shift));
-        const bool ok = static_cast<unsigned>(page) < static_cast<unsigned>(a.c.pages);
-        if (!ok) {
-          atomicOr(&g_device_error, DEVERR_BOUNDS);
-          page = 0;
-        }
-        sm.bad[warp][st] = !ok;
-        const int h = in.pair / a.RT;
-        const int row = ((page * a.c.Hkv + h) << a.c.page_shift) + (key0 & ((1 << a.c.page_shift) - 1));
-        uint64_t* bar = &sm.full[warp][st];
-        uint8_t* dst = sm.kv[warp][st];
-        mbar_expect_tx(bar, C::kStageBytes + (E4M3 ? 128 : 0));
-#pragma unroll
-        for (int x = 0; x < C::kBoxes; ++x) {
-          tma_load_2d(dst + x * 2048, &tm_k, bar, x * 64, row);
-          tma_load_2d(dst + C::kTileBytes + x * 2048, &tm_v, bar, x * 64, row);
-        }
-        if (E4M3) {
-          bulk_load(sm.sc[warp][st], a.c.ks + row, 64, bar);
-          bulk_load(sm.sc[warp][st] + 16, a.c.vs + row, 64, bar);
-        }
-      }
-      ++in_t;
-      if (in_t < nt) in.next(a, pairs, kRowsTile);
-      if (here) {
-        ++issued;
+      if (key0 < in.s.len + in.s.n) {
+        page = __ldg(a.table + (size_t)in.b * a.MP + (key0 >> a.c.page_shift));
         return;
       }
+      if (++in_t < nt) in.next(a, pairs, kRowsTile);
     }
   };
+  // Issues the loads of that tile, if the run has one.
+  auto issue = [&]() {
+    if (in_t >= nt) return;
+    if (lane == 0) {
+      const int key0 = in.tile * kRowsTile + warp * 16;
+      const int st = issued % C::kStages;
+      const bool ok = page_inside(page, a.c.pages);
+      if (!ok) atomicOr(&g_device_error, DEVERR_BOUNDS);
+      sm.bad[warp][st] = !ok;
+      const int row = (int)row_of(ok ? page : 0, a.c.Hkv, in.pair / a.RT, a.c.page_shift, key0);
+      uint64_t* bar = &sm.full[warp][st];
+      uint8_t* dst = sm.kv[warp][st];
+      mbar_expect_tx(bar, C::kStageBytes + (E4M3 ? 128 : 0));
+#pragma unroll
+      for (int x = 0; x < C::kBoxes; ++x) {
+        tma_load_2d(dst + x * 2048, &tm_k, bar, x * 64, row);
+        tma_load_2d(dst + C::kTileBytes + x * 2048, &tm_v, bar, x * 64, row);
+      }
+      if (E4M3) {
+        bulk_load(sm.sc[warp][st], a.c.ks + row, 64, bar);
+        bulk_load(sm.sc[warp][st] + 16, a.c.vs + row, 64, bar);
+      }
+    }
+    ++issued;
+    if (++in_t < nt) in.next(a, pairs, kRowsTile);
+    seek();
+  };
+  seek();
   for (int s = 0; s < C::kStages; ++s) issue();
   __syncwarp();                               // lane 0's sm.bad
 
   uint32_t qf[MT][D / 16][4];
   float acc[MT][NT][4];
-  float m[MT][2], l[MT][2], qs[MT][2], vref = kVrefLeast;
+  float m[MT][2], l[MT][2], qs[MT][2];        // m: the reference (log2 units)
+  // log2 of how far P may exceed 1: fp16 ends at 2^16; a bf16 P of 2^40 leaves its sums far from fp32's end
+  constexpr float kGrow = BF ? 40.f : 14.f;
   const float kL2E = 1.4426950408889634f;
 
   for (int t = 0; t < nt; ++t) {
@@ -397,7 +408,6 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 2)
     const int h = at.pair / a.RT;
     if (t == 0 || at.tile == 0) {
       // a piece starts: its rows' Q fragments
-      vref = kVrefLeast;
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
         const uint16_t* src[2];
@@ -526,49 +536,44 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 2)
             const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
-              const uint32_t b0 = e4m3x2_f16x2(ww[y] & 0xffffu), b1 = e4m3x2_f16x2(ww[y] >> 16);
+              uint32_t b0, b1;
+              widen4(ww[y], b0, b1);
 #pragma unroll
               for (int mt = 0; mt < MT; ++mt) mma16816<BF>(s[mt][j], qf[mt][4 * x + y], b0, b1);
             }
           }
       }
-      // ---- softmax of the 16 keys: this thread has keys 8j + 2c + {0,1} of rows g, g+8
-      float kscl[2][2], vscl[2][2];
-      bool vup = false;
-      float vold = vref;
+      // ---- softmax of the 16 keys: this thread has keys 8j + 2c + {0,1} of rows g, g+8.  The
+      // exponentials are taken against the reference that the earlier keys have left; it moves (and
+      // the sums and O with it) only when a score of the warp lies far above it.
+      float kscl[2][2], vscl[2][2], lv = 0.f;
       if (E4M3) {
-        float vm = 0.f;
+        float vm = kVrefLeast;
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            kscl[j][e] = sm.sc[warp][st][8 * j + 2 * c + e];
-            vscl[j][e] = sm.sc[warp][st][16 + 8 * j + 2 * c + e];
-            vm = fmaxf(vm, vscl[j][e]);
-          }
+        for (int j = 0; j < 2; ++j) {
+          const float2 k2 = *reinterpret_cast<const float2*>(&sm.sc[warp][st][8 * j + 2 * c]);
+          const float2 v2 = *reinterpret_cast<const float2*>(&sm.sc[warp][st][16 + 8 * j + 2 * c]);
+          kscl[j][0] = k2.x;
+          kscl[j][1] = k2.y;
+          vscl[j][0] = v2.x;
+          vscl[j][1] = v2.y;
+          vm = fmaxf(vm, fmaxf(v2.x, v2.y));
+        }
         vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 1));
         vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 2));
-        vup = vm > vref;
-        vref = fmaxf(vref, vm);
-        const float iv = __fdividef(1.f, vref);
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) vscl[j][e] *= iv;
+        lv = __log2f(vm);
       }
-      uint32_t pf[MT][4];
-      bool grew = vup;
-      float al[MT][2];
+      float x[MT][2][2][2];
+      bool over = false;
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float x[2][2];
 #pragma unroll
           for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int y = 0; y < 2; ++y)
-              x[j][y] = s[mt][j][2 * e + y] * (E4M3 ? qs[mt][e] * kscl[j][y] : qs[mt][e]);
+              x[mt][e][j][y] = s[mt][j][2 * e + y] * (E4M3 ? qs[mt][e] * kscl[j][y] : qs[mt][e]);
           if (edge) {
             const int r = row0 + mt * 16 + g + 8 * e;
             const int i = r % a.T;
@@ -579,43 +584,53 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 2)
                 const int k = 8 * j + 2 * c + y, jj = key0 + k - at.s.len;
                 const bool ok = k < live && r < R &&
                                 (jj < 0 || tree_allows(a.mask ? a.mask + at.b * a.mask_sb : nullptr, a.T, i, jj));
-                if (!ok) x[j][y] = -INFINITY;
-                else if ((badrows >> k) & 1u) x[j][y] = __int_as_float(0x7fffffff);
+                if (!ok) x[mt][e][j][y] = -INFINITY;
+                else if ((badrows >> k) & 1u) x[mt][e][j][y] = __int_as_float(0x7fffffff);
               }
           }
-          float mx = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[1][0], x[1][1]));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          const float mn = fmaxf(m[mt][e], mx);
-          const float mb = mn == -INFINITY ? 0.f : mn;
-          al[mt][e] = ex2(m[mt][e] - mb);
-          grew = grew || mn > m[mt][e];
-          m[mt][e] = mn;
-          float p[2][2], sum = 0.f;
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              p[j][y] = ex2(x[j][y] - mb);
-              sum += p[j][y];
-              if (E4M3) p[j][y] *= vscl[j][y];
-            }
-          l[mt][e] = l[mt][e] * al[mt][e] + sum;
-          pf[mt][e] = pack2<BF>(p[0][0], p[0][1]);
-          pf[mt][2 + e] = pack2<BF>(p[1][0], p[1][1]);
+          const float mx = fmaxf(fmaxf(x[mt][e][0][0], x[mt][e][0][1]), fmaxf(x[mt][e][1][0], x[mt][e][1][1]));
+          over = over || (mx > -INFINITY && mx + lv > m[mt][e] + kGrow);
         }
-      if (__any_sync(0xffffffffu, grew)) {
-        const float vr = (E4M3 && vup) ? __fdividef(vold, vref) : 1.f;
+      if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            acc[mt][j][0] *= al[mt][0] * vr;
-            acc[mt][j][1] *= al[mt][0] * vr;
-            acc[mt][j][2] *= al[mt][1] * vr;
-            acc[mt][j][3] *= al[mt][1] * vr;
+          for (int e = 0; e < 2; ++e) {
+            float mx = fmaxf(fmaxf(x[mt][e][0][0], x[mt][e][0][1]), fmaxf(x[mt][e][1][0], x[mt][e][1][1]));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            const float now = mx == -INFINITY ? m[mt][e] : fmaxf(m[mt][e], mx + lv);
+            const float f = m[mt][e] == -INFINITY ? 0.f : ex2(m[mt][e] - now);
+            m[mt][e] = now;
+            l[mt][e] *= f;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+              acc[mt][j][2 * e] *= f;
+              acc[mt][j][2 * e + 1] *= f;
+            }
           }
       }
+      uint32_t pf[MT][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float mb = m[mt][e] == -INFINITY ? 0.f : m[mt][e];
+          float p[2][2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) p[j][y] = ex2(x[mt][e][j][y] - mb);
+          l[mt][e] += (p[0][0] + p[0][1]) + (p[1][0] + p[1][1]);
+          if (E4M3) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int y = 0; y < 2; ++y) p[j][y] *= vscl[j][y];
+          }
+          pf[mt][e] = pack2<BF>(p[0][0], p[0][1]);
+          pf[mt][2 + e] = pack2<BF>(p[1][0], p[1][1]);
+        }
       // ---- O += P V
       if (!E4M3) {
         const uint32_t base = smem_u32(vt);
@@ -649,15 +664,14 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 2)
 #pragma unroll
           for (int hh = 0; hh < 2; ++hh) {
             const uint32_t sel = hh ? 0x7362u : 0x5140u;
-            const uint32_t lo = __byte_perm(w[0][x], w[1][x], sel);
-            const uint32_t hi = __byte_perm(w[2][x], w[3][x], sel);
+            uint32_t b0[2], b1[2];
+            widen4(__byte_perm(w[0][x], w[1][x], sel), b0[0], b0[1]);
+            widen4(__byte_perm(w[2][x], w[3][x], sel), b1[0], b1[1]);
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const uint32_t b0 = e4m3x2_f16x2(y ? lo >> 16 : lo & 0xffffu);
-              const uint32_t b1 = e4m3x2_f16x2(y ? hi >> 16 : hi & 0xffffu);
+            for (int y = 0; y < 2; ++y)
 #pragma unroll
-              for (int mt = 0; mt < MT; ++mt) mma16816<BF>(acc[mt][4 * x + 2 * hh + y], pf[mt], b0, b1);
-            }
+              for (int mt = 0; mt < MT; ++mt)
+                mma16816<BF>(acc[mt][4 * x + 2 * hh + y], pf[mt], b0[y], b1[y]);
           }
       }
       __syncwarp();
@@ -689,7 +703,7 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 2)
           float M = -INFINITY;
 #pragma unroll
           for (int w = 0; w < kRowsWarps; ++w) M = fmaxf(M, sm.ml[w][g + 8 * e].x);
-          f[e] = ex2(m[mt][e] - (M == -INFINITY ? 0.f : M)) * (E4M3 ? vref : 1.f);
+          f[e] = ex2(m[mt][e] - (M == -INFINITY ? 0.f : M));
         }
 #pragma unroll
         for (int part = 0; part < D / 32; ++part) {
@@ -886,141 +900,6 @@ __global__ void __launch_bounds__(128) k_tree_join(const __grid_constant__ TreeA
   if (a.lse && tid == 0) a.lse[orow] = none ? -INFINITY : row_lse(M, sum);
 }
 
-// ------------------------------------------------------------ weights
-// acc[b][h][s] += sum over the rows that attend slot s of exp(x - lse).  A warp
-// holds 16 keys as the A operand, the rows pass as B in groups of 32, and a
-// thread adds up its keys' weights over all rows before the four threads that
-// share a key meet once: a slot is owned by one warp, so the sum has a fixed order.
-// e4m3: the codes become the type of Q, exactly; the key scale multiplies the score.
-constexpr int kWKeys = 64;
-
-template <int D, bool E4M3, bool BF>
-__global__ void __launch_bounds__(128) k_cache_weights(const __grid_constant__ TreeArgs a,
-                                                       const float* __restrict__ lse,
-                                                       float* __restrict__ tally, long long ab,
-                                                       long long ah, int S) {
-  constexpr int RS = D + 8;                   // 16-bit elements of a padded row
-  __shared__ __align__(16) uint16_t kt[kWKeys * RS];
-  __shared__ __align__(16) uint16_t qt[32 * RS];
-  __shared__ float z[32];
-  const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int g = lane >> 2, c = lane & 3;
-  const SeqLen s = seq_len(a.lens, a.n, b, a.T, a.MP, a.c.page_shift);
-  const int L = s.n == 0 ? 0 : s.len + s.n;
-  const int key0 = blockIdx.x * kWKeys;
-  if (key0 >= L) return;
-  if (L > S && key0 == 0 && h == 0 && tid == 0) atomicOr(&g_device_error, DEVERR_BOUNDS);
-  for (int i = tid; i < kWKeys * (D / 8); i += 128) {
-    const int r = i / (D / 8), ch = i % (D / 8);
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (key0 + r < L) {
-      const int page = __ldg(a.table + (size_t)b * a.MP + ((key0 + r) >> a.c.page_shift));
-      if (static_cast<unsigned>(page) < static_cast<unsigned>(a.c.pages)) {
-        const long long row = (((long long)page * a.c.Hkv + h) << a.c.page_shift) +
-                              ((key0 + r) & ((1 << a.c.page_shift) - 1));
-        if (!E4M3) {
-          v = __ldg(reinterpret_cast<const uint4*>(a.c.k + row * D * 2) + ch);
-        } else {
-          const uint2 w = __ldg(reinterpret_cast<const uint2*>(a.c.k + row * D) + ch);
-          uint32_t o4[4] = {e4m3x2_f16x2(w.x & 0xffffu), e4m3x2_f16x2(w.x >> 16),
-                            e4m3x2_f16x2(w.y & 0xffffu), e4m3x2_f16x2(w.y >> 16)};
-          if (BF) {
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&o4[u]));
-              o4[u] = pack2<true>(f.x, f.y);
-            }
-          }
-          v = make_uint4(o4[0], o4[1], o4[2], o4[3]);
-        }
-      }
-    }
-    *reinterpret_cast<uint4*>(kt + r * RS + 8 * ch) = v;
-  }
-  __syncthreads();
-  uint32_t kf[D / 16][4];
-#pragma unroll
-  for (int ks = 0; ks < D / 16; ++ks)
-    ldsm4(smem_u32(kt + (warp * 16 + (lane & 15)) * RS + ks * 16 + 8 * (lane >> 4)), kf[ks]);
-  float ksc[2] = {1.f, 1.f};
-  bool there[2];
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int k = key0 + warp * 16 + g + 8 * e;
-    there[e] = k < L;
-    if (k < L) {
-      const int page = __ldg(a.table + (size_t)b * a.MP + (k >> a.c.page_shift));
-      if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.c.pages)) {
-        atomicOr(&g_device_error, DEVERR_BOUNDS);
-        there[e] = false;
-      } else if (E4M3) {
-        ksc[e] = __ldg(a.c.ks + ((((long long)page * a.c.Hkv + h) << a.c.page_shift) +
-                                 (k & ((1 << a.c.page_shift) - 1))));
-      }
-    }
-  }
-  const float kL2E = 1.4426950408889634f;
-  const float scl[2] = {a.sm_scale * kL2E * ksc[0], a.sm_scale * kL2E * ksc[1]};
-  const uint8_t* mask = a.mask ? a.mask + b * a.mask_sb : nullptr;
-  const bool edge = key0 + kWKeys > s.len;
-  const int R = a.G * a.T;
-  float sum[2] = {0.f, 0.f};
-  for (int r0 = 0; r0 < R; r0 += 32) {
-    __syncthreads();
-    for (int i = tid; i < 32 * (D / 8); i += 128) {
-      const int r = i / (D / 8), ch = i % (D / 8);
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (r0 + r < R)
-        v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + b * a.sb +
-                                                 (long long)(h * a.G + (r0 + r) / a.T) * a.sh +
-                                                 (long long)((r0 + r) % a.T) * a.st) + ch);
-      *reinterpret_cast<uint4*>(qt + r * RS + 8 * ch) = v;
-    }
-    if (tid < 32) {
-      // a row that does not count: +inf, so that its weights are 0
-      float v = INFINITY;
-      const int r = r0 + tid;
-      if (r < R && r % a.T < s.n) {
-        v = __ldg(lse + ((size_t)b * a.Hq + h * a.G + r / a.T) * a.T + r % a.T) * kL2E;
-        if (v == -INFINITY) v = INFINITY;
-      }
-      z[tid] = v;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int j2 = 0; j2 < 2; ++j2) {
-      float d[2][4] = {};
-#pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
-        uint32_t bq[4];
-        ldsm4(smem_u32(qt + (j2 * 16 + (lane >> 4) * 8 + (lane & 7)) * RS + ks * 16 +
-                       8 * ((lane >> 3) & 1)), bq);
-        mma16816<BF>(d[0], kf[ks], bq[0], bq[1]);
-        mma16816<BF>(d[1], kf[ks], bq[2], bq[3]);
-      }
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int e = u >> 1, rr = j2 * 16 + j * 8 + 2 * c + (u & 1);
-          bool ok = there[e] && z[rr] < INFINITY;
-          if (edge && ok) {
-            const int jj = key0 + warp * 16 + g + 8 * e - s.len;
-            ok = jj < 0 || tree_allows(mask, a.T, (r0 + rr) % a.T, jj);
-          }
-          if (ok) sum[e] += ex2(d[j][u] * scl[e] - z[rr]);
-        }
-    }
-  }
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 1);
-    sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 2);
-    const int k = key0 + warp * 16 + g + 8 * e;
-    if (c == 0 && there[e] && k < S) tally[b * ab + h * ah + k] += sum[e];
-  }
-}
-
 // ------------------------------------------------------------ launches
 static int sm_count(int dev) {
   static int n[64] = {};
@@ -1029,7 +908,7 @@ static int sm_count(int dev) {
     int v = 0;
     if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0)
       v = 148;
-    n[dev] = v < kMostBlocks / 2 ? v : kMostBlocks / 2;
+    n[dev] = v < kMostBlocks / 4 ? v : kMostBlocks / 4;
   }
   return n[dev];
 }
@@ -1059,9 +938,9 @@ static cudaError_t launch_join(const TreeArgs& a, int tile, int rows_tile, int g
 
 template <int D, bool E4M3, bool QBF, int MT>
 static cudaError_t launch_rows(TreeArgs a, int dev, cudaMemPool_t pool, cudaStream_t st) {
-  using C = RowsCfg<D, E4M3>;
+  using C = RowsCfg<D, E4M3, MT>;
   a.RT = (a.G * a.T + 16 * MT - 1) / (16 * MT);
-  const int grid = 2 * sm_count(dev);
+  const int grid = C::kBlocks * sm_count(dev);
   CUtensorMap tk, tv;
   const uint64_t rows = (uint64_t)a.c.pages * a.c.Hkv << a.c.page_shift;
   const int eb = E4M3 ? 1 : 2;
@@ -1075,7 +954,7 @@ static cudaError_t launch_rows(TreeArgs a, int dev, cudaMemPool_t pool, cudaStre
   e = split_workspace(&a, prow, D, pool, st);
   if (e != cudaSuccess) return e;
   auto kern = k_tree_rows<D, E4M3, QBF, MT>;
-  const int smem = sizeof(RowsSmem<D, E4M3>) + 1024;
+  const int smem = sizeof(RowsSmem<D, E4M3, MT>) + 1024;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e == cudaSuccess) {
     kern<<<grid, 32 * kRowsWarps, smem, st>>>(tk, tv, a);
@@ -1100,16 +979,6 @@ static cudaError_t tree_pick(const TreeArgs& a, int dev, cudaMemPool_t pool, cud
   if (R <= 32) return launch_rows<D, E4M3, QBF, 2>(a, dev, pool, st);
   if (R <= kTR) return launch_tiles<D, E4M3, QBF, false>(a, dev, pool, st);
   return launch_tiles<D, E4M3, QBF, true>(a, dev, pool, st);
-}
-
-template <int D, bool E4M3, bool QBF>
-static cudaError_t launch_weights(const TreeArgs& a, const float* lse, float* acc, long long ab,
-                                  long long ah, int S, int dev, cudaStream_t st) {
-  return launch_weights_tiles<D, E4M3, QBF>(a, lse, acc, ab, ah, S, dev, st);
-  const int cap = a.MP << a.c.page_shift;
-  k_cache_weights<D, E4M3, QBF><<<dim3((cap + kWKeys - 1) / kWKeys, a.c.Hkv, a.B), 128, 0, st>>>(
-      a, lse, acc, ab, ah, S);
-  return cudaGetLastError();
 }
 
 // What sage2_attn_tree and sage2_cache_weights check alike.
@@ -1211,15 +1080,15 @@ sage2_status sage2_cache_weights(const void* q, int dtype, const int64_t* q_stri
   const bool bf = dtype == SAGE2_BF16, e4 = a.c.kv_dtype == SAGE2_E4M3;
   cudaError_t e;
   if (a.c.d == 64)
-    e = e4 ? (bf ? launch_weights<64, true, true>(a, lse, acc, ab, ah, S, dev, st)
-                 : launch_weights<64, true, false>(a, lse, acc, ab, ah, S, dev, st))
-           : (bf ? launch_weights<64, false, true>(a, lse, acc, ab, ah, S, dev, st)
-                 : launch_weights<64, false, false>(a, lse, acc, ab, ah, S, dev, st));
+    e = e4 ? (bf ? launch_weights_tiles<64, true, true>(a, lse, acc, ab, ah, S, dev, st)
+                 : launch_weights_tiles<64, true, false>(a, lse, acc, ab, ah, S, dev, st))
+           : (bf ? launch_weights_tiles<64, false, true>(a, lse, acc, ab, ah, S, dev, st)
+                 : launch_weights_tiles<64, false, false>(a, lse, acc, ab, ah, S, dev, st));
   else
-    e = e4 ? (bf ? launch_weights<128, true, true>(a, lse, acc, ab, ah, S, dev, st)
-                 : launch_weights<128, true, false>(a, lse, acc, ab, ah, S, dev, st))
-           : (bf ? launch_weights<128, false, true>(a, lse, acc, ab, ah, S, dev, st)
-                 : launch_weights<128, false, false>(a, lse, acc, ab, ah, S, dev, st));
+    e = e4 ? (bf ? launch_weights_tiles<128, true, true>(a, lse, acc, ab, ah, S, dev, st)
+                 : launch_weights_tiles<128, true, false>(a, lse, acc, ab, ah, S, dev, st))
+           : (bf ? launch_weights_tiles<128, false, true>(a, lse, acc, ab, ah, S, dev, st)
+                 : launch_weights_tiles<128, false, false>(a, lse, acc, ab, ah, S, dev, st));
   return from_cuda(e);
 }
 

@@ -137,13 +137,6 @@ __device__ __forceinline__ uint64_t desc_of(uint32_t lo, uint32_t hi) {
 __device__ __forceinline__ void prefetch_l2(const void* p) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
-// Four e4m3 codes to two packed fp16 pairs, exact.
-__device__ __forceinline__ void widen4(uint32_t w, uint32_t& a, uint32_t& b) {
-  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
-      : "=r"(a), "=r"(b)
-      : "r"(w));
-}
 // Lane 0's value, which the compiler then knows to be alike in all lanes.
 template <typename T>
 __device__ __forceinline__ T uniform(T x) {

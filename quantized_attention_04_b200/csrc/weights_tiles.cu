@@ -52,7 +52,7 @@ struct __align__(1024) WeightsSmem {
   float amax[kWExp];
   uint64_t full[kWStages], empty[kWStages];
   uint64_t q_full;           // the exponential warps
-  uint64_t d_full[2][2], d_empty[2][2];     // by tile parity, half of the columns
+  uint64_t d_full[2], d_empty[2];           // by tile parity
   uint64_t drain;
   uint32_t tmem;
   int abort_flag;
@@ -93,9 +93,9 @@ __global__ void __launch_bounds__(kWThreads, 1)
       mbar_init(&sm.empty[i], 1);
     }
     mbar_init(&sm.q_full, kWExp);
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(&sm.d_full[i >> 1][i & 1], 1);
-      mbar_init(&sm.d_empty[i >> 1][i & 1], kWExp / 4);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.d_full[i], 1);
+      mbar_init(&sm.d_empty[i], kWExp / 2);
     }
     mbar_init(&sm.drain, 1);
     sm.abort_flag = 0;
@@ -169,8 +169,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
     auto idesc_of = [&](int n) { return E4M3 ? idesc_e4m3_e5m2(kWK, n) : idesc_f16_f32(kWK, n, QBF); };
     const uint64_t dk0 = smem_desc_kmajor(sm.k[0], C::kLine), dq0 = smem_desc_kmajor(sm.q[0], C::kLine);
     const uint32_t hi = uniform((uint32_t)(dk0 >> 32)), k_lo = uniform((uint32_t)dk0), q_lo = uniform((uint32_t)dq0);
-    const uint32_t tm = uniform(tmem), id0 = uniform(idesc_of(cols0)), id1 = uniform(idesc_of(cols - cols0));
-    const int halves_used = cols > cols0 ? 2 : 1;
+    const uint32_t tm = uniform(tmem), id = uniform(idesc_of(cols));
     const uint32_t leader = elect_one();
     int units = 0;
     while (ok && left > 0) {
@@ -187,29 +186,23 @@ __global__ void __launch_bounds__(kWThreads, 1)
             break;
           }
           const uint32_t kb = uniform(k_lo + st * (C::kTileBytes >> 4));
-#pragma unroll 1
-          for (int hf = 0; hf < halves_used; ++hf) {
-            if (t >= 2 && !tile_wait(&sm.d_empty[p][hf], ((t >> 1) - 1) & 1, abort_flag)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint32_t d = uniform(tm + p * 256 + hf * 128), id = uniform(hf ? id1 : id0);
-            const uint32_t qb = uniform(q_lo + (hf ? cols0 * (C::kLine >> 4) : 0));
+          if (t >= 2 && !tile_wait(&sm.d_empty[p], ((t >> 1) - 1) & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t d = uniform(tm + p * 256);
 #pragma unroll
             for (int x = 0; x < C::kTerms; ++x)
 #pragma unroll
               for (int kk = 0; kk < C::kRowBytes / 32; ++kk) {
                 const uint32_t qo = (kk >> 2) * ((kWR * 128) >> 4) + (kk & 3) * 2 + x * (C::kTermBytes >> 4);
                 const uint32_t ko = (kk >> 2) * ((kWK * 128) >> 4) + (kk & 3) * 2;
-                if (E4M3) mma_f8_ss_if(leader, d, desc_of(kb + ko, hi), desc_of(qb + qo, hi), id, x > 0 || kk > 0);
-                else mma_f16_ss_if(leader, d, desc_of(kb + ko, hi), desc_of(qb + qo, hi), id, kk > 0);
+                if (E4M3) mma_f8_ss_if(leader, d, desc_of(kb + ko, hi), desc_of(q_lo + qo, hi), id, x > 0 || kk > 0);
+                else mma_f16_ss_if(leader, d, desc_of(kb + ko, hi), desc_of(q_lo + qo, hi), id, kk > 0);
               }
-            tc_commit_if(leader, &sm.d_full[p][hf]);
-            if (hf == halves_used - 1) tc_commit_if(leader, &sm.empty[st]);
-            __syncwarp();
-          }
-          if (!ok) break;
+          tc_commit_if(leader, &sm.d_full[p]);
+          tc_commit_if(leader, &sm.empty[st]);
         }
       }
       next_piece(cnt);
@@ -232,17 +225,21 @@ __global__ void __launch_bounds__(kWThreads, 1)
         const int rl = tid >> 1, half = tid & 1, r = u * rows_unit + rl;
         const int i = r % a.T;
         float z = INFINITY;
-        if (rl < rows_unit && r < R && i < at.s.n) {
+        const bool there = rl < rows_unit && r < R && i < at.s.n;
+        if (there) {
           z = __ldg(lse + ((size_t)at.b * a.Hq + h * a.G + r / a.T) * a.T + i) * kL2E;
           if (z == -INFINITY) z = INFINITY;
         }
-        const bool counts = !(z == INFINITY);
         uint4 w[D / 16];
         const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at.b * a.sb +
-                                                          (long long)(h * a.G + (counts ? r / a.T : 0)) * a.sh +
-                                                          (long long)(counts ? i : 0) * a.st) + half * (D / 16);
+                                                          (long long)(h * a.G + (there ? r / a.T : 0)) * a.sh +
+                                                          (long long)(there ? i : 0) * a.st) + half * (D / 16);
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) w[c] = counts ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+        for (int c = 0; c < D / 16; ++c) w[c] = there ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+        if (z == INFINITY) {
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) w[c] = make_uint4(0u, 0u, 0u, 0u);
+        }
         float qs = a.sm_scale * kL2E;
         // everyone is done with the last unit's rows: the threads have all read its last tile, and its
         // MMAs are over (d_full has been waited for)
@@ -340,11 +337,11 @@ __global__ void __launch_bounds__(kWThreads, 1)
           float* out = tally + at.b * ab + h * ah + key;
           const float old = next_old;
           next_old = old_of(k + 2);
-          if (c0 < c1st) ok = ok && tile_wait(&sm.d_full[p][part], (tt >> 1) & 1, abort_flag);
+          ok = ok && tile_wait(&sm.d_full[p], (tt >> 1) & 1, abort_flag);
           tc_fence_after();
           float2 sum = make_float2(0.f, 0.f), sum2 = sum;
           const float2 c2 = make_float2(c1, c1);
-          const uint32_t d = tD + p * 256 + part * 128 - c0;
+          const uint32_t d = tD + p * 256;
           if (!edge && ok) {
             auto add = [&](const uint32_t (&x)[16], int c) {
 #pragma unroll
@@ -398,7 +395,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
           }
           tc_fence_before();
           __syncwarp();
-          mbar_arrive_lane0(&sm.d_empty[p][part], lane);
+          mbar_arrive_lane0(&sm.d_empty[p], lane);
           const float half_sum = (sum.x + sum.y) + (sum2.x + sum2.y);
           const int turn = (tt >> 1) & 1;
           if (part == 1) sm.red[p][turn][key_l] = half_sum;
