@@ -296,11 +296,10 @@ struct RowsCfg {
   static constexpr int kTileBytes = 16 * kRowBytes;                     // K or V of a warp's 16 keys
   static constexpr int kStageBytes = 2 * kTileBytes;
   // Blocks of an SM, and stages of a warp in the shared memory that leaves them.  A warp's chain of
-  // waits, products and exponentials is long: more warps, not deeper rings, keep the bytes coming
-  // (one token over 32768 e4m3 slots x 8 heads: 2 blocks of 6 stages 35 us, see the launch for 4 of 2).
-  static constexpr int kBlocks = MT == 2 ? 2 : (D == 64 ? 4 : 3);
-  static constexpr int kStages = MT == 2 ? (E4M3 ? (D == 128 ? 6 : 8) : (D == 128 ? 3 : 6))
-                                         : (E4M3 ? (D == 64 ? 4 : 3) : 2);
+  // waits, products and exponentials is long, so that more warps keep more bytes coming than deeper rings.
+  static constexpr int kBlocks = MT == 2 ? 2 : (D == 64 ? 4 : (E4M3 ? 3 : 2));
+  static constexpr int kStages = MT == 2 ? (E4M3 ? (D == 128 ? 4 : 8) : (D == 128 ? 2 : 4))
+                                         : (E4M3 ? (D == 64 ? 4 : 2) : 2);
 };
 
 template <int D, bool E4M3, int MT>
@@ -308,7 +307,7 @@ struct __align__(1024) RowsSmem {
   using C = RowsCfg<D, E4M3, MT>;
   uint8_t kv[kRowsWarps][C::kStages][C::kStageBytes];
   float sc[kRowsWarps][C::kStages][E4M3 ? 32 : 4];  // key scales, value scales
-  float red[kRowsWarps][16][36];                    // 32 columns of the rows of an m-tile
+  float red[kRowsWarps][16][D + 4];                 // O of the rows of an m-tile
   float2 ml[kRowsWarps][16];
   uint64_t full[kRowsWarps][C::kStages];
   int bad[kRowsWarps][C::kStages];                  // the stage's page was out of range
@@ -706,57 +705,66 @@ __global__ void __launch_bounds__(32 * kRowsWarps, (RowsCfg<D, E4M3, MT>::kBlock
           f[e] = ex2(m[mt][e] - (M == -INFINITY ? 0.f : M));
         }
 #pragma unroll
-        for (int part = 0; part < D / 32; ++part) {
+        for (int e = 0; e < 2; ++e) {
+          if (row0 + mt * 16 + g + 8 * e >= R) continue;
+          float* to = sm.red[warp][g + 8 * e];
+          if (!E4M3) {
 #pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            if (!E4M3) {
-              if (j / 4 == part) {
-                *reinterpret_cast<float2*>(&sm.red[warp][g][8 * (j % 4) + 2 * c]) =
-                    make_float2(acc[mt][j][0] * f[0], acc[mt][j][1] * f[0]);
-                *reinterpret_cast<float2*>(&sm.red[warp][g + 8][8 * (j % 4) + 2 * c]) =
-                    make_float2(acc[mt][j][2] * f[1], acc[mt][j][3] * f[1]);
-              }
-            } else {
+            for (int j = 0; j < NT; ++j)
+              *reinterpret_cast<float2*>(to + 8 * j + 2 * c) =
+                  make_float2(acc[mt][j][2 * e] * f[e], acc[mt][j][2 * e + 1] * f[e]);
+          } else {
+            // column y of n-tile j is d = (D/8) (2c + y) + j
 #pragma unroll
-              for (int u = 0; u < 4; ++u) {
-                const int dd = (D / 8) * (2 * c + (u & 1)) + j;
-                if (dd / 32 == part) sm.red[warp][g + 8 * (u >> 1)][dd % 32] = acc[mt][j][u] * f[u >> 1];
-              }
-            }
+            for (int y = 0; y < 2; ++y)
+#pragma unroll
+              for (int j = 0; j < NT; j += 4)
+                *reinterpret_cast<float4*>(to + NT * (2 * c + y) + j) =
+                    make_float4(acc[mt][j][2 * e + y] * f[e], acc[mt][j + 1][2 * e + y] * f[e],
+                                acc[mt][j + 2][2 * e + y] * f[e], acc[mt][j + 3][2 * e + y] * f[e]);
           }
-          __syncthreads();
-          const int rr = tid / 8, col = (tid % 8) * 4;
-          const int r = row0 + mt * 16 + rr;
-          if (r < R) {
-            float M = -INFINITY, sum = 0.f, o4[4];
+        }
+        __syncthreads();
+        // eight threads a row, every eighth float4
+        const int rr = tid >> 3, r = row0 + mt * 16 + rr;
+        if (r < R) {
+          float M = -INFINITY, sum = 0.f;
 #pragma unroll
-            for (int w = 0; w < kRowsWarps; ++w) M = fmaxf(M, sm.ml[w][rr].x);
-            const float mb = M == -INFINITY ? 0.f : M;
+          for (int w = 0; w < kRowsWarps; ++w) M = fmaxf(M, sm.ml[w][rr].x);
+          const float mb = M == -INFINITY ? 0.f : M;
 #pragma unroll
-            for (int w = 0; w < kRowsWarps; ++w) sum += ex2(sm.ml[w][rr].x - mb) * sm.ml[w][rr].y;
+          for (int w = 0; w < kRowsWarps; ++w) sum += ex2(sm.ml[w][rr].x - mb) * sm.ml[w][rr].y;
+          const int i = r % a.T;
+          const bool none = i >= at.s.n || sum == 0.f;
+          const float inv = none ? 0.f : 1.f / sum;
+          const size_t row = whole ? ((size_t)at.b * a.Hq + h * a.G + r / a.T) * a.T + i
+                                   : (size_t)slot * (16 * MT) + mt * 16 + rr;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              o4[i] = sm.red[0][rr][col + i];
+          for (int col = 4 * (tid & 7); col < D; col += 32) {
+            float4 v = *reinterpret_cast<const float4*>(&sm.red[0][rr][col]);
 #pragma unroll
-              for (int w = 1; w < kRowsWarps; ++w) o4[i] += sm.red[w][rr][col + i];
+            for (int w = 1; w < kRowsWarps; ++w) {
+              const float4 y = *reinterpret_cast<const float4*>(&sm.red[w][rr][col]);
+              v.x += y.x;
+              v.y += y.y;
+              v.z += y.z;
+              v.w += y.w;
             }
+            float o4[4] = {v.x, v.y, v.z, v.w};
             if (whole) {
-              const int i = r % a.T;
-              const bool none = i >= at.s.n || sum == 0.f;
-              const float inv = none ? 0.f : 1.f / sum;
 #pragma unroll
               for (int x = 0; x < 4; ++x) o4[x] = none ? 0.f : o4[x] * inv;
-              const size_t orow = ((size_t)at.b * a.Hq + h * a.G + r / a.T) * a.T + i;
-              store4(a.o, a.o_dtype, orow * D + part * 32 + col, o4);
-              if (a.lse && part == 0 && col == 0) a.lse[orow] = none ? -INFINITY : row_lse(M, sum);
+              store4(a.o, a.o_dtype, row * D + col, o4);
             } else {
-              const size_t prow = (size_t)slot * (16 * MT) + mt * 16 + rr;
-              store4(a.part, 2, prow * D + part * 32 + col, o4);
-              if (part == 0 && col == 0) a.part_ml[prow] = make_float2(M, sum);
+              store4(a.part, 2, row * D + col, o4);
             }
           }
-          __syncthreads();
+          if ((tid & 7) == 0) {
+            if (!whole) a.part_ml[row] = make_float2(M, sum);
+            else if (a.lse) a.lse[row] = none ? -INFINITY : row_lse(M, sum);
+          }
         }
+        __syncthreads();
       }
     }
     if (t + 1 < nt) at.next(a, pairs, kRowsTile);
