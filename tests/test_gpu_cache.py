@@ -429,3 +429,191 @@ def test_serving_run(qa):
         o, lse = qa.sage2_attn_tree(c2.q.cuda(), cache, table, new)
         assert qa.sage2_check_device_error() == 0
         check_tree(c2, o, lse, R.attend(c2), c2.dtype)
+
+
+def bad_index(qa):
+    from quantized_attention_04_b200 import Sage2Error
+    status = qa.sage2_check_device_error()
+    assert qa.sage2_check_device_error() == 0        # reading clears it
+    return status == 8
+
+
+@pytest.mark.parametrize("T, G", [(3, 2), (40, 4)])
+@pytest.mark.parametrize("kv", ["same", "e4m3"])
+def test_device_integers_out_of_range(qa, T, G, kv):
+    """Lengths, counts, pages and indices out of range set the error word; the sequences beside them and all
+    rows that nothing names keep what they hold."""
+    c = R.Case(19, [100, 37], T, 2, G, 64, 16, "bf16", kv, junk=False)
+    want = R.attend(c)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    cap = c.MP * 16
+    for what, v in (("lens", [cap - T + 1, 37]), ("lens", [-1, 37]), ("lens", [2 ** 31 - 1, 37]), ("n", [T + 1, T]),
+                    ("n", [-5, T]), ("page", c.pages), ("page", -1), ("page", 2 ** 31 - 1)):
+        x = c.cuda()
+        if what == "page":
+            x["table"][0, 1] = v
+        else:
+            x[what] = i32(v)
+        before = {n: t.clone() for n, t in x["cache"].items()}
+        o, lse = qa.sage2_attn_tree(**x)
+        assert bad_index(qa), (what, v)
+        acc = torch.ones(2, 2, cap, device="cuda")
+        qa.sage2_cache_weights(x["q"], want[1].float().cuda(), x["cache"], x["table"], x["lens"], acc,
+                               mask=x["mask"], n=x["n"])
+        assert bad_index(qa), (what, v)
+        for n, t in x["cache"].items():
+            assert same_bits(t, before[n])
+        one = type(c)(19, [37], T, 2, G, 64, 16, "bf16", kv, junk=False)
+        one.pool, one.table, one.q, one.mask, one.MP = c.pool, c.table[1:], c.q[1:], c.mask[1:], c.MP
+        check_tree(one, o[1:], lse[1:], tuple(w[1:] for w in want), c.dtype)
+        k = torch.ones(2, 2, T, 64, dtype=c.dtype, device="cuda")
+        other = set(range(c.pages)) - set(c.table.flatten().tolist())
+        qa.sage2_cache_append(k, k, x["cache"], x["table"], x["lens"], n=x["n"])
+        if what != "page" or v == c.pages:
+            bad_index(qa)                            # only if a row of the bad page is written
+        for n, t in x["cache"].items():
+            for p in other:
+                assert same_bits(t[p], before[n][p])
+    x = c.cuda()
+    before = {n: t.clone() for n, t in x["cache"].items()}
+    idx = torch.tensor([3, 0, 200000, -1], dtype=torch.int32, device="cuda").expand(2, 2, 4).contiguous()
+    qa.sage2_cache_compact(x["cache"], x["table"], idx)   # slot 1 from slot 0 would move back
+    assert bad_index(qa)
+    after = pools_after_move(c.pool, c.table, c.table, 16, torch.full((2, 2, 1), 3), [1, 1], [0, 0])
+    for n, t in x["cache"].items():
+        assert same_bits(t, after[n]), n
+
+
+def test_refusals(qa):
+    c = R.Case(20, [40], 3, 2, 2, 64, 16, "bf16", "same")
+    x = c.cuda()
+    q, cache, table, lens, mask = x["q"], x["cache"], x["table"], x["lens"], x["mask"]
+    acc = torch.zeros(1, 2, 64, device="cuda")
+    err = (ValueError, qa.Sage2Error)
+    with pytest.raises(err):
+        qa.sage2_attn_tree(q.float(), cache, table, lens)
+    with pytest.raises(err):
+        qa.sage2_attn_tree(q.half(), cache, table, lens)                 # a 16-bit cache takes its own type
+    with pytest.raises(err):
+        qa.sage2_attn_tree(q[:, :3], cache, table, lens)                 # heads no multiple of the cache's
+    with pytest.raises(err):
+        qa.sage2_attn_tree(q, cache, table.long(), lens)
+    with pytest.raises(err):
+        qa.sage2_attn_tree(q, cache, table, lens.cpu())
+    with pytest.raises(err):
+        qa.sage2_attn_tree(q, cache, table, lens, mask=mask[:, :2])
+    with pytest.raises(err):
+        qa.sage2_attn_tree(q, cache, table, lens, sm_scale=-1.0)
+    with pytest.raises(err):
+        qa.sage2_attn_tree(q, {"k": cache["k"], "v": cache["v"].transpose(1, 2)}, table, lens)
+    with pytest.raises(err):
+        qa.sage2_attn_tree(q.transpose(2, 3), cache, table, lens)
+    with pytest.raises(err):
+        qa.sage2_cache_weights(q, torch.zeros(1, 4, 2, device="cuda"), cache, table, lens, acc)
+    with pytest.raises(err):
+        qa.sage2_cache_weights(q, torch.zeros(1, 4, 3, device="cuda"), cache, table, lens, acc.double())
+    with pytest.raises(err):
+        qa.sage2_cache_evict(cache, table, lens, acc, 8, sinks=5, recent=4)
+    with pytest.raises(err):
+        qa.sage2_cache_evict(cache, table, lens, acc, 8, out_table=table.clone(), acc_out=acc)
+    with pytest.raises(err):
+        qa.sage2_cache_compact(cache, table, torch.zeros(1, 3, 4, dtype=torch.int32, device="cuda"))
+    with pytest.raises(err):
+        qa.sage2_cache_append(q[:, :2], q[:, :2], cache, table, lens, n=torch.zeros(2, dtype=torch.int32, device="cuda"))
+    assert qa.sage2_check_device_error() == 0
+
+
+@pytest.mark.parametrize("kv", ["same", "e4m3"])
+def test_streams_and_graphs(qa, kv):
+    """The calls on another stream than the default one, and captured: two graphs replayed at the same
+    time on two streams give what eager calls give."""
+    cs = [R.Case(s, [700, 90, 0], T, 2, 4, 128, 32, "bf16", kv, junk=False) for s, T in ((21, 2), (22, 30))]
+    want = []
+    for c in cs:
+        x = c.cuda()
+        o, lse = qa.sage2_attn_tree(**x)
+        acc = torch.zeros(3, 2, c.MP * 32, device="cuda")
+        qa.sage2_cache_weights(x["q"], lse, x["cache"], x["table"], x["lens"], acc, mask=x["mask"], n=x["n"])
+        idx, new, kept = qa.sage2_cache_evict(x["cache"], x["table"], x["lens"], acc, 64, 2, 8)
+        want.append([o, lse, acc, idx, new, kept, *x["cache"].values()])
+    torch.cuda.synchronize()
+    runs = []
+    for c in cs:
+        x = c.cuda()
+        start = {n: t.clone() for n, t in x["cache"].items()}
+        acc, kept = torch.zeros(3, 2, c.MP * 32, device="cuda"), torch.zeros(3, 2, 64, device="cuda")
+        st, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g, stream=st):
+            for n, t in x["cache"].items():
+                t.view(torch.uint8).copy_(start[n].view(torch.uint8))
+            acc.zero_()
+            kept.zero_()
+            o, lse = qa.sage2_attn_tree(**x)
+            qa.sage2_cache_weights(x["q"], lse, x["cache"], x["table"], x["lens"], acc, mask=x["mask"], n=x["n"])
+            idx, new, _ = qa.sage2_cache_evict(x["cache"], x["table"], x["lens"], acc, 64, 2, 8, acc_out=kept)
+        # x and start stay alive: the graph reads them
+        runs.append((st, g, [o, lse, acc, idx, new, kept, *x["cache"].values()], x, start))
+    for _ in range(3):
+        for st, g, *_ in runs:
+            with torch.cuda.stream(st):
+                g.replay()
+        torch.cuda.synchronize()
+        for (_, _, got, *_), w in zip(runs, want):
+            for a, b in zip(got, w):
+                assert same_bits(a, b)
+    assert qa.sage2_check_device_error() == 0
+    # eager, on a stream of its own, while the graphs live
+    c, w = cs[1], want[1]
+    st = torch.cuda.Stream()
+    x = c.cuda()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        o, lse = qa.sage2_attn_tree(**x)
+    st.synchronize()
+    assert same_bits(o, w[0]) and same_bits(lse, w[1])
+
+
+@pytest.mark.parametrize("T, G", [(1, 4), (20, 4), (50, 4)])
+def test_strided_queries_and_masks(qa, T, G):
+    """q as a fused projection lays it out, one mask for all, a mask per sequence apart, out and lse given."""
+    c = R.Case(23, [300, 41], T, 2, G, 64, 16, "fp16", "e4m3")
+    c.mask[1] = c.mask[0]
+    x = c.cuda()
+    want = R.attend(c)
+    wide = torch.zeros(2, T, 2 * G, 3, 64, dtype=c.dtype, device="cuda")
+    wide[:, :, :, 1] = x["q"].transpose(1, 2)
+    x["q"] = wide[:, :, :, 1].transpose(1, 2)
+    far = torch.zeros(2, 3, T, T, dtype=torch.bool, device="cuda")
+    far[:, 1] = x["mask"]
+    for mask in (x["mask"][0].clone(), far[:, 1]):
+        x["mask"] = mask
+        out, lse = torch.empty(2, 2 * G, T, 64, dtype=torch.bfloat16, device="cuda"), torch.empty(2, 2 * G, T, device="cuda")
+        o, l = qa.sage2_attn_tree(out=out, lse=lse, **x)
+        assert o is out and l is lse and qa.sage2_check_device_error() == 0
+        check_tree(c, o, l, want, torch.bfloat16)
+
+
+def test_pools_past_32_bits(qa):
+    """Rows whose offset in the pools passes 2^32 bytes (and 2^31 values)."""
+    pages, Hkv, page, d = 70000, 8, 64, 128                   # 4.6 GB each of k and v
+    cache = qa.sage2_cache_alloc(pages, Hkv, page, d, torch.float8_e4m3fn)
+    near = qa.sage2_cache_alloc(8, Hkv, page, d, torch.float8_e4m3fn)
+    g = torch.Generator("cuda").manual_seed(1)
+    k, v = (torch.randn(1, Hkv, 200, d, device="cuda", generator=g, dtype=torch.bfloat16) for _ in range(2))
+    q = torch.randn(1, 4 * Hkv, 40, d, device="cuda", generator=g, dtype=torch.bfloat16)
+    far = torch.arange(pages - 4, pages, dtype=torch.int32, device="cuda")[None]
+    tables = (far, torch.arange(4, dtype=torch.int32, device="cuda")[None])
+    zero, lens = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.full((1,), 160, dtype=torch.int32, device="cuda")
+    got = []
+    for c, t in ((cache, tables[0]), (near, tables[1])):
+        qa.sage2_cache_append(k, v, c, t, zero)
+        res = [qa.sage2_attn_tree(q[:, :, :T].contiguous(), c, t, lens) for T in (1, 8, 20, 40)]
+        acc = torch.zeros(1, Hkv, 256, device="cuda")
+        qa.sage2_cache_weights(q, res[-1][1], c, t, lens, acc)
+        idx, new, kept = qa.sage2_cache_evict(c, t, lens, acc, 70, 1, 5)
+        rows = [x[t[0].long()].contiguous() for x in (c["k"].view(torch.uint8), c["v"].view(torch.uint8), c["k_scale"])]
+        got.append([*(y for r in res for y in r), acc, idx, kept, *rows])
+    assert qa.sage2_check_device_error() == 0
+    for a, b in zip(*got):
+        assert same_bits(a, b)
