@@ -328,7 +328,7 @@ sage2_status sage2_cache_append(const void* k, const void* v, int dtype, const i
  * A token with nothing to attend and the tokens i >= n[b] get o = 0, lse = -inf.
  * Slots from lens[b] + n[b] on may hold any bits, and an infinity or NaN in the
  * row of a drafted token reaches only the tokens that attend it (their whole o
- * is NaN).  Scores, their maxima and sums and the
+ * is NaN).  |v| is to be below 2^100.  Scores, their maxima and sums and the
  * accumulators are fp32; P is rounded to the MMA's 16-bit type.  The order of the
  * sums depends on the sizes and lengths alone, so equal calls give equal bits.
  */
@@ -344,8 +344,9 @@ sage2_status sage2_attn_tree(const void* q, int dtype, const int64_t* q_strides,
  *                   attend slot s of exp(sm_scale * q[b][hq][i] . K_s - lse[b][hq][i])
  * with the arguments of sage2_attn_tree and the lse it wrote (rows with lse = -inf
  * add nothing).
- *   acc : f32, slots contiguous, acc_strides {batch, head} in elements, S slots a
- *         head (a slot >= S is left out and sets the device error word).
+ *   acc : f32, slots contiguous, acc_strides {batch, head} in elements (no two heads
+ *         the same), S slots a head (a slot >= S is left out and sets the device error
+ *         word).
  */
 sage2_status sage2_cache_weights(const void* q, int dtype, const int64_t* q_strides,
                                  const float* lse, const sage2_cache* cache, const int* table,

@@ -681,6 +681,9 @@ static sage2_status move_args(const sage2_cache* cache, const int* table, int ma
     if (S <= 0 || SO <= 0 || !acc_strides || !acc_out_strides) return SAGE2_ERR_INVALID_ARG;
     if (acc_strides[0] < 0 || acc_strides[1] < 0 || acc_out_strides[0] < 0 || acc_out_strides[1] < 0)
       return SAGE2_ERR_INVALID_ARG;
+    // a tally that heads share would be written by several at once
+    if ((B > 1 && acc_out_strides[0] == 0) || (a->c.Hkv > 1 && acc_out_strides[1] == 0))
+      return SAGE2_ERR_INVALID_ARG;
     a->ab = acc_strides[0];
     a->ah = acc_strides[1];
     a->ob = acc_out_strides[0];

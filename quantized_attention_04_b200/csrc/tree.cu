@@ -397,8 +397,8 @@ __global__ void __launch_bounds__(32 * kRowsWarps, (RowsCfg<D, E4M3, MT>::kBlock
   uint32_t qf[MT][D / 16][4];
   float acc[MT][NT][4];
   float m[MT][2], l[MT][2], qs[MT][2];        // m: the reference (log2 units)
-  // log2 of how far P may exceed 1: fp16 ends at 2^16; a bf16 P of 2^40 leaves its sums far from fp32's end
-  constexpr float kGrow = BF ? 40.f : 14.f;
+  // log2 of how far P may exceed 1: fp16 ends at 2^16; with a bf16 P of 2^24 O stays finite up to |V| = 2^100
+  constexpr float kGrow = BF ? 24.f : 14.f;
   const float kL2E = 1.4426950408889634f;
 
   for (int t = 0; t < nt; ++t) {
@@ -1081,6 +1081,8 @@ sage2_status sage2_cache_weights(const void* q, int dtype, const int64_t* q_stri
   s = check_words(lse, acc);
   if (s != SAGE2_OK) return s;
   if (S <= 0 || !acc_strides || acc_strides[0] < 0 || acc_strides[1] < 0) return SAGE2_ERR_INVALID_ARG;
+  // a tally that heads share would be written by several at once
+  if ((B > 1 && acc_strides[0] == 0) || (a.c.Hkv > 1 && acc_strides[1] == 0)) return SAGE2_ERR_INVALID_ARG;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return SAGE2_ERR_CUDA;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

@@ -263,9 +263,9 @@ __global__ void __launch_bounds__(kTThreads<E4M3>, 1)
   constexpr int kRing = SHARE ? C::kBufs / 2 : C::kBufs / 4;     // buffers of a ring
   constexpr int kGroup = !E4M3 ? 1 : (SHARE ? 4 : 2);            // loader warps of a ring
   constexpr bool BF = QBF && !E4M3;              // type of the MMA operands
-  // log2 of how far P may exceed 1 before the reference moves: fp16 ends at 2^16; a bf16 P of
-  // 2^40 leaves its sums and O (fp32) far from their end
-  constexpr float kGrow = BF ? 40.f : 14.f;
+  // log2 of how far P may exceed 1 before the reference moves: fp16 ends at 2^16; with a bf16 P of
+  // 2^24 O stays finite up to |V| = 2^100
+  constexpr float kGrow = BF ? 24.f : 14.f;
   constexpr int kMma = 16 + kTLoad<E4M3>;
   extern __shared__ uint8_t smem_raw[];
   Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &

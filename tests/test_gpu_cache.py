@@ -617,3 +617,60 @@ def test_pools_past_32_bits(qa):
     assert qa.sage2_check_device_error() == 0
     for a, b in zip(*got):
         assert same_bits(a, b)
+
+
+@pytest.mark.parametrize("S", [53999, 54001, 80000])
+def test_evict_long_tallies(qa, S):
+    """Tallies on both sides of what the choice holds in shared memory, with many equal ones."""
+    c = R.Case(24, [S, 30000], 1, 2, 1, 64, 128, "bf16", "e4m3", junk=False)
+    x = c.cuda()
+    g = torch.Generator().manual_seed(6)
+    S = c.MP * 128
+    acc = (torch.rand(2, 2, S, generator=g) * 500).floor() / 64
+    keep, sinks, recent = 5001, 3, 77
+    out_table = torch.arange(c.B * 40, dtype=torch.int32).view(2, 40) + c.pages
+    cache = {n: torch.cat([t.view(torch.uint8), torch.zeros(c.B * 40, *t.shape[1:], dtype=torch.uint8)]).view(t.dtype).cuda()
+             if t.dtype == torch.float8_e4m3fn else torch.cat([t, torch.zeros(c.B * 40, *t.shape[1:])]).cuda()
+             for n, t in c.pool.items()}
+    idx, new, kept = qa.sage2_cache_evict(cache, x["table"], x["lens"], acc.cuda(), keep, sinks, recent,
+                                          out_table=out_table.cuda())
+    assert qa.sage2_check_device_error() == 0 and new.tolist() == [keep, keep]
+    for b in range(2):
+        ln = c.lens[b]
+        for h in range(2):
+            mid = np.arange(sinks, ln - recent)
+            best = mid[np.lexsort((mid, -acc[b, h, mid].double().numpy()))[:keep - sinks - recent]]
+            want = np.sort(np.concatenate([np.arange(sinks), best, np.arange(ln - recent, ln)]))
+            assert (idx[b, h].cpu().numpy() == want).all()
+            assert torch.equal(kept[b, h].cpu(), acc[b, h, torch.from_numpy(want)])
+            at = torch.from_numpy(want)
+            src = c.pool["k"].view(torch.uint8)[c.table[b].long()[at // 128], h, at % 128]
+            i = torch.arange(keep)
+            assert torch.equal(cache["k"].view(torch.uint8).cpu()[out_table[b].long()[i // 128], h, i % 128], src)
+
+
+@pytest.mark.parametrize("kv, d", [("same", 128), ("e4m3", 128), ("e4m3", 64)])
+def test_compact_in_place_many_heads(qa, kv, d):
+    """So many heads that a block walks whole rows; indices with repeats and rows that stay."""
+    c = R.Case(25, [200 - b for b in range(30)], 1, 6, 1, d, 16, "bf16", kv, junk=False)
+    x = c.cuda()
+    g = torch.Generator().manual_seed(7)
+    M = 150
+    i = torch.arange(M)
+    idx = (i + (torch.rand(30, 6, M, generator=g) ** 4 * (170 - i).clamp(min=0)).long()).to(torch.int32)
+    count = [(M, 0, 1, 77)[b % 4] for b in range(30)]
+    acc = torch.rand(30, 6, c.MP * 16, generator=g)
+    want = pools_after_move(c.pool, c.table, c.table, 16, idx, count, [0] * 30)
+    wacc = acc.clone()
+    for b in range(30):
+        for h in range(6):
+            wacc[b, h, :count[b]] = acc[b, h, idx[b, h, :count[b]].long()]
+    accd = acc.cuda()
+    qa.sage2_cache_compact(x["cache"], x["table"], idx.cuda(), torch.tensor(count, dtype=torch.int32).cuda(), acc=accd)
+    assert qa.sage2_check_device_error() == 0
+    for name, t in want.items():
+        assert same_bits(x["cache"][name], t), name
+    assert same_bits(accd, wacc)
+    with pytest.raises((ValueError, qa.Sage2Error)):
+        qa.sage2_cache_compact(x["cache"], x["table"], idx.cuda(), acc=acc.cuda(),
+                               acc_out=torch.zeros(30, 1, 160, device="cuda").expand(30, 6, 160))
