@@ -271,33 +271,36 @@ __global__ void __launch_bounds__(kWThreads, 1)
           const int sh = (ex == 0 || ex == 255) ? 0 : max(-113, min(60, 14 + 127 - ex));
           const float up = __uint_as_float((uint32_t)(127 + sh) << 23);
           qs *= __uint_as_float((uint32_t)(127 - sh) << 23);
-          // 16 bytes of each term at a time
+          // 16 bytes of each term at a time, in packed fp16: the scaled values, what each term leaves of
+          // them and the terms themselves are exact there (but for what lies below 2^-24)
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
-            float v[16];
+            uint32_t v[8];
 #pragma unroll
             for (int y = 0; y < 8; ++y) {
               const uint4& ww = w[2 * c + (y >> 2)];
-              const uint32_t e = (y & 3) == 0 ? ww.x : (y & 3) == 1 ? ww.y : (y & 3) == 2 ? ww.z : ww.w;
-              const float2 f = halves<QBF>(e);
-              v[2 * y] = f.x * up;
-              v[2 * y + 1] = f.y * up;
+              const float2 f = halves<QBF>((y & 3) == 0 ? ww.x : (y & 3) == 1 ? ww.y : (y & 3) == 2 ? ww.z : ww.w);
+              v[y] = pack2<false>(f.x * up, f.y * up);
             }
 #pragma unroll
             for (int x = 0; x < C::kTerms; ++x) {
               uint32_t o4[4];
 #pragma unroll
               for (int y = 0; y < 8; ++y) {
-                const __nv_fp8x2_storage_t e =
-                    __nv_cvt_float2_to_fp8x2(make_float2(v[2 * y], v[2 * y + 1]), __NV_SATFINITE, __NV_E5M2);
-                const float2 back = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(e, __NV_E5M2)));
-                v[2 * y] -= back.x;
-                v[2 * y + 1] -= back.y;
+                __half2_raw hv;
+                hv.x = static_cast<unsigned short>(v[y]);
+                hv.y = static_cast<unsigned short>(v[y] >> 16);
+                const __nv_fp8x2_storage_t e = __nv_cvt_halfraw2_to_fp8x2(hv, __NV_SATFINITE, __NV_E5M2);
+                if (x + 1 < C::kTerms) {
+                  const __half2 rest = __hsub2(__half2(hv), __half2(__nv_cvt_fp8x2_to_halfraw2(e, __NV_E5M2)));
+                  v[y] = *reinterpret_cast<const uint32_t*>(&rest);
+                }
                 if (y & 1) o4[y >> 1] |= static_cast<uint32_t>(e) << 16;
                 else o4[y >> 1] = static_cast<uint32_t>(e);
               }
-              *reinterpret_cast<uint4*>(sm.q[x] + line_off<C, kWR>(rl, half * (D / 32) + c)) =
-                  make_uint4(o4[0], o4[1], o4[2], o4[3]);
+              if (rl < cols)
+                *reinterpret_cast<uint4*>(sm.q[x] + line_off<C, kWR>(rl, half * (D / 32) + c)) =
+                    make_uint4(o4[0], o4[1], o4[2], o4[3]);
             }
           }
         }
