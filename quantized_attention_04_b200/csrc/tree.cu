@@ -270,7 +270,7 @@ __device__ __forceinline__ float row_lse(float m, float sum) {
 }
 
 // ------------------------------------------------------------ few rows
-// k_tree_rows: a tile of 16*MT rows (all the rows of a pair where T*G is small)
+// k_tree_rows: a tile of 16 rows (all the rows of a pair where T*G is small)
 // against the keys.  Bound by the cache's bytes: at up to 32 rows a byte of
 // 16-bit cache meets at most 32 multiply-adds, which the legacy tensor path
 // (no TMEM round trip, P stays in registers) sustains well above the rate at
@@ -284,11 +284,13 @@ __device__ __forceinline__ float row_lse(float m, float sum) {
 // falls below fp16's range is under 2^-37 of it).  The key scales multiply the
 // scores; the value scales multiply P, whose reference includes the tile's largest value scale.
 constexpr int kRowsWarps = 4;
+constexpr int MT = 1;                  // m-tiles of 16 rows of a warp; with two the e4m3 form spilled (64 us against
+                                       // 48 to 53 for 20 rows of 8 heads)
 constexpr float kVrefLeast = 1e-30f;   // value scales below it count as part of it
 constexpr int kRowsTile = 16 * kRowsWarps;
 constexpr int kRowsLeast = 2;          // tiles that a block takes at least
 
-template <int D, bool E4M3, int MT>
+template <int D, bool E4M3>
 struct RowsCfg {
   static constexpr int kRowBytes = D * (E4M3 ? 1 : 2);
   static constexpr int kBoxBytes = kRowBytes < 128 ? kRowBytes : 128;   // swizzle span
@@ -297,14 +299,13 @@ struct RowsCfg {
   static constexpr int kStageBytes = 2 * kTileBytes;
   // Blocks of an SM, and stages of a warp in the shared memory that leaves them.  A warp's chain of
   // waits, products and exponentials is long, so that more warps keep more bytes coming than deeper rings.
-  static constexpr int kBlocks = MT == 2 ? 2 : (D == 64 ? 4 : (E4M3 ? 3 : 2));
-  static constexpr int kStages = MT == 2 ? (E4M3 ? (D == 128 ? 4 : 8) : (D == 128 ? 2 : 4))
-                                         : (E4M3 ? (D == 64 ? 4 : 2) : 2);
+  static constexpr int kBlocks = D == 64 ? 4 : (E4M3 ? 3 : 2);
+  static constexpr int kStages = E4M3 && D == 64 ? 4 : 2;
 };
 
-template <int D, bool E4M3, int MT>
+template <int D, bool E4M3>
 struct __align__(1024) RowsSmem {
-  using C = RowsCfg<D, E4M3, MT>;
+  using C = RowsCfg<D, E4M3>;
   uint8_t kv[kRowsWarps][C::kStages][C::kStageBytes];
   float sc[kRowsWarps][C::kStages][E4M3 ? 32 : 4];  // key scales, value scales
   float red[kRowsWarps][16][D + 4];                 // O of the rows of an m-tile
@@ -317,21 +318,21 @@ struct __align__(1024) RowsSmem {
 // Byte offset of 16-byte chunk `ch` of row `r` in a tile of 16 rows.
 template <int D, bool E4M3>
 __device__ __forceinline__ uint32_t rows_off(int r, int ch) {
-  using C = RowsCfg<D, E4M3, 1>;
+  using C = RowsCfg<D, E4M3>;
   if (C::kBoxBytes == 128)
     return (ch >> 3) * (16 * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
   return r * 64 + ((ch ^ ((r >> 1) & 3)) << 4);
 }
 
-template <int D, bool E4M3, bool QBF, int MT>
-__global__ void __launch_bounds__(32 * kRowsWarps, (RowsCfg<D, E4M3, MT>::kBlocks))
+template <int D, bool E4M3, bool QBF>
+__global__ void __launch_bounds__(32 * kRowsWarps, (RowsCfg<D, E4M3>::kBlocks))
     k_tree_rows(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                 const __grid_constant__ TreeArgs a) {
-  using C = RowsCfg<D, E4M3, MT>;
+  using C = RowsCfg<D, E4M3>;
   constexpr bool BF = QBF && !E4M3;           // type of the MMA operands
   constexpr int NT = D / 8;                   // n-tiles of O
   extern __shared__ uint8_t smem_raw[];
-  RowsSmem<D, E4M3, MT>& sm = *reinterpret_cast<RowsSmem<D, E4M3, MT>*>(
+  RowsSmem<D, E4M3>& sm = *reinterpret_cast<RowsSmem<D, E4M3>*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, c = lane & 3;
@@ -944,9 +945,9 @@ static cudaError_t launch_join(const TreeArgs& a, int tile, int rows_tile, int g
   return cudaGetLastError();
 }
 
-template <int D, bool E4M3, bool QBF, int MT>
+template <int D, bool E4M3, bool QBF>
 static cudaError_t launch_rows(TreeArgs a, int dev, cudaMemPool_t pool, cudaStream_t st) {
-  using C = RowsCfg<D, E4M3, MT>;
+  using C = RowsCfg<D, E4M3>;
   a.RT = (a.G * a.T + 16 * MT - 1) / (16 * MT);
   const int grid = C::kBlocks * sm_count(dev);
   CUtensorMap tk, tv;
@@ -961,8 +962,8 @@ static cudaError_t launch_rows(TreeArgs a, int dev, cudaMemPool_t pool, cudaStre
   const size_t prow = (size_t)2 * grid * 16 * MT;
   e = split_workspace(&a, prow, D, pool, st);
   if (e != cudaSuccess) return e;
-  auto kern = k_tree_rows<D, E4M3, QBF, MT>;
-  const int smem = sizeof(RowsSmem<D, E4M3, MT>) + 1024;
+  auto kern = k_tree_rows<D, E4M3, QBF>;
+  const int smem = sizeof(RowsSmem<D, E4M3>) + 1024;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e == cudaSuccess) {
     kern<<<grid, 32 * kRowsWarps, smem, st>>>(tk, tv, a);
@@ -982,9 +983,12 @@ namespace sage2 {
 
 template <int D, bool E4M3, bool QBF>
 static cudaError_t tree_pick(const TreeArgs& a, int dev, cudaMemPool_t pool, cudaStream_t st) {
+  // A row tile of 16 reads the cache once more, from L2 mostly; k_tree_tiles reads it once and costs the same
+  // for 17 rows as for 128.  Measured, us (1 x 32768 / 8 x 4096 / 32 x 1000 slots, 8 heads, d = 128):
+  //   16 bits  16 rows: tiles of 16 37 / 34 / 33, k_tree_tiles 39 / 37 / 39;  20 rows: 54 / 46 / 50, 40 / 37 / 41
+  //   e4m3     44 rows: tiles of 16 71 / 65 / 76, k_tree_tiles 76 / 80 / 97;  64 rows: k_tree_tiles 78 / 80 / 105
   const int R = a.G * a.T;
-  if (R <= 16) return launch_rows<D, E4M3, QBF, 1>(a, dev, pool, st);
-  if (R <= 32) return launch_rows<D, E4M3, QBF, 2>(a, dev, pool, st);
+  if (R <= (E4M3 ? 48 : 16)) return launch_rows<D, E4M3, QBF>(a, dev, pool, st);
   if (R <= kTR) return launch_tiles<D, E4M3, QBF, false>(a, dev, pool, st);
   return launch_tiles<D, E4M3, QBF, true>(a, dev, pool, st);
 }
