@@ -60,6 +60,14 @@ __device__ __forceinline__ SeqLen seq_len(const int* lens, const int* ns, int b,
 __device__ __forceinline__ bool tree_allows(const uint8_t* mask, int T, int i, int j) {
   return mask ? __ldg(mask + (size_t)i * T + j) != 0 : j <= i;
 }
+// Does drafted token i of a sequence (n > 0) attend slot `key`?  The byte of the mask is asked for in any case,
+// at the nearest drafted slot, so that many such loads are on their way at once (behind a condition each
+// waited for the one before: 16 us for the 128 keys and 256 rows of an edge tile of the tally).
+__device__ __forceinline__ bool slot_allowed(const TreeArgs& a, const uint8_t* mask, SeqLen s, int i, int key) {
+  const int j = key - s.len;
+  const bool in = tree_allows(mask, a.T, i, min(max(j, 0), s.n - 1));
+  return j < 0 || (j < s.n && in);
+}
 
 // ------------------------------------------------------------ the work split
 // A block's run of the global tile sequence and the pair it starts in.
@@ -577,14 +585,14 @@ __global__ void __launch_bounds__(32 * kRowsWarps, (RowsCfg<D, E4M3>::kBlocks))
           if (edge) {
             const int r = row0 + mt * 16 + g + 8 * e;
             const int i = r % a.T;
+            const uint8_t* mask = a.mask ? a.mask + at.b * a.mask_sb : nullptr;
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
               for (int y = 0; y < 2; ++y) {
-                const int k = 8 * j + 2 * c + y, jj = key0 + k - at.s.len;
-                const bool ok = k < live && r < R &&
-                                (jj < 0 || tree_allows(a.mask ? a.mask + at.b * a.mask_sb : nullptr, a.T, i, jj));
-                if (!ok) x[mt][e][j][y] = -INFINITY;
+                const int k = 8 * j + 2 * c + y;
+                const bool in = slot_allowed(a, mask, at.s, i, key0 + k);
+                if (!(in && k < live && r < R)) x[mt][e][j][y] = -INFINITY;
                 else if ((badrows >> k) & 1u) x[mt][e][j][y] = __int_as_float(0x7fffffff);
               }
           }

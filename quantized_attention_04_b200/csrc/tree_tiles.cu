@@ -177,12 +177,6 @@ __device__ __forceinline__ bool tile_wait(uint64_t* bar, uint32_t parity, volati
   return ok;
 }
 
-// Does drafted token i of a sequence attend slot `key`?
-__device__ __forceinline__ bool slot_allowed(const TreeArgs& a, const uint8_t* mask, SeqLen s, int i, int key) {
-  const int j = key - s.len;
-  return j < 0 || (j < s.n && tree_allows(mask, a.T, i, j));
-}
-
 // 32 lanes x 16 consecutive columns: thread t gets lane (base + t).
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
@@ -800,7 +794,7 @@ __global__ void __launch_bounds__(kTThreads<E4M3>, 1)
 #pragma unroll 1
           for (int c = 0; c < kTK; c += 32) {
             uint32_t bits = 0;
-#pragma unroll 4
+#pragma unroll 8
             for (int y = 0; y < 16; ++y)
               if (slot_allowed(a, mask, at.s, y & 2 ? i1 : i0, key0 + c + 8 * (y >> 2) + 2 * g + (y & 1)))
                 bits |= 1u << y;

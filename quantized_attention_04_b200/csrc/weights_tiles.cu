@@ -221,97 +221,6 @@ __global__ void __launch_bounds__(kWThreads, 1)
       const uint8_t* mask = a.mask ? a.mask + at.b * a.mask_sb : nullptr;
       if (L > S && tid == 0 && h == 0) atomicOr(&g_device_error, DEVERR_BOUNDS);
       for (int u = 0; u < a.RT; ++u) {
-        // ---- the unit's rows: two threads a row.  Rows that do not count become zeros with z = +inf.
-        const int rl = tid >> 1, half = tid & 1, r = u * rows_unit + rl;
-        const int i = r % a.T;
-        float z = INFINITY;
-        const bool there = rl < rows_unit && r < R && i < at.s.n;
-        if (there) {
-          z = __ldg(lse + ((size_t)at.b * a.Hq + h * a.G + r / a.T) * a.T + i) * kL2E;
-          if (z == -INFINITY) z = INFINITY;
-        }
-        uint4 w[D / 16];
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at.b * a.sb +
-                                                          (long long)(h * a.G + (there ? r / a.T : 0)) * a.sh +
-                                                          (long long)(there ? i : 0) * a.st) + half * (D / 16);
-#pragma unroll
-        for (int c = 0; c < D / 16; ++c) w[c] = there ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-        if (z == INFINITY) {
-#pragma unroll
-          for (int c = 0; c < D / 16; ++c) w[c] = make_uint4(0u, 0u, 0u, 0u);
-        }
-        float qs = a.sm_scale * kL2E;
-        // everyone is done with the last unit's rows: the threads have all read its last tile, and its
-        // MMAs are over (d_full has been waited for)
-        bar_exp();
-        if (!E4M3) {
-#pragma unroll
-          for (int c = 0; c < D / 16; ++c)
-            *reinterpret_cast<uint4*>(sm.q[0] + line_off<C, kWR>(rl, half * (D / 16) + c)) = w[c];
-        } else {
-          float amax = 0.f;
-#pragma unroll
-          for (int c = 0; c < D / 16; ++c) {
-            const uint32_t w4[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const float2 f = halves<QBF>(w4[y]);
-              amax = max3f(amax, fabsf(f.x), fabsf(f.y));
-            }
-          }
-#pragma unroll
-          for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-          if (lane == 0) sm.amax[warp] = amax;
-          bar_exp();
-          amax = sm.amax[lane & (kWExp - 1)];
-#pragma unroll
-          for (int o = 8; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-          // an exact power of two that puts the unit's largest value at 2^14
-          const int ex = (int)(__float_as_uint(amax) >> 23);
-          const int sh = (ex == 0 || ex == 255) ? 0 : max(-113, min(60, 14 + 127 - ex));
-          const float up = __uint_as_float((uint32_t)(127 + sh) << 23);
-          qs *= __uint_as_float((uint32_t)(127 - sh) << 23);
-          // 16 bytes of each term at a time, in packed fp16: the scaled values, what each term leaves of
-          // them and the terms themselves are exact there (but for what lies below 2^-24)
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t v[8];
-#pragma unroll
-            for (int y = 0; y < 8; ++y) {
-              const uint4& ww = w[2 * c + (y >> 2)];
-              const float2 f = halves<QBF>((y & 3) == 0 ? ww.x : (y & 3) == 1 ? ww.y : (y & 3) == 2 ? ww.z : ww.w);
-              v[y] = pack2<false>(f.x * up, f.y * up);
-            }
-#pragma unroll
-            for (int x = 0; x < C::kTerms; ++x) {
-              uint32_t o4[4];
-#pragma unroll
-              for (int y = 0; y < 8; ++y) {
-                __half2_raw hv;
-                hv.x = static_cast<unsigned short>(v[y]);
-                hv.y = static_cast<unsigned short>(v[y] >> 16);
-                const __nv_fp8x2_storage_t e = __nv_cvt_halfraw2_to_fp8x2(hv, __NV_SATFINITE, __NV_E5M2);
-                if (x + 1 < C::kTerms) {
-                  const __half2 rest = __hsub2(__half2(hv), __half2(__nv_cvt_fp8x2_to_halfraw2(e, __NV_E5M2)));
-                  v[y] = *reinterpret_cast<const uint32_t*>(&rest);
-                }
-                if (y & 1) o4[y >> 1] |= static_cast<uint32_t>(e) << 16;
-                else o4[y >> 1] = static_cast<uint32_t>(e);
-              }
-              if (rl < cols)
-                *reinterpret_cast<uint4*>(sm.q[x] + line_off<C, kWR>(rl, half * (D / 32) + c)) =
-                    make_uint4(o4[0], o4[1], o4[2], o4[3]);
-            }
-          }
-        }
-        if (half == 0) {
-          sm.z[rl] = -z;
-          sm.tok[rl] = i;
-        }
-        fence_proxy_async_smem();
-        bar_exp();
-        if (lane == 0) mbar_arrive(&sm.q_full);
-
         // this group's tiles: every other one; the page of the thread's key two of them ahead, the key
         // scale one
         const int k0 = (t & 1) == group ? 0 : 1;
@@ -328,8 +237,108 @@ __global__ void __launch_bounds__(kWThreads, 1)
           const int key = (at.tile + k) * kWK + key_l;
           return part == 0 && k < cnt && key < L && key < S ? tally[at.b * ab + h * ah + key] : 0.f;
         };
-        float ks = scale_of(k0, page_of(k0)), next_old = old_of(k0);
+        const int page0 = page_of(k0);
         int page = page_of(k0 + 2);
+        // ---- the unit's rows: two threads a row.  Rows that do not count become zeros with z = +inf.
+        const int rl = tid >> 1, half = tid & 1, r = u * rows_unit + rl;
+        const int i = r % a.T;
+        float z = INFINITY;
+        const bool there = rl < rows_unit && r < R && i < at.s.n;
+        const bool mine_q = 16 * warp < cols;           // this warp's rows are among the MMA's columns
+        if (there) {
+          z = __ldg(lse + ((size_t)at.b * a.Hq + h * a.G + r / a.T) * a.T + i) * kL2E;
+          if (z == -INFINITY) z = INFINITY;
+        }
+        uint4 w[D / 16];
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at.b * a.sb +
+                                                          (long long)(h * a.G + (there ? r / a.T : 0)) * a.sh +
+                                                          (long long)(there ? i : 0) * a.st) + half * (D / 16);
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) w[c] = there ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+        float ks = scale_of(k0, page0);
+        if (z == INFINITY) {
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) w[c] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        float qs = a.sm_scale * kL2E;
+        // everyone is done with the last unit's rows: the threads have all read its last tile, and its
+        // MMAs are over (d_full has been waited for)
+        bar_exp();
+        // (after it: with an odd count of tiles the other group has added the unit before to them)
+        float next_old = old_of(k0);
+        if (!E4M3) {
+          if (mine_q) {
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c)
+              *reinterpret_cast<uint4*>(sm.q[0] + line_off<C, kWR>(rl, half * (D / 16) + c)) = w[c];
+          }
+        } else {
+          float amax = 0.f;
+          if (mine_q) {
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+              const uint32_t w4[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                const float2 f = halves<QBF>(w4[y]);
+                amax = max3f(amax, fabsf(f.x), fabsf(f.y));
+              }
+            }
+          }
+#pragma unroll
+          for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          if (lane == 0) sm.amax[warp] = amax;
+          bar_exp();
+          amax = sm.amax[lane & (kWExp - 1)];
+#pragma unroll
+          for (int o = 8; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          // an exact power of two that puts the unit's largest value at 2^14
+          const int ex = (int)(__float_as_uint(amax) >> 23);
+          const int sh = (ex == 0 || ex == 255) ? 0 : max(-113, min(60, 14 + 127 - ex));
+          const float up = __uint_as_float((uint32_t)(127 + sh) << 23);
+          qs *= __uint_as_float((uint32_t)(127 - sh) << 23);
+          // 16 bytes of each term at a time, in packed fp16: the scaled values, what each term leaves of
+          // them and the terms themselves are exact there (but for what lies below 2^-24)
+          if (mine_q) {
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t v[8];
+#pragma unroll
+              for (int y = 0; y < 8; ++y) {
+                const uint4& ww = w[2 * c + (y >> 2)];
+                const float2 f = halves<QBF>((y & 3) == 0 ? ww.x : (y & 3) == 1 ? ww.y : (y & 3) == 2 ? ww.z : ww.w);
+                v[y] = pack2<false>(f.x * up, f.y * up);
+              }
+#pragma unroll
+              for (int x = 0; x < C::kTerms; ++x) {
+                uint32_t o4[4];
+#pragma unroll
+                for (int y = 0; y < 8; ++y) {
+                  __half2_raw hv;
+                  hv.x = static_cast<unsigned short>(v[y]);
+                  hv.y = static_cast<unsigned short>(v[y] >> 16);
+                  const __nv_fp8x2_storage_t e = __nv_cvt_halfraw2_to_fp8x2(hv, __NV_SATFINITE, __NV_E5M2);
+                  if (x + 1 < C::kTerms) {
+                    const __half2 rest = __hsub2(__half2(hv), __half2(__nv_cvt_fp8x2_to_halfraw2(e, __NV_E5M2)));
+                    v[y] = *reinterpret_cast<const uint32_t*>(&rest);
+                  }
+                  if (y & 1) o4[y >> 1] |= static_cast<uint32_t>(e) << 16;
+                  else o4[y >> 1] = static_cast<uint32_t>(e);
+                }
+                *reinterpret_cast<uint4*>(sm.q[x] + line_off<C, kWR>(rl, half * (D / 32) + c)) =
+                    make_uint4(o4[0], o4[1], o4[2], o4[3]);
+              }
+            }
+          }
+        }
+        if (half == 0) {
+          sm.z[rl] = -z;
+          sm.tok[rl] = i;
+        }
+        fence_proxy_async_smem();
+        bar_exp();
+        if (lane == 0) mbar_arrive(&sm.q_full);
+
         const int c0 = part ? cols0 : 0, c1st = part ? cols : cols0;      // this warp's columns
         for (int k = k0; k < cnt; k += 2) {
           const int tt = t + k, key0 = (at.tile + k) * kWK, key = key0 + key_l, p = group;
