@@ -272,6 +272,12 @@ __device__ __forceinline__ void store2(void* out, int dtype, size_t idx, float x
   if (dtype == 2) *reinterpret_cast<float2*>(static_cast<float*>(out) + idx) = make_float2(x, y);
   else *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(out) + idx) = dtype == 1 ? pack2<true>(x, y) : pack2<false>(x, y);
 }
+// Value scales outside of these count as one of them in P's reference.
+constexpr float kVrefLeast = 1e-30f, kVrefMost = 1.6e32f;   // the second: 2^107
+// log2 of a value scale as P's reference counts it (NaN: the least).
+__device__ __forceinline__ float vref_log2(float scale) {
+  return __log2f(fminf(fmaxf(scale, kVrefLeast), kVrefMost));
+}
 // ln of a row's sum of exponentials from its maximum (log2 units) and the sum relative to it.
 __device__ __forceinline__ float row_lse(float m, float sum) {
   return (m + log2f(sum)) * 0.6931471805599453f;
@@ -290,11 +296,11 @@ __device__ __forceinline__ float row_lse(float m, float sum) {
 // e4m3 cache: codes become fp16 in registers (exact).  Q (fp16 or bf16) enters as
 // fp16 scaled by a power of two that puts the row's largest value at 2^13 (what
 // falls below fp16's range is under 2^-37 of it).  The key scales multiply the
-// scores; the value scales multiply P, whose reference includes the tile's largest value scale.
+// scores; the value scales multiply P, whose reference is the largest of score + log2(value scale) among the
+// keys that the row attends: a large value row that weighs nothing takes no bits from the others.
 constexpr int kRowsWarps = 4;
 constexpr int MT = 1;                  // m-tiles of 16 rows of a warp; with two the e4m3 form spilled (64 us against
                                        // 48 to 53 for 20 rows of 8 heads)
-constexpr float kVrefLeast = 1e-30f;   // value scales below it count as part of it
 constexpr int kRowsTile = 16 * kRowsWarps;
 constexpr int kRowsLeast = 2;          // tiles that a block takes at least
 
@@ -553,7 +559,9 @@ __global__ void __launch_bounds__(32 * kRowsWarps, (RowsCfg<D, E4M3>::kBlocks))
       }
       // ---- softmax of the 16 keys: this thread has keys 8j + 2c + {0,1} of rows g, g+8.  The
       // exponentials are taken against the reference that the earlier keys have left; it moves (and
-      // the sums and O with it) only when a score of the warp lies far above it.
+      // the sums and O with it) only when a score of the warp lies far above it.  e4m3: whether it does is
+      // asked of a bound, the largest score and the tile's largest value scale (lv); where it moves to, of
+      // each key's own.
       float kscl[2][2], vscl[2][2], lv = 0.f;
       if (E4M3) {
         float vm = kVrefLeast;
@@ -604,10 +612,15 @@ __global__ void __launch_bounds__(32 * kRowsWarps, (RowsCfg<D, E4M3>::kBlocks))
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float mx = fmaxf(fmaxf(x[mt][e][0][0], x[mt][e][0][1]), fmaxf(x[mt][e][1][0], x[mt][e][1][1]));
+            float mx = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int y = 0; y < 2; ++y)
+                mx = fmaxf(mx, E4M3 ? x[mt][e][j][y] + vref_log2(vscl[j][y]) : x[mt][e][j][y]);
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            const float now = mx == -INFINITY ? m[mt][e] : fmaxf(m[mt][e], mx + lv);
+            const float now = fmaxf(m[mt][e], mx);
             const float f = m[mt][e] == -INFINITY ? 0.f : ex2(m[mt][e] - now);
             m[mt][e] = now;
             l[mt][e] *= f;

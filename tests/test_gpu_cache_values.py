@@ -1,0 +1,120 @@
+"""Attention over a paged cache where its values are far apart: value rows of very different sizes, scores that
+climb late, sums of many keys.  Against 64-bit definitions; tolerances as derived in tests/test_gpu_cache.py,
+but for P's absolute rounding with an e4m3 cache.  P times a key's value scale is packed to fp16 relative to the
+largest such product among the keys that the row attends (at most: a reference that lags is below it), so that
+each key is off by 2^-25 of that largest product, times its code of 448 at most.
+"""
+import math
+
+import pytest
+import torch
+
+from tests import cache_ref as R
+from tests.test_gpu_cache import logit_error
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def qa():
+    from quantized_attention_04_b200 import build
+    build.build()
+    import quantized_attention_04_b200 as m
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    m.lib()
+    assert m.sage2_check_device_error() == 0
+    return m
+
+
+def attend(c):
+    """(o, lse, mag, top): outputs in 64 bits, sum_s w_s |V_s| and the largest w_s * (value scale of s)."""
+    B, Hq = c.B, c.Hkv * c.G
+    o = torch.zeros(B, Hq, c.T, c.d, dtype=torch.float64)
+    lse, mag = torch.full((B, Hq, c.T), -math.inf, dtype=torch.float64), torch.zeros_like(o)
+    top = torch.zeros(B, Hq, c.T, dtype=torch.float64)
+    for b in range(B):
+        ln, n = c.lens[b], c.n[b]
+        bar = torch.zeros(n, ln + n, dtype=torch.float64)
+        bar[:, ln:][~c.mask[b, :n, :n]] = -math.inf
+        for h in range(c.Hkv):
+            K, V = (c.dense(w, b, h, ln + n) for w in "kv")
+            size = V.abs().amax(-1) / 448
+            for g in range(c.G):
+                r = h * c.G + g
+                s = c.q[b, r, :n].double() @ K.T * c.sm + bar
+                z = torch.logsumexp(s, -1)
+                w = torch.exp(s - z[:, None])
+                o[b, r, :n], mag[b, r, :n], lse[b, r, :n] = w @ V, w @ V.abs(), z
+                top[b, r, :n] = (w * size).amax(-1)
+    return o, lse, mag, top
+
+
+def check(c, o, lse, want):
+    """o in fp32."""
+    wo, wl, mag, top = want
+    e = logit_error(c)
+    keys = max(x + y for x, y in zip(c.lens, c.n))
+    bf = c.dtype == torch.bfloat16 and c.kv != "e4m3"
+    # an exponential against a reference r away is off by 2^-24 |x - r|, counted in logit_error by |x|
+    rel = math.expm1(2 * e) + (2.0 ** -8 if bf else 2.0 ** -11) + 4 * 2.0 ** -24 + keys * 2.0 ** -24
+    tol = rel * mag + 1e-30
+    if not bf:
+        tol = tol + (2.0 ** -25 * keys * 448) * top[..., None]
+    o, lse = o.double().cpu(), lse.double().cpu()
+    assert torch.isfinite(o).all()
+    err = (o - wo).abs()
+    assert (err <= tol).all(), ("o", (err > tol).nonzero()[:5].tolist(), (err / tol).max().item())
+    ltol = e + 2.0 ** -22 * (wl.abs() + 1) + keys * 2.0 ** -24
+    assert ((lse - wl).abs() <= ltol).all(), ("lse", (lse - wl).abs().max().item())
+
+
+def cell(c, b, slot):
+    return int(c.table[b, slot // c.page]), slot % c.page
+
+
+# rows of a head: up to 48 one kernel, more the other (up to 128 and above)
+ROWS = [(1, 1, 128), (4, 4, 64), (9, 5, 128), (50, 1, 128), (31, 4, 64), (64, 4, 128), (64, 8, 64)]
+
+
+@pytest.mark.parametrize("up", [12, 20, 40, 60])
+@pytest.mark.parametrize("T, G, d", ROWS)
+def test_large_value_rows_that_weigh_nothing(qa, T, G, d, up):
+    """A drafted token's value row of 2^up times the others' size leaves the rows that do not attend it alone,
+    and a context token's counts for no more than its weight."""
+    c = R.Case(31, [200, 75], T, 2, G, d, 16, "bf16", "e4m3")
+    if T > 1:                                    # token 1 is attended by itself alone
+        c.mask[:, :, 1] = False
+        c.mask[:, 1, 1] = True
+    base = torch.randn(2 * G, 1, d, generator=torch.Generator().manual_seed(5))
+    c.q = (c.q + 4 * base).to(c.dtype)
+    for b in range(2):
+        if T > 1:
+            p, r = cell(c, b, c.lens[b] + 1)
+            c.pool["v_scale"][p, :, r] *= 2.0 ** up
+        for slot in (3, 70):                     # keys that point away from the queries of the first head
+            p, r = cell(c, b, slot)
+            for h in range(2):
+                far = -base[h * G, 0] / base[h * G, 0].norm() * 30
+                c.pool["k"].view(torch.uint8)[p, h, r], c.pool["k_scale"][p, h, r] = (
+                    x.view(torch.uint8) if x.dtype == torch.float8_e4m3fn else x for x in R.codes(far))
+                c.pool["v_scale"][p, h, r] *= 2.0 ** (up - 4)
+    x = c.cuda()
+    o, lse = qa.sage2_attn_tree(out_dtype=torch.float32, **x)
+    assert qa.sage2_check_device_error() == 0
+    check(c, o, lse, attend(c))
+
+
+@pytest.mark.parametrize("T, G, d", ROWS)
+def test_infinite_value_scale_of_a_context_token(qa, T, G, d):
+    """Every token attends it: o is not finite, and lse is what the keys alone make it."""
+    c = R.Case(32, [100], T, 2, G, d, 16, "bf16", "e4m3")
+    want = attend(c)[1]
+    p, r = cell(c, 0, 40)
+    c.pool["v_scale"][p, 1, r] = math.inf
+    x = c.cuda()
+    o, lse = qa.sage2_attn_tree(out_dtype=torch.float32, **x)
+    assert qa.sage2_check_device_error() == 0
+    assert torch.isfinite(o[:, :G]).all() and not torch.isfinite(o[:, G:]).any()
+    e = logit_error(c)
+    tol = e + 2.0 ** -22 * (want.abs() + 1) + (100 + T) * 2.0 ** -24
+    assert ((lse.double().cpu() - want).abs() <= tol).all()
