@@ -272,8 +272,10 @@ __device__ __forceinline__ void store2(void* out, int dtype, size_t idx, float x
   if (dtype == 2) *reinterpret_cast<float2*>(static_cast<float*>(out) + idx) = make_float2(x, y);
   else *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(out) + idx) = dtype == 1 ? pack2<true>(x, y) : pack2<false>(x, y);
 }
-// Value scales outside of these count as one of them in P's reference.
-constexpr float kVrefLeast = 1e-30f, kVrefMost = 1.6e32f;   // the second: 2^107
+// Value scales outside of these count as one of them in P's reference: 2^-80, as a sum of 2^30 exponentials, each
+// 2^14 above the reference at most, is then below 2^124; and 2^107, as the exponential of a key with such a
+// scale is then still a normal number.
+constexpr float kVrefLeast = 8.2718061e-25f, kVrefMost = 1.6225928e32f;
 // log2 of a value scale as P's reference counts it (NaN: the least).
 __device__ __forceinline__ float vref_log2(float scale) {
   return __log2f(fminf(fmaxf(scale, kVrefLeast), kVrefMost));

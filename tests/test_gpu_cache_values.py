@@ -118,3 +118,39 @@ def test_infinite_value_scale_of_a_context_token(qa, T, G, d):
     e = logit_error(c)
     tol = e + 2.0 ** -22 * (want.abs() + 1) + (100 + T) * 2.0 ** -24
     assert ((lse.double().cpu() - want).abs() <= tol).all()
+
+
+def two_levels(kv, d, page, slots, B, G, rise, v):
+    """B sequences of `slots` slots (the last a drafted token) over two pages in turn: all keys of the first have
+    the score 0, of the second `rise` log2 units; all values are v.  (arguments of the call, lse)"""
+    dt = torch.bfloat16
+    pool = {}
+    for name, rows in (("k", (0.0, 1.0)), ("v", (v, v))):
+        x = torch.tensor(rows, dtype=torch.float64)[:, None, None, None].expand(2, 1, page, d).to(dt)
+        if kv == "e4m3":
+            pool[name], pool[name + "_scale"] = R.codes(x)
+        else:
+            pool[name] = x.clone(memory_format=torch.contiguous_format)
+    key = float(R.codes(torch.ones(1, d))[1]) * 448 if kv == "e4m3" else 1.0
+    MP = slots // page
+    table = (torch.arange(MP, dtype=torch.int32) % 2).expand(B, MP).contiguous().cuda()
+    sm = rise * math.log(2.0) / d
+    x = dict(q=torch.ones(B, G, 1, d, dtype=dt, device="cuda"), cache={n: t.cuda() for n, t in pool.items()},
+             table=table, lens=torch.full((B,), slots - 1, dtype=torch.int32, device="cuda"), sm_scale=sm)
+    high = (MP // 2) * page
+    lse = math.log((slots - high) + high * math.exp(key * d * sm))
+    return x, lse
+
+
+@pytest.mark.parametrize("G", [1, 33, 64, 160])
+def test_sums_of_keys_without_values(qa, G):
+    """Many keys whose value rows are zero, their scores rising by less than moves the reference: lse is finite."""
+    slots, rise = 20_000_000 // 256 * 256, 13.9
+    x, want = two_levels("e4m3", 64, 128, slots, 1, G, rise, 0.0)
+    o, lse = qa.sage2_attn_tree(out_dtype=torch.float32, **x)
+    assert qa.sage2_check_device_error() == 0
+    assert (o == 0).all()
+    # logits and their exponentials as in logit_error; a thread adds the keys of its block at most
+    x = rise * math.log(2.0)
+    tol = x * (64 * 2.0 ** -23 + 4 * 2.0 ** -24) + 2.0 ** -22 * (want + 2) + (slots / 148 + 1024) * 2.0 ** -24
+    assert ((lse.double() - want).abs() <= tol).all(), (lse.min().item(), lse.max().item(), want)
