@@ -328,8 +328,8 @@ sage2_status sage2_cache_append(const void* k, const void* v, int dtype, const i
  * A token with nothing to attend and the tokens i >= n[b] get o = 0, lse = -inf.
  * Slots from lens[b] + n[b] on may hold any bits, and an infinity or NaN in the
  * row of a drafted token reaches only the tokens that attend it (their whole o
- * is NaN).  |v| is to be below 2^100; in an SAGE2_E4M3 cache rows of values below
- * 2^-85 may count as zeros.  Scores, their maxima and sums and the
+ * is NaN).  |v| * (lens[b] + n[b]) is to stay below 2^114; in an SAGE2_E4M3 cache
+ * rows of values below 2^-85 may count as zeros.  Scores, their maxima and sums and the
  * accumulators are fp32; P is rounded to the MMA's 16-bit type.  The order of the
  * sums depends on the sizes and lengths alone, so equal calls give equal bits.
  */

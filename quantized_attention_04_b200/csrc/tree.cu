@@ -276,6 +276,9 @@ __device__ __forceinline__ void store2(void* out, int dtype, size_t idx, float x
 // 2^14 above the reference at most, is then below 2^124; and 2^107, as the exponential of a key with such a
 // scale is then still a normal number.
 constexpr float kVrefLeast = 8.2718061e-25f, kVrefMost = 1.6225928e32f;
+// log2 of how far P may exceed 1 before the reference moves: an fp16 P ends at 2^16, and O, a sum of P V over
+// N keys, stays finite up to |V| N = 2^114.
+constexpr float kRefGrow = 14.f;
 // log2 of a value scale as P's reference counts it (NaN: the least).
 __device__ __forceinline__ float vref_log2(float scale) {
   return __log2f(fminf(fmaxf(scale, kVrefLeast), kVrefMost));
@@ -414,8 +417,6 @@ __global__ void __launch_bounds__(32 * kRowsWarps, (RowsCfg<D, E4M3>::kBlocks))
   uint32_t qf[MT][D / 16][4];
   float acc[MT][NT][4];
   float m[MT][2], l[MT][2], qs[MT][2];        // m: the reference (log2 units)
-  // log2 of how far P may exceed 1: fp16 ends at 2^16; with a bf16 P of 2^24 O stays finite up to |V| = 2^100
-  constexpr float kGrow = BF ? 24.f : 14.f;
   const float kL2E = 1.4426950408889634f;
 
   for (int t = 0; t < nt; ++t) {
@@ -607,7 +608,7 @@ __global__ void __launch_bounds__(32 * kRowsWarps, (RowsCfg<D, E4M3>::kBlocks))
               }
           }
           const float mx = fmaxf(fmaxf(x[mt][e][0][0], x[mt][e][0][1]), fmaxf(x[mt][e][1][0], x[mt][e][1][1]));
-          over = over || (mx > -INFINITY && mx + lv > m[mt][e] + kGrow);
+          over = over || (mx > -INFINITY && mx + lv > m[mt][e] + kRefGrow);
         }
       if (__any_sync(0xffffffffu, over)) {
 #pragma unroll

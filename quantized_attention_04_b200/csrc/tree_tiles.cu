@@ -15,7 +15,7 @@
 //
 // The softmax passes over S once: exponentials are taken against the reference
 // left by the earlier keys, and only if some score of the warp's rows lies far above
-// it (kGrow) the reference moves, and O and the row sums are rescaled.  A P above 1
+// it (kRefGrow) the reference moves, and O and the row sums are rescaled.  A P above 1
 // keeps its relative precision.
 //
 // 16-bit caches: K and V arrive by TMA, a box a page.  e4m3 caches: eight warps load
@@ -315,9 +315,6 @@ __global__ void __launch_bounds__(kTThreads<E4M3>, 1)
   constexpr int kRing = SHARE ? C::kBufs / 2 : C::kBufs / 4;     // buffers of a ring
   constexpr int kGroup = !E4M3 ? 1 : (SHARE ? 4 : 2);            // loader warps of a ring
   constexpr bool BF = QBF && !E4M3;              // type of the MMA operands
-  // log2 of how far P may exceed 1 before the reference moves: fp16 ends at 2^16; with a bf16 P of
-  // 2^24 O stays finite up to |V| = 2^100
-  constexpr float kGrow = BF ? 24.f : 14.f;
   constexpr int kMma = 16 + kTLoad<E4M3>;
   extern __shared__ uint8_t smem_raw[];
   Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -894,8 +891,8 @@ __global__ void __launch_bounds__(kTThreads<E4M3>, 1)
               }
             }
             // e4m3: a bound, the largest score and the tile's largest value scale
-            const bool over = (mx[0] > -INFINITY && mx[0] * qs[0] + lv > ref[0] + kGrow) ||
-                              (mx[1] > -INFINITY && mx[1] * qs[1] + lv > ref[1] + kGrow);
+            const bool over = (mx[0] > -INFINITY && mx[0] * qs[0] + lv > ref[0] + kRefGrow) ||
+                              (mx[1] > -INFINITY && mx[1] * qs[1] + lv > ref[1] + kRefGrow);
             if (!__any_sync(0xffffffffu, over)) break;
             // the references move to the largest scores so far: the sums and O (at rest once P V of
             // the tile before is done) follow, and the tile is done again

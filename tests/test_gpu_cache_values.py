@@ -154,3 +154,19 @@ def test_sums_of_keys_without_values(qa, G):
     x = rise * math.log(2.0)
     tol = x * (64 * 2.0 ** -23 + 4 * 2.0 ** -24) + 2.0 ** -22 * (want + 2) + (slots / 148 + 1024) * 2.0 ** -24
     assert ((lse.double() - want).abs() <= tol).all(), (lse.min().item(), lse.max().item(), want)
+
+
+@pytest.mark.parametrize("G", [1, 16, 64, 160])
+@pytest.mark.parametrize("rise", [23.5, 13.5])
+def test_large_values_of_many_keys(qa, G, rise):
+    """16-bit caches: values just below 2^100, 8192 keys a sequence, scores that rise in the middle of a run."""
+    v = float(torch.tensor(2.0 ** 99.9).to(torch.bfloat16))
+    x, want = two_levels("same", 128, 64, 8192, 16, G, rise, v)
+    o, lse = qa.sage2_attn_tree(out_dtype=torch.float32, **x)
+    assert qa.sage2_check_device_error() == 0
+    t = rise * math.log(2.0)
+    e = t * (128 * 2.0 ** -23 + 4 * 2.0 ** -24) + 2.0 ** -22
+    assert ((lse.double() - want).abs() <= e + 2.0 ** -22 * (want + 1) + 8192 * 2.0 ** -24).all()
+    # equal weights among equal scores, values alike: o is v but for P's rounding and the sums'
+    rel = math.expm1(2 * e) + 2.0 ** -8 + 4 * 2.0 ** -24 + 8192 * 2.0 ** -24
+    assert ((o.double() / v - 1).abs() <= rel).all(), (o.min().item() / v, o.max().item() / v)
