@@ -381,7 +381,8 @@ sage2_status sage2_cache_compact(const sage2_cache* cache, const int* table, int
  * all.  The kept slots go to idx[b][h][..] in ascending order (-1 behind the
  * last), their number to new_lens[b], and their rows and tallies to the slots 0..
  * of out_table and acc_out, as sage2_cache_compact does (acc_out NULL is not
- * allowed; it may be acc when in place).  sinks + recent <= keep.
+ * allowed; it may be acc when in place).  The tallies behind them, acc_out[b][h][s] for
+ * new_lens[b] <= s < SO, become 0.  sinks + recent <= keep.
  *   idx : DEVICE int32 [B, Hkv, keep].  new_lens : DEVICE int32 [B], not lens.
  */
 sage2_status sage2_cache_evict(const sage2_cache* cache, const int* table, int max_pages,

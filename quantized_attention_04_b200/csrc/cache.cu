@@ -363,6 +363,7 @@ struct MoveArgs {
   int slice_bytes;         // bytes of a row that one block moves
   int piece_blocks;        // blocks that move them; the others move the 4-byte values
   int in_place;
+  int clear;               // acc_out behind the last row becomes 0
 };
 
 constexpr int kMoveThreads = 256;
@@ -481,6 +482,13 @@ __global__ void __launch_bounds__(kMoveThreads, 4) k_cache_move(MoveArgs a) {
       }
     }
   };
+  // Each word block its share.  In place all of them have been read by the last barrier.
+  auto clear_rest = [&]() {
+    if (!words || !a.clear || !acc_out) return;
+    const int step = INPLACE ? kMoveThreads : ((int)gridDim.x - a.piece_blocks) * kMoveThreads;
+    for (long long i = (long long)base + n + (INPLACE ? 0 : chunk0 * kMoveThreads) + tid; i < a.SO; i += step)
+      acc_out[i] = 0.f;
+  };
   int s[NR];
   Pages p;
   Data x0;
@@ -490,6 +498,7 @@ __global__ void __launch_bounds__(kMoveThreads, 4) k_cache_move(MoveArgs a) {
     ask_pages(p, s, i0);
     ask_data(x0, p, i0);
     write(x0, i0);
+    clear_rest();
     return;
   }
   Data x1;
@@ -513,6 +522,7 @@ __global__ void __launch_bounds__(kMoveThreads, 4) k_cache_move(MoveArgs a) {
     __syncthreads();
     write(x1, i0 + rpc);
   }
+  clear_rest();
 }
 
 static cudaError_t launch_move(MoveArgs a, int B, cudaStream_t st) {
@@ -746,6 +756,7 @@ sage2_status sage2_cache_evict(const sage2_cache* cache, const int* table, int m
   a.ih = keep;
   a.n = new_lens;
   a.base = nullptr;
+  a.clear = 1;             // a token that takes one of these slots starts from 0
   SelectArgs sel{acc, a.ab, a.ah, lens, idx, new_lens, a.c.Hkv, S, keep, sinks, recent};
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = launch_select(sel, B, st);
