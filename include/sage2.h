@@ -347,7 +347,9 @@ sage2_status sage2_attn_tree(const void* q, int dtype, const int64_t* q_strides,
  * add nothing).
  *   acc : f32, slots contiguous, acc_strides {batch, head} in elements (no two heads
  *         the same), S slots a head (a slot >= S is left out and sets the device error
- *         word).
+ *         word).  A drafted token's slot is added to as well: its tally is to be 0
+ *         when the token is written there (sage2_cache_evict leaves zeros behind the
+ *         kept tokens, sage2_cache_compact what was there).
  */
 sage2_status sage2_cache_weights(const void* q, int dtype, const int64_t* q_strides,
                                  const float* lse, const sage2_cache* cache, const int* table,
@@ -365,7 +367,8 @@ sage2_status sage2_cache_weights(const void* q, int dtype, const int64_t* q_stri
  * front, idx[i] >= base + i, in any order and with repeats; a row that would move
  * back is left out and sets the device error word.  acc_out may be acc then.
  * Otherwise the pages of out_table must not be among those of table, nor acc_out
- * overlap acc.  No row of the result may be named twice.
+ * overlap acc.  No row of the result may be named twice.  Slots and tallies behind the
+ * last row written stay as they are.
  */
 sage2_status sage2_cache_compact(const sage2_cache* cache, const int* table, int max_pages,
                                  const int* out_table, int out_max_pages, const int* idx,

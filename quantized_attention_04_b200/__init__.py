@@ -561,7 +561,8 @@ def sage2_cache_weights(q: torch.Tensor, lse: torch.Tensor, cache: dict, table: 
                         n: torch.Tensor | None = None, sm_scale: float | None = None) -> torch.Tensor:
     """Adds to acc [B, Hkv, slots] (float32) the attention weight that each cached
     token received from q, over all its heads and drafted tokens; the arguments
-    are those of sage2_attn_tree and the lse it returned."""
+    are those of sage2_attn_tree and the lse it returned.  The tally of a drafted
+    token's slot is to be 0 when the token is appended."""
     cs, dev = _cache_of(cache)
     sq = _bhtd(q, dev, cs.d, "q")
     B, Hq, T, d = q.shape
@@ -593,7 +594,8 @@ def sage2_cache_compact(cache: dict, table: torch.Tensor, idx: torch.Tensor,
     i < n[b] (None: all of idx [B, Hkv, M]; base None: 0).  out_table None: in
     place, rows moving towards the front only.  For an accepted path of a tree:
     idx = lens + path, base = lens, the same for every head (an expanded idx).  With
-    acc [B, Hkv, slots] its values move along, to acc_out (None: in place)."""
+    acc [B, Hkv, slots] its values move along, to acc_out (None: in place); those behind
+    the last one moved stay as they are."""
     cs, dev = _cache_of(cache)
     if idx.dim() != 3 or idx.dtype != torch.int32 or idx.get_device() != dev or idx.shape[1] != cs.Hkv \
             or (idx.shape[2] > 1 and idx.stride(2) != 1):
@@ -623,7 +625,8 @@ def sage2_cache_evict(cache: dict, table: torch.Tensor, lens: torch.Tensor, acc:
     """Cuts each sequence to at most `keep` tokens a head: the first `sinks`, the last
     `recent` and those of the largest acc [B, Hkv, slots] between them.  The kept
     rows move to the slots 0.. of out_table (None: in place), their tallies to
-    acc_out (None: a new tensor [B, Hkv, keep]).  Returns (idx int32 [B, Hkv, keep]:
+    acc_out, which becomes 0 behind them (None: a new tensor [B, Hkv, keep]; to go on
+    counting give one of all slots, in place acc itself).  Returns (idx int32 [B, Hkv, keep]:
     the kept slots, ascending, -1 behind the last; lens int32 [B]; acc_out)."""
     cs, dev = _cache_of(cache)
     B = lens.shape[0] if lens.dim() == 1 else -1

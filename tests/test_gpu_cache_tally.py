@@ -49,3 +49,98 @@ def test_eviction_clears_the_tally_behind_the_kept(qa, where, kv, keep):
             at = idx[b, h, :new[b]].cpu().long()
             want[b, h, :len(at)] = acc[b, h, at]
     assert same_bits(out, want)
+
+
+@pytest.mark.parametrize("kv", ["same", "e4m3"])
+def test_rounds_of_drafting_and_eviction(qa, kv):
+    """The loop of a server, as the README gives it, three times over: append, attention, tally, accepted path,
+    and an eviction in each.  The tally of every token is the weight that it has received since it was written (in
+    64 bits on the host), and slots without a token have none."""
+    B, Hkv, G, T, d, page, keep, sinks, recent = 2, 2, 2, 6, 64, 16, 40, 2, 8
+    dt, rng = torch.bfloat16, torch.Generator().manual_seed(9)
+    Hq, sm = Hkv * G, 1.0 / math.sqrt(d)
+    cache = qa.sage2_cache_alloc(2 * 8, Hkv, page, d, torch.float8_e4m3fn if kv == "e4m3" else dt)
+    table = torch.randperm(16, generator=rng).to(torch.int32).view(2, 8).cuda()
+    acc = torch.zeros(B, Hkv, 8 * page, device="cuda")
+    slots = torch.arange(8 * page, device="cuda")
+    lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+
+    def rows(x):                       # what the cache holds of rows x
+        if kv == "same":
+            return x.double()
+        code, scale = R.codes(x)
+        return code.double() * scale.double()[..., None]
+
+    # on the host: by sequence and head, the keys of its tokens in slot order, and their tallies
+    keys = [[torch.zeros(0, d, dtype=torch.float64) for _ in range(Hkv)] for _ in range(B)]
+    tally = [[torch.zeros(0, dtype=torch.float64) for _ in range(Hkv)] for _ in range(B)]
+    err = 0.0                          # bound on what a tally may be off by
+
+    def draft(k, v, q, mask):
+        nonlocal err
+        qa.sage2_cache_append(k.cuda(), v.cuda(), cache, table, lens)
+        o, lse = qa.sage2_attn_tree(q.cuda(), cache, table, lens, mask=mask.cuda())
+        qa.sage2_cache_weights(q.cuda(), lse, cache, table, lens, acc, mask=mask.cuda())
+        lse, t, most = lse.double().cpu(), k.shape[2], 0.0
+        for b in range(B):
+            for h in range(Hkv):
+                K = keys[b][h] = torch.cat([keys[b][h], rows(k[b, h])])
+                ln = len(K) - t
+                add = torch.zeros(len(K), dtype=torch.float64)
+                for g in range(G):
+                    s = q[b, h * G + g].double() @ K.T * sm
+                    s[:, ln:][~mask[b]] = -math.inf
+                    add += torch.exp(s - lse[b, h * G + g, :, None]).sum(0)
+                tally[b][h] = torch.cat([tally[b][h], torch.zeros(t, dtype=torch.float64)]) + add
+                x = q[b].double().norm(dim=-1).max().item() * K.norm(dim=-1).max().item() * sm
+                e = x * (d * 2.0 ** -23 + 4 * 2.0 ** -24) + 2.0 ** -22 * (lse.abs().max().item() + 2)
+                most = max(most, (add * (math.expm1(e) + (G * t + 4) * 2.0 ** -24)).max().item()
+                           + 2.0 ** -24 * tally[b][h].max().item())
+        err += most
+
+    def compare():
+        assert qa.sage2_check_device_error() == 0
+        got, ln = acc.double().cpu(), lens.tolist()
+        for b in range(B):
+            for h in range(Hkv):
+                assert ln[b] == len(keys[b][h])
+                assert ((got[b, h, :ln[b]] - tally[b][h]).abs() <= err).all()
+            assert (got[b, :, ln[b]:] == 0).all()
+
+    new = lambda *s: torch.randn(*s, d, generator=rng).to(dt)
+    P = 50                             # the prompt: its queries too, as one chain
+    draft(new(B, Hkv, P), new(B, Hkv, P), 2 * new(B, Hq, P), torch.ones(B, P, P).tril().bool())
+    lens += P
+    compare()
+    for step in range(3):
+        mask = torch.eye(T).bool().expand(B, T, T).clone()
+        for b in range(B):
+            for i in range(1, T):
+                mask[b, i] |= mask[b, int(torch.randint(0, i, (1,), generator=rng))]
+        draft(new(B, Hkv, T), new(B, Hkv, T), 2 * new(B, Hq, T), mask)
+        # the accepted path: the ancestors of a node
+        took = [int(torch.nonzero(mask[b, T - 1 - b]).numel()) for b in range(B)]
+        path = torch.zeros(B, T, dtype=torch.int32)
+        for b in range(B):
+            path[b, :took[b]] = torch.nonzero(mask[b, T - 1 - b])[:, 0].to(torch.int32)
+        path_slots = (lens[:, None] + path.cuda())[:, None].expand(B, Hkv, T)
+        n = torch.tensor(took, dtype=torch.int32, device="cuda")
+        qa.sage2_cache_compact(cache, table, path_slots, n=n, base=lens, acc=acc)
+        lens = lens + n
+        acc.masked_fill_(slots >= lens[:, None, None], 0)
+        for b in range(B):
+            for h in range(Hkv):
+                ln = len(keys[b][h]) - T
+                at = torch.cat([torch.arange(ln), ln + path[b, :took[b]].long()])
+                keys[b][h], tally[b][h] = keys[b][h][at], tally[b][h][at]
+        compare()
+        before = acc.cpu()
+        old = lens.tolist()
+        idx, lens, acc = qa.sage2_cache_evict(cache, table, lens, acc, keep, sinks, recent, acc_out=acc)
+        assert lens.tolist() == [min(keep, x) for x in old]
+        for b in range(B):
+            for h in range(Hkv):
+                at = torch.tensor(R.choose(before[b, h], old[b], keep, sinks, recent))
+                assert torch.equal(idx[b, h, :len(at)].cpu().long(), at)
+                keys[b][h], tally[b][h] = keys[b][h][at], tally[b][h][at]
+        compare()
