@@ -239,7 +239,9 @@ __global__ void __launch_bounds__(kWThreads, 1)
         };
         const int page0 = page_of(k0);
         int page = page_of(k0 + 2);
-        // ---- the unit's rows: two threads a row.  Rows that do not count become zeros with z = +inf.
+        // ---- the unit's rows: two threads a row.  Rows that do not count become zeros with z = +inf; a row
+        // whose lse is NaN gives NaN whatever its Q, which becomes zeros too (an infinity there is not
+        // to set the scale of the others).
         const int rl = tid >> 1, half = tid & 1, r = u * rows_unit + rl;
         const int i = r % a.T;
         float z = INFINITY;
@@ -256,7 +258,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) w[c] = there ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
         float ks = scale_of(k0, page0);
-        if (z == INFINITY) {
+        if (!(z < INFINITY)) {
 #pragma unroll
           for (int c = 0; c < D / 16; ++c) w[c] = make_uint4(0u, 0u, 0u, 0u);
         }
@@ -401,7 +403,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
 #pragma unroll
               for (int y = 0; y < 16; ++y) {
                 const float zz = sm.z[c + y], e = ex2(fmaf(__uint_as_float(x[y]), c1, zz));
-                if (((in >> y) & 1u) && zz > -INFINITY) sum.x += e;
+                if (((in >> y) & 1u) && zz != -INFINITY) sum.x += e;
               }
             }
           }

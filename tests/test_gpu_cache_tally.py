@@ -144,3 +144,30 @@ def test_rounds_of_drafting_and_eviction(qa, kv):
                 assert torch.equal(idx[b, h, :len(at)].cpu().long(), at)
                 keys[b][h], tally[b][h] = keys[b][h][at], tally[b][h][at]
         compare()
+
+
+@pytest.mark.parametrize("kv", ["same", "e4m3"])
+@pytest.mark.parametrize("T, G, d, dtype", [(1, 1, 128, "bf16"), (9, 4, 64, "fp16"), (40, 8, 128, "bf16")])
+@pytest.mark.parametrize("query", [False, True])
+def test_rows_whose_lse_is_not_a_number(qa, T, G, d, dtype, kv, query):
+    """Such a row (an attended key or its own query was not finite) reaches the tallies of the slots that it
+    attends, all of them, and no others; with an infinity in its query too."""
+    c = R.Case(42, [300, 20], T, 2, G, d, 16, dtype, kv)
+    _, lse, _ = R.attend(c)
+    lse = lse.float()
+    i = min(2, T - 1)
+    lse[0, G, i] = math.nan                                  # a row of sequence 0, head 1
+    want = R.weights(c, lse)                                 # of finite q: NaN where the row attends
+    if query:
+        c.q[0, G, i, 5] = math.inf
+    x = c.cuda()
+    acc = torch.zeros(2, 2, c.MP * 16, device="cuda")
+    qa.sage2_cache_weights(x["q"], lse.cuda(), x["cache"], x["table"], x["lens"], acc, mask=x["mask"], n=x["n"])
+    assert qa.sage2_check_device_error() == 0
+    got = acc.double().cpu()
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    c.q[0, G, i, 5] = 0
+    fine = torch.isfinite(lse)
+    e = logit_error(c) + 2.0 ** -22 * (lse[fine].abs().max().item() + 1)
+    some = ~torch.isnan(want)
+    assert ((got - want).abs() <= want * (math.expm1(e) + (G * T + 8) * 2.0 ** -24))[some].all()
