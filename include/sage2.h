@@ -345,8 +345,8 @@ sage2_status sage2_attn_tree(const void* q, int dtype, const int64_t* q_strides,
  *                   attend slot s of exp(sm_scale * q[b][hq][i] . K_s - lse[b][hq][i])
  * with the arguments of sage2_attn_tree and the lse it wrote (rows with lse = -inf
  * add nothing).
- *   acc : f32, slots contiguous, acc_strides {batch, head} in elements (no two heads
- *         the same), S slots a head (a slot >= S is left out and sets the device error
+ *   acc : f32, slots contiguous, acc_strides {batch, head} in elements (the S slots of
+ *         each head its own), S slots a head (a slot >= S is left out and sets the device error
  *         word).  A drafted token's slot is added to as well: its tally is to be 0
  *         when the token is written there (sage2_cache_evict leaves zeros behind the
  *         kept tokens, sage2_cache_compact what was there).
@@ -365,7 +365,8 @@ sage2_status sage2_cache_weights(const void* q, int dtype, const int64_t* q_stri
  *   n, base : DEVICE int32 [B]; NULL: M and 0.
  * out_table NULL or equal to table: in place.  Rows then only move towards the
  * front, idx[i] >= base + i, in any order and with repeats; a row that would move
- * back is left out and sets the device error word.  acc_out may be acc then.
+ * back is left out and sets the device error word.  acc_out may be acc then, with
+ * the same strides.  The SO slots of each head of acc_out are its own.
  * Otherwise the pages of out_table must not be among those of table, nor acc_out
  * overlap acc.  No row of the result may be named twice.  Slots and tallies behind the
  * last row written stay as they are.

@@ -598,6 +598,17 @@ static sage2_status check_table(const CacheView& c, int B, int MP) {
   return SAGE2_OK;
 }
 
+// Does every head of a tally that is written ({batch, head} strides, S slots a head) have slots of its own?
+// Nested either way: what several blocks write at once may not be shared.
+static bool heads_apart(const int64_t* st, int B, int H, int S) {
+  if (st[0] < 0 || st[1] < 0) return false;
+  const __int128 b = st[0], h = st[1];
+  if (B == 1 && H == 1) return true;
+  if (B == 1) return h >= S;
+  if (H == 1) return b >= S;
+  return h <= b ? h >= S && b >= h * (H - 1) + S : b >= S && h >= b * (B - 1) + S;
+}
+
 // Strides of a [B, H, T, d] tensor (elements; null: contiguous): rows must
 // start on 16-byte boundaries.
 static sage2_status take_strides(const int64_t* s, int64_t H, int64_t T, int64_t d, long long* out) {
@@ -689,10 +700,12 @@ static sage2_status move_args(const sage2_cache* cache, const int* table, int ma
     s = check_words(acc, acc_out);
     if (s != SAGE2_OK) return s;
     if (S <= 0 || SO <= 0 || !acc_strides || !acc_out_strides) return SAGE2_ERR_INVALID_ARG;
-    if (acc_strides[0] < 0 || acc_strides[1] < 0 || acc_out_strides[0] < 0 || acc_out_strides[1] < 0)
+    if (acc_strides[0] < 0 || acc_strides[1] < 0 || !heads_apart(acc_out_strides, B, a->c.Hkv, SO))
       return SAGE2_ERR_INVALID_ARG;
-    // a tally that heads share would be written by several at once
-    if ((B > 1 && acc_out_strides[0] == 0) || (a->c.Hkv > 1 && acc_out_strides[1] == 0))
+    // onto itself: in place, and laid out alike
+    if (acc == acc_out &&
+        (out_table != table || (B > 1 && acc_strides[0] != acc_out_strides[0]) ||
+         (a->c.Hkv > 1 && acc_strides[1] != acc_out_strides[1])))
       return SAGE2_ERR_INVALID_ARG;
     a->ab = acc_strides[0];
     a->ah = acc_strides[1];

@@ -1108,9 +1108,7 @@ sage2_status sage2_cache_weights(const void* q, int dtype, const int64_t* q_stri
   if (s != SAGE2_OK) return s;
   s = check_words(lse, acc);
   if (s != SAGE2_OK) return s;
-  if (S <= 0 || !acc_strides || acc_strides[0] < 0 || acc_strides[1] < 0) return SAGE2_ERR_INVALID_ARG;
-  // a tally that heads share would be written by several at once
-  if ((B > 1 && acc_strides[0] == 0) || (a.c.Hkv > 1 && acc_strides[1] == 0)) return SAGE2_ERR_INVALID_ARG;
+  if (S <= 0 || !acc_strides || !heads_apart(acc_strides, B, a.c.Hkv, S)) return SAGE2_ERR_INVALID_ARG;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return SAGE2_ERR_CUDA;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

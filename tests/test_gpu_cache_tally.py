@@ -171,3 +171,23 @@ def test_rows_whose_lse_is_not_a_number(qa, T, G, d, dtype, kv, query):
     e = logit_error(c) + 2.0 ** -22 * (lse[fine].abs().max().item() + 1)
     some = ~torch.isnan(want)
     assert ((got - want).abs() <= want * (math.expm1(e) + (G * T + 8) * 2.0 ** -24))[some].all()
+
+
+def test_tallies_in_other_layouts(qa):
+    """Heads before sequences, slots of a wider buffer, a sequence's tally apart: as the contiguous one."""
+    c = R.Case(43, [150, 99, 20], 4, 2, 2, 64, 16, "bf16", "same", junk=False)
+    x = c.cuda()
+    _, lse = qa.sage2_attn_tree(**x)
+    S = c.MP * 16
+    got = []
+    for make in (lambda: torch.zeros(3, 2, S, device="cuda"), lambda: torch.zeros(2, 3, S, device="cuda").transpose(0, 1),
+                 lambda: torch.zeros(3, 2, 2 * S, device="cuda")[:, :, S:], lambda: torch.zeros(2, 5, S, device="cuda")[:, 1:4].transpose(0, 1)):
+        acc, y = make(), c.cuda()
+        qa.sage2_cache_weights(x["q"], lse, x["cache"], x["table"], x["lens"], acc, mask=x["mask"])
+        one = acc.clone()
+        idx, new, out = qa.sage2_cache_evict(y["cache"], y["table"], y["lens"], acc, 64, 2, 8, acc_out=acc)
+        got.append((one, idx, new, out))
+    assert qa.sage2_check_device_error() == 0
+    for other in got[1:]:
+        for a, b in zip(got[0], other):
+            assert same_bits(a, b)
