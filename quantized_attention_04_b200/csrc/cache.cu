@@ -764,6 +764,7 @@ sage2_status sage2_cache_evict(const sage2_cache* cache, const int* table, int m
   if (SO < keep) return SAGE2_ERR_INVALID_ARG;
   s = check_words(lens, idx, new_lens);
   if (s != SAGE2_OK) return s;
+  if (new_lens == lens) return SAGE2_ERR_INVALID_ARG;   // other blocks still read them
   a.idx = idx;
   a.ib = (long long)a.c.Hkv * keep;
   a.ih = keep;

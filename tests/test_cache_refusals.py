@@ -5,6 +5,10 @@ import pytest
 from tests.test_cache_abi import P, append, cache, compact, evict, qa, strides, tree, weights  # noqa: F401
 
 
+def test_lengths_are_not_written_over(qa):
+    assert evict(qa, new=P, lens=P) == 1
+
+
 @pytest.mark.parametrize("st", [(128, 63), (127, 64), (64, 64), (64, 128 - 1), (63, 128), (0, 64), (128, 0), (2 ** 62, 1),
                                 (1, 2 ** 62)])
 def test_tallies_that_overlap(qa, st):
