@@ -363,6 +363,8 @@ sage2_status sage2_cache_weights(const void* q, int dtype, const int64_t* q_stri
  * acc[b][h][idx[b][h][i]], i < n[b].
  *   idx  : DEVICE int32 [B, Hkv, M], idx_strides {batch, head} (0 allowed).
  *   n, base : DEVICE int32 [B]; NULL: M and 0.
+ *   acc, acc_out : S and SO slots a head, strides as in sage2_cache_weights.  A slot
+ *          >= S counts 0, one >= SO is left out, and both set the device error word.
  * out_table NULL or equal to table: in place.  Rows then only move towards the
  * front, idx[i] >= base + i, in any order and with repeats; a row that would move
  * back is left out and sets the device error word.  acc_out may be acc then, with

@@ -459,7 +459,11 @@ __global__ void __launch_bounds__(kMoveThreads, 4) k_cache_move(MoveArgs a) {
           x.v[u][0].x = __float_as_uint(a.c.ks[src]);
           x.v[u][0].y = __float_as_uint(a.c.vs[src]);
         }
-        if (acc) x.v[u][0].z = p.slot[u] < a.S ? __float_as_uint(acc[p.slot[u]]) : 0u;
+        if (acc) {
+          const bool in = p.slot[u] < a.S;
+          x.v[u][0].z = in ? __float_as_uint(acc[p.slot[u]]) : 0u;
+          if (!in || to >= a.SO) atomicOr(&g_device_error, DEVERR_BOUNDS);
+        }
       }
     }
   };

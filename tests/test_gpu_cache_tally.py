@@ -191,3 +191,27 @@ def test_tallies_in_other_layouts(qa):
     for other in got[1:]:
         for a, b in zip(got[0], other):
             assert same_bits(a, b)
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+def test_moves_outside_of_the_tally(qa, in_place):
+    """A row whose tally, taken or written, has no place in acc or acc_out sets the error word; the rows move and the
+    other tallies with them."""
+    c = R.Case(44, [200], 1, 2, 1, 64, 16, "bf16", "e4m3", spare=13, junk=False)
+    other = sorted(set(range(c.pages)) - set(c.table.flatten().tolist()))
+    table = None if in_place else torch.tensor(other, dtype=torch.int32)[None].cuda()
+    idx = torch.arange(40, 60, dtype=torch.int32).expand(1, 2, 20)
+    for S, SO in ((50, 100), (100, 7), (100, 100)):
+        x = c.cuda()
+        acc = torch.rand(1, 2, S, device="cuda")
+        out = torch.full((1, 2, SO), 3.0, device="cuda")
+        qa.sage2_cache_compact(x["cache"], x["table"], idx.cuda(), out_table=table, acc=acc, acc_out=out)
+        assert qa.sage2_check_device_error() == (0 if S == SO else 8)
+        n = min(S - 40, SO, 20)
+        assert torch.equal(out[:, :, :n], acc[:, :, 40:40 + n])
+        assert (out[:, :, 20:] == 3).all()
+        to = c.table[0] if in_place else table[0].cpu()
+        for i in range(20):
+            p, r, q, t = int(c.table[0, (40 + i) // 16]), (40 + i) % 16, int(to[i // 16]), i % 16
+            assert same_bits(x["cache"]["k"].view(torch.uint8)[q, :, t], c.pool["k"].view(torch.uint8)[p, :, r])
+            assert same_bits(x["cache"]["v_scale"][q, :, t], c.pool["v_scale"][p, :, r])
