@@ -166,11 +166,13 @@ def sage2_layout_info() -> dict:
 
 
 def sage2_check_device_error(device=None) -> int:
-    """Synchronize torch's current stream and return (and clear) the device
-    error status (0 = OK, 6 = a bounded wait timed out)."""
+    """Synchronize torch's current stream of `device` (None: the current one) and
+    return (and clear) that device's error status (0 = OK, 6 = a bounded wait timed
+    out, 8 = a length, page or slot of a cache out of range)."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     st = ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
-    return int(lib().sage2_check_device_error(st))
+    with torch.cuda.device(dev):           # the error word is one of the current device
+        return int(lib().sage2_check_device_error(st))
 
 
 def _qk_bits_of(t: torch.Tensor) -> int:

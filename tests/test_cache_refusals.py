@@ -25,3 +25,36 @@ def test_tallies_moved_onto_themselves(qa):
     assert compact(qa, aost=strides(128, 64), ot=2 * P, om=4, **a) == 1
     assert evict(qa, aost=strides(64, 128), new=2 * P) == 1
     assert evict(qa, ot=2 * P, om=4, new=2 * P) == 1
+
+
+def test_error_word_of_the_device_asked_for(qa, monkeypatch):
+    """The error word is the current device's in the library: the binding makes the device that is asked for
+    current around the call, as the cache entries do for the device of their tensors."""
+    import torch
+    now, seen = [0], []
+
+    class Device:
+        def __init__(self, dev):
+            self.dev = torch.device(dev).index
+
+        def __enter__(self):
+            self.old, now[0] = now[0], self.dev
+
+        def __exit__(self, *a):
+            now[0] = self.old
+
+    class Lib:
+        def sage2_check_device_error(self, st):
+            seen.append((now[0], st.value))
+            return 8
+
+    class Stream:
+        def __init__(self, dev):
+            self.cuda_stream = 100 + torch.device(dev).index
+
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: now[0])
+    monkeypatch.setattr(torch.cuda, "current_stream", Stream)
+    monkeypatch.setattr(qa, "lib", Lib)
+    assert qa.sage2_check_device_error("cuda:1") == 8 and qa.sage2_check_device_error() == 8
+    assert seen == [(1, 101), (0, 100)] and now == [0]
