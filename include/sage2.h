@@ -303,6 +303,7 @@ typedef struct {
  * Writes new tokens to the cache: slot lens[b] + t of each head takes k[b][h][t]
  * and v[b][h][t], t < n[b].  `lens` is not changed.
  *   k, v : [B, Hkv, T, d] in dtype (SAGE2_F16 or SAGE2_BF16; a 16-bit cache has the same).
+ *          T is at most the table's slots, or with n (a padded batch) any number.
  * SAGE2_E4M3: scale = amax/448, code = RNE e4m3 of fp32(x * (448/amax)), each
  * fp32 operation rounded once.  A row with amax below 2^-100 is stored as zeros
  * (scale 0), a row with an infinity or NaN gets scale NaN.
@@ -362,7 +363,8 @@ sage2_status sage2_cache_weights(const void* q, int dtype, const int64_t* q_stri
  * K, V, their scales and (if acc is given) the tally: acc_out[b][h][base[b] + i] =
  * acc[b][h][idx[b][h][i]], i < n[b].
  *   idx  : DEVICE int32 [B, Hkv, M], idx_strides {batch, head} (0 allowed).
- *   n, base : DEVICE int32 [B]; NULL: M and 0.
+ *   n, base : DEVICE int32 [B]; NULL: M and 0.  M is at most the slots of out_table, or
+ *          with n any number.
  *   acc, acc_out : S and SO slots a head, strides as in sage2_cache_weights.  A slot
  *          >= S counts 0, one >= SO is left out, and both set the device error word.
  * out_table NULL or equal to table: in place.  Rows then only move towards the
@@ -388,7 +390,8 @@ sage2_status sage2_cache_compact(const sage2_cache* cache, const int* table, int
  * last), their number to new_lens[b], and their rows and tallies to the slots 0..
  * of out_table and acc_out, as sage2_cache_compact does (acc_out NULL is not
  * allowed; it may be acc when in place).  The tallies behind them, acc_out[b][h][s] for
- * new_lens[b] <= s < SO, become 0.  sinks + recent <= keep.
+ * new_lens[b] <= s < SO, become 0.  sinks + recent <= keep,
+ * and keep is at most the slots of out_table and SO.
  *   idx : DEVICE int32 [B, Hkv, keep].  new_lens : DEVICE int32 [B], not lens.
  */
 sage2_status sage2_cache_evict(const sage2_cache* cache, const int* table, int max_pages,

@@ -649,7 +649,7 @@ sage2_status sage2_cache_append(const void* k, const void* v, int dtype, const i
   const bool e4m3 = a.c.kv_dtype == SAGE2_E4M3;
   if (!e4m3 && dtype != a.c.kv_dtype) return SAGE2_ERR_INVALID_ARG;
   if (T <= 0) return SAGE2_ERR_INVALID_ARG;
-  if (T > (max_pages << a.c.page_shift)) return SAGE2_ERR_INVALID_ARG;
+  if (!n && T > (max_pages << a.c.page_shift)) return SAGE2_ERR_INVALID_ARG;   // n: a padded batch
   if ((int64_t)B * a.c.Hkv > INT32_MAX) return SAGE2_ERR_UNSUPPORTED;
   s = check_ptrs(k, v);
   if (s != SAGE2_OK) return s;
@@ -678,11 +678,12 @@ sage2_status sage2_cache_append(const void* k, const void* v, int dtype, const i
                                       : append_pick<__nv_bfloat16>(a, a.c.d, e4m3, st));
 }
 
-// One move of rows, the arguments checked but for idx.
+// One move of rows, the arguments checked but for idx.  padded: of the M indices a count on the device is in use.
 static sage2_status move_args(const sage2_cache* cache, const int* table, int max_pages,
                               const int* out_table, int out_max_pages, const float* acc,
                               const int64_t* acc_strides, int S, float* acc_out,
-                              const int64_t* acc_out_strides, int SO, int B, int M, MoveArgs* a) {
+                              const int64_t* acc_out_strides, int SO, int B, int M, bool padded,
+                              MoveArgs* a) {
   sage2_status s = check_cache(cache, &a->c);
   if (s != SAGE2_OK) return s;
   s = check_table(a->c, B, max_pages);
@@ -696,7 +697,7 @@ static sage2_status move_args(const sage2_cache* cache, const int* table, int ma
   }
   s = check_table(a->c, B, out_max_pages);
   if (s != SAGE2_OK) return s;
-  if (M > (out_max_pages << a->c.page_shift)) return SAGE2_ERR_INVALID_ARG;
+  if (!padded && M > (out_max_pages << a->c.page_shift)) return SAGE2_ERR_INVALID_ARG;
   s = check_words(out_table);
   if (s != SAGE2_OK) return s;
   if ((acc == nullptr) != (acc_out == nullptr)) return SAGE2_ERR_INVALID_ARG;
@@ -738,7 +739,7 @@ sage2_status sage2_cache_compact(const sage2_cache* cache, const int* table, int
                                  sage2_stream_t stream) {
   MoveArgs a{};
   sage2_status s = move_args(cache, table, max_pages, out_table, out_max_pages, acc, acc_strides, S,
-                             acc_out, acc_out_strides, SO, B, M, &a);
+                             acc_out, acc_out_strides, SO, B, M, n != nullptr, &a);
   if (s != SAGE2_OK) return s;
   if (M == 0) return SAGE2_OK;
   s = check_words(idx);
@@ -763,7 +764,7 @@ sage2_status sage2_cache_evict(const sage2_cache* cache, const int* table, int m
     return SAGE2_ERR_INVALID_ARG;
   MoveArgs a{};
   sage2_status s = move_args(cache, table, max_pages, out_table, out_max_pages, acc, acc_strides, S,
-                             acc_out, acc_out_strides, SO, B, keep, &a);
+                             acc_out, acc_out_strides, SO, B, keep, false, &a);
   if (s != SAGE2_OK) return s;
   if (SO < keep) return SAGE2_ERR_INVALID_ARG;
   s = check_words(lens, idx, new_lens);
