@@ -1,8 +1,9 @@
 """Attention over a paged cache where its values are far apart: value rows of very different sizes, scores that
 climb late, sums of many keys.  Against 64-bit definitions; tolerances as derived in tests/test_gpu_cache.py,
-but for P's absolute rounding with an e4m3 cache.  P times a key's value scale is packed to fp16 relative to the
+but for P's absolute rounding to fp16.  With an e4m3 cache P times a key's value scale is packed relative to the
 largest such product among the keys that the row attends (at most: a reference that lags is below it), so that
-each key is off by 2^-25 of that largest product, times its code of 448 at most.
+each key is off by 2^-25 of that largest product, times its code of 448 at most.  With a 16-bit one P is packed
+relative to the largest weight at most: a key of less than 2^-14 of it is off by 2^-25 of it, times its value.
 """
 import math
 
@@ -27,7 +28,7 @@ def qa():
 
 
 def attend(c):
-    """(o, lse, mag, top): outputs in 64 bits, sum_s w_s |V_s| and the largest w_s * (value scale of s)."""
+    """(o, lse, mag, top): outputs in 64 bits, sum_s w_s |V_s|, and the values that P's rounding by 2^-25 meets."""
     B, Hq = c.B, c.Hkv * c.G
     o = torch.zeros(B, Hq, c.T, c.d, dtype=torch.float64)
     lse, mag = torch.full((B, Hq, c.T), -math.inf, dtype=torch.float64), torch.zeros_like(o)
@@ -45,7 +46,11 @@ def attend(c):
                 z = torch.logsumexp(s, -1)
                 w = torch.exp(s - z[:, None])
                 o[b, r, :n], mag[b, r, :n], lse[b, r, :n] = w @ V, w @ V.abs(), z
-                top[b, r, :n] = (w * size).amax(-1)
+                if c.kv == "e4m3":
+                    top[b, r, :n] = (w * size).amax(-1) * 448 * (ln + n)
+                else:
+                    most = w.amax(-1, keepdim=True)
+                    top[b, r, :n] = ((w < most * 2.0 ** -13).double() @ V.abs().amax(-1)) * most[:, 0]
     return o, lse, mag, top
 
 
@@ -59,7 +64,7 @@ def check(c, o, lse, want):
     rel = math.expm1(2 * e) + (2.0 ** -8 if bf else 2.0 ** -11) + 4 * 2.0 ** -24 + keys * 2.0 ** -24
     tol = rel * mag + 1e-30
     if not bf:
-        tol = tol + (2.0 ** -25 * keys * 448) * top[..., None]
+        tol = tol + 2.0 ** -25 * top[..., None]
     o, lse = o.double().cpu(), lse.double().cpu()
     assert torch.isfinite(o).all()
     err = (o - wo).abs()
@@ -170,3 +175,58 @@ def test_large_values_of_many_keys(qa, G, rise):
     # equal weights among equal scores, values alike: o is v but for P's rounding and the sums'
     rel = math.expm1(2 * e) + 2.0 ** -8 + 4 * 2.0 ** -24 + 8192 * 2.0 ** -24
     assert ((o.double() / v - 1).abs() <= rel).all(), (o.min().item() / v, o.max().item() / v)
+
+
+def set_rows(c, name, b, h, first, x):
+    """Rows `first`.. of sequence b, head h become x [n, d]."""
+    if c.kv == "e4m3":
+        code, scale = R.codes(x.to(c.dtype))
+    for i in range(len(x)):
+        p, r = cell(c, b, first + i)
+        if c.kv == "e4m3":
+            c.pool[name].view(torch.uint8)[p, h, r] = code[i].view(torch.uint8)
+            c.pool[name + "_scale"][p, h, r] = scale[i]
+        else:
+            c.pool[name][p, h, r] = x[i].to(c.dtype)
+
+
+# (T, G, d, dtype): rows of a head below and above each kernel's limits
+CLIMB = [(1, 1, 128, "bf16"), (1, 8, 64, "fp16"), (3, 5, 128, "fp16"), (6, 8, 64, "bf16"), (30, 2, 128, "bf16"),
+         (25, 4, 64, "fp16"), (50, 4, 128, "fp16"), (50, 4, 64, "bf16"), (64, 5, 128, "bf16")]
+
+
+@pytest.mark.parametrize("profile", ["climb", "steps", "values"])
+@pytest.mark.parametrize("kv", ["same", "e4m3"])
+@pytest.mark.parametrize("T, G, d, dtype", CLIMB)
+def test_scores_that_climb(qa, T, G, d, dtype, kv, profile):
+    """References that move in the middle of a run, by more than 2^14, sums and O with them.  climb: over each 300
+    keys the scores rise by 60; steps: 100 keys, then 20 whose score is 14.5 log2 units higher, with values
+    of 2^13 in the lower ones, so that what was added before a move is as much as what comes after it.  values: the
+    scores alike, the values of 2^-20 in the 100 and 1 in the 20: with an e4m3 cache the reference moves all the same,
+    and the keys before a move hold most of the sum."""
+    lens, Hkv = [2600, 1111], 8
+    c = R.Case(33, lens, T, Hkv, G, d, 32, dtype, kv, junk=False)
+    g = torch.Generator().manual_seed(12)
+    u = torch.randn(Hkv, d, generator=g)
+    u /= u.norm(dim=-1, keepdim=True)
+    # a query's part along u: the score of a key k u + noise is about k
+    size = math.sqrt(1 / c.sm)
+    q = 0.3 * torch.randn(2, Hkv, G, T, d, generator=g) + size * u[:, None, None]
+    c.q = q.view(2, Hkv * G, T, d).to(c.dtype)
+    for b in range(2):
+        n = lens[b] + T
+        s = torch.arange(n)
+        if profile == "climb":
+            score, val = (s % 300) / 300 * 60.0, torch.ones(n)
+        elif profile == "values":
+            score, val = torch.zeros(n), torch.where(s % 120 >= 100, 1.0, 2.0 ** -20)
+        else:
+            high = s % 120 >= 100
+            score, val = torch.where(high, 14.5 * math.log(2.0), 0.0), torch.where(high, 1.0, 2.0 ** 13)
+        for h in range(Hkv):
+            set_rows(c, "k", b, h, 0, size * score[:, None] * u[h] + 0.3 * torch.randn(n, d, generator=g))
+            set_rows(c, "v", b, h, 0, val[:, None] * torch.randn(n, d, generator=g).clamp(-3, 3))
+    x = c.cuda()
+    o, lse = qa.sage2_attn_tree(out_dtype=torch.float32, **x)
+    assert qa.sage2_check_device_error() == 0
+    check(c, o, lse, attend(c))
