@@ -304,8 +304,6 @@ __device__ __forceinline__ float row_lse(float m, float sum) {
 // scores; the value scales multiply P, whose reference is the largest of score + log2(value scale) among the
 // keys that the row attends: a large value row that weighs nothing takes no bits from the others.
 constexpr int kRowsWarps = 4;
-constexpr int MT = 1;                  // m-tiles of 16 rows of a warp; with two the e4m3 form spilled (64 us against
-                                       // 48 to 53 for 20 rows of 8 heads)
 constexpr int kRowsTile = 16 * kRowsWarps;
 constexpr int kRowsLeast = 2;          // tiles that a block takes at least
 
@@ -414,71 +412,68 @@ __global__ void __launch_bounds__(32 * kRowsWarps, (RowsCfg<D, E4M3>::kBlocks))
   for (int s = 0; s < C::kStages; ++s) issue();
   __syncwarp();                               // lane 0's sm.bad
 
-  uint32_t qf[MT][D / 16][4];
-  float acc[MT][NT][4];
-  float m[MT][2], l[MT][2], qs[MT][2];        // m: the reference (log2 units)
+  uint32_t qf[D / 16][4];
+  float acc[NT][4];
+  float m[2], l[2], qs[2];        // m: the reference (log2 units)
   const float kL2E = 1.4426950408889634f;
 
   for (int t = 0; t < nt; ++t) {
     const int L = at.s.len + at.s.n;
-    const int row0 = (at.pair % a.RT) * 16 * MT;
+    const int row0 = (at.pair % a.RT) * 16;
     const int h = at.pair / a.RT;
     if (t == 0 || at.tile == 0) {
       // a piece starts: its rows' Q fragments
+      const uint16_t* src[2];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        const uint16_t* src[2];
+      for (int e = 0; e < 2; ++e) {
+        const int r = row0 + g + 8 * e;
+        src[e] = r < R ? static_cast<const uint16_t*>(a.q) + at.b * a.sb +
+                             (long long)(h * a.G + r / a.T) * a.sh + (long long)(r % a.T) * a.st
+                       : nullptr;
+        m[e] = -INFINITY;
+        l[e] = 0.f;
+        qs[e] = a.sm_scale * kL2E;
+      }
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          // 16 bit: k = 16 ks + 2c (+8).  e4m3: the thread's bytes of a key are
+          // contiguous (D/4 of them), so k-step ks takes d = (D/4) c + 4 ks + {0,1}, {2,3}
+          const int dd = E4M3 ? (D / 4) * c + 4 * ks + 2 * (u >> 1) : 16 * ks + 2 * c + 8 * (u >> 1);
+          qf[ks][u] = src[u & 1] ? __ldg(reinterpret_cast<const uint32_t*>(src[u & 1] + dd)) : 0u;
+        }
+      if (E4M3) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int r = row0 + mt * 16 + g + 8 * e;
-          src[e] = r < R ? static_cast<const uint16_t*>(a.q) + at.b * a.sb +
-                               (long long)(h * a.G + r / a.T) * a.sh + (long long)(r % a.T) * a.st
-                         : nullptr;
-          m[mt][e] = -INFINITY;
-          l[mt][e] = 0.f;
-          qs[mt][e] = a.sm_scale * kL2E;
+          float amax = 0.f;
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+            for (int u = e; u < 4; u += 2) {
+              const float2 f = halves<QBF>(qf[ks][u]);
+              amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+            }
+          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+          // 2^(13 - exponent): an exact power of two; left alone where the row is 0 or not finite
+          const int ex = (int)(__float_as_uint(amax) >> 23);
+          const int sh = (ex == 0 || ex == 255) ? 0 : max(-114, min(60, 13 + 127 - ex));
+          const float up = __uint_as_float((uint32_t)(127 + sh) << 23);
+          qs[e] *= __uint_as_float((uint32_t)(127 - sh) << 23);
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+            for (int u = e; u < 4; u += 2) {
+              const float2 f = halves<QBF>(qf[ks][u]);
+              qf[ks][u] = pack2<false>(f.x * up, f.y * up);
+            }
         }
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            // 16 bit: k = 16 ks + 2c (+8).  e4m3: the thread's bytes of a key are
-            // contiguous (D/4 of them), so k-step ks takes d = (D/4) c + 4 ks + {0,1}, {2,3}
-            const int dd = E4M3 ? (D / 4) * c + 4 * ks + 2 * (u >> 1) : 16 * ks + 2 * c + 8 * (u >> 1);
-            qf[mt][ks][u] = src[u & 1] ? __ldg(reinterpret_cast<const uint32_t*>(src[u & 1] + dd)) : 0u;
-          }
-        if (E4M3) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float amax = 0.f;
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks)
-#pragma unroll
-              for (int u = e; u < 4; u += 2) {
-                const float2 f = halves<QBF>(qf[mt][ks][u]);
-                amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
-              }
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-            // 2^(13 - exponent): an exact power of two; left alone where the row is 0 or not finite
-            const int ex = (int)(__float_as_uint(amax) >> 23);
-            const int sh = (ex == 0 || ex == 255) ? 0 : max(-114, min(60, 13 + 127 - ex));
-            const float up = __uint_as_float((uint32_t)(127 + sh) << 23);
-            qs[mt][e] *= __uint_as_float((uint32_t)(127 - sh) << 23);
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks)
-#pragma unroll
-              for (int u = e; u < 4; u += 2) {
-                const float2 f = halves<QBF>(qf[mt][ks][u]);
-                qf[mt][ks][u] = pack2<false>(f.x * up, f.y * up);
-              }
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int u = 0; u < 4; ++u) acc[mt][j][u] = 0.f;
       }
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) acc[j][u] = 0.f;
     }
 
     const int key0 = at.tile * kRowsTile + warp * 16;
@@ -522,13 +517,11 @@ __global__ void __launch_bounds__(32 * kRowsWarps, (RowsCfg<D, E4M3>::kBlocks))
         __syncwarp();
       }
       // ---- S = Q K^T
-      float s[MT][2][4];
+      float s[2][4];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int u = 0; u < 4; ++u) s[mt][j][u] = 0.f;
+        for (int u = 0; u < 4; ++u) s[j][u] = 0.f;
       if (!E4M3) {
         const uint32_t base = smem_u32(kt);
 #pragma unroll
@@ -536,11 +529,8 @@ __global__ void __launch_bounds__(32 * kRowsWarps, (RowsCfg<D, E4M3>::kBlocks))
           uint32_t b[4];
           const int key = (lane >> 4) * 8 + (lane & 7), ch = 2 * ks + ((lane >> 3) & 1);
           ldsm4(base + rows_off<D, E4M3>(key, ch), b);
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            mma16816<BF>(s[mt][0], qf[mt][ks], b[0], b[1]);
-            mma16816<BF>(s[mt][1], qf[mt][ks], b[2], b[3]);
-          }
+          mma16816<BF>(s[0], qf[ks], b[0], b[1]);
+          mma16816<BF>(s[1], qf[ks], b[2], b[3]);
         }
       } else {
 #pragma unroll
@@ -555,8 +545,7 @@ __global__ void __launch_bounds__(32 * kRowsWarps, (RowsCfg<D, E4M3>::kBlocks))
             for (int y = 0; y < 4; ++y) {
               uint32_t b0, b1;
               widen4(ww[y], b0, b1);
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt) mma16816<BF>(s[mt][j], qf[mt][4 * x + y], b0, b1);
+              mma16816<BF>(s[j], qf[4 * x + y], b0, b1);
             }
           }
       }
@@ -582,79 +571,73 @@ __global__ void __launch_bounds__(32 * kRowsWarps, (RowsCfg<D, E4M3>::kBlocks))
         vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 2));
         lv = __log2f(vm);
       }
-      float x[MT][2][2][2];
+      float x[2][2][2];
       bool over = false;
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+            x[e][j][y] = s[j][2 * e + y] * (E4M3 ? qs[e] * kscl[j][y] : qs[e]);
+        if (edge) {
+          const int r = row0 + g + 8 * e;
+          const int i = r % a.T;
+          const uint8_t* mask = a.mask ? a.mask + at.b * a.mask_sb : nullptr;
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const int k = 8 * j + 2 * c + y;
+              const bool in = slot_allowed(a, mask, at.s, i, key0 + k);
+              if (!(in && k < live && r < R)) x[e][j][y] = -INFINITY;
+              else if ((badrows >> k) & 1u) x[e][j][y] = __int_as_float(0x7fffffff);
+            }
+        }
+        const float mx = fmaxf(fmaxf(x[e][0][0], x[e][0][1]), fmaxf(x[e][1][0], x[e][1][1]));
+        over = over || (mx > -INFINITY && mx + lv > m[e] + kRefGrow);
+      }
+      if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
+          float mx = -INFINITY;
 #pragma unroll
           for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int y = 0; y < 2; ++y)
-              x[mt][e][j][y] = s[mt][j][2 * e + y] * (E4M3 ? qs[mt][e] * kscl[j][y] : qs[mt][e]);
-          if (edge) {
-            const int r = row0 + mt * 16 + g + 8 * e;
-            const int i = r % a.T;
-            const uint8_t* mask = a.mask ? a.mask + at.b * a.mask_sb : nullptr;
+              mx = fmaxf(mx, E4M3 ? x[e][j][y] + vref_log2(vscl[j][y]) : x[e][j][y]);
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          const float now = fmaxf(m[e], mx);
+          const float f = m[e] == -INFINITY ? 0.f : ex2(m[e] - now);
+          m[e] = now;
+          l[e] *= f;
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                const int k = 8 * j + 2 * c + y;
-                const bool in = slot_allowed(a, mask, at.s, i, key0 + k);
-                if (!(in && k < live && r < R)) x[mt][e][j][y] = -INFINITY;
-                else if ((badrows >> k) & 1u) x[mt][e][j][y] = __int_as_float(0x7fffffff);
-              }
+          for (int j = 0; j < NT; ++j) {
+            acc[j][2 * e] *= f;
+            acc[j][2 * e + 1] *= f;
           }
-          const float mx = fmaxf(fmaxf(x[mt][e][0][0], x[mt][e][0][1]), fmaxf(x[mt][e][1][0], x[mt][e][1][1]));
-          over = over || (mx > -INFINITY && mx + lv > m[mt][e] + kRefGrow);
         }
-      if (__any_sync(0xffffffffu, over)) {
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float mx = -INFINITY;
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-              for (int y = 0; y < 2; ++y)
-                mx = fmaxf(mx, E4M3 ? x[mt][e][j][y] + vref_log2(vscl[j][y]) : x[mt][e][j][y]);
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            const float now = fmaxf(m[mt][e], mx);
-            const float f = m[mt][e] == -INFINITY ? 0.f : ex2(m[mt][e] - now);
-            m[mt][e] = now;
-            l[mt][e] *= f;
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-              acc[mt][j][2 * e] *= f;
-              acc[mt][j][2 * e + 1] *= f;
-            }
-          }
       }
-      uint32_t pf[MT][4];
+      uint32_t pf[4];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int e = 0; e < 2; ++e) {
+        const float mb = m[e] == -INFINITY ? 0.f : m[e];
+        float p[2][2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float mb = m[mt][e] == -INFINITY ? 0.f : m[mt][e];
-          float p[2][2];
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) p[j][y] = ex2(x[e][j][y] - mb);
+        l[e] += (p[0][0] + p[0][1]) + (p[1][0] + p[1][1]);
+        if (E4M3) {
 #pragma unroll
           for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int y = 0; y < 2; ++y) p[j][y] = ex2(x[mt][e][j][y] - mb);
-          l[mt][e] += (p[0][0] + p[0][1]) + (p[1][0] + p[1][1]);
-          if (E4M3) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-              for (int y = 0; y < 2; ++y) p[j][y] *= vscl[j][y];
-          }
-          pf[mt][e] = pack2<BF>(p[0][0], p[0][1]);
-          pf[mt][2 + e] = pack2<BF>(p[1][0], p[1][1]);
+            for (int y = 0; y < 2; ++y) p[j][y] *= vscl[j][y];
         }
+        pf[e] = pack2<BF>(p[0][0], p[0][1]);
+        pf[2 + e] = pack2<BF>(p[1][0], p[1][1]);
+      }
       // ---- O += P V
       if (!E4M3) {
         const uint32_t base = smem_u32(vt);
@@ -663,11 +646,8 @@ __global__ void __launch_bounds__(32 * kRowsWarps, (RowsCfg<D, E4M3>::kBlocks))
           uint32_t b[4];
           const int key = ((lane >> 3) & 1) * 8 + (lane & 7), ch = 2 * jj + (lane >> 4);
           ldsm4_t(base + rows_off<D, E4M3>(key, ch), b);
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            mma16816<BF>(acc[mt][2 * jj], pf[mt], b[0], b[1]);
-            mma16816<BF>(acc[mt][2 * jj + 1], pf[mt], b[2], b[3]);
-          }
+          mma16816<BF>(acc[2 * jj], pf, b[0], b[1]);
+          mma16816<BF>(acc[2 * jj + 1], pf, b[2], b[3]);
         }
       } else {
         // keys 2c, 2c+1, 2c+8, 2c+9; column g of n-tile j is d = (D/8) g + j
@@ -693,9 +673,7 @@ __global__ void __launch_bounds__(32 * kRowsWarps, (RowsCfg<D, E4M3>::kBlocks))
             widen4(__byte_perm(w[2][x], w[3][x], sel), b1[0], b1[1]);
 #pragma unroll
             for (int y = 0; y < 2; ++y)
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt)
-                mma16816<BF>(acc[mt][4 * x + 2 * hh + y], pf[mt], b0[y], b1[y]);
+              mma16816<BF>(acc[4 * x + 2 * hh + y], pf, b0[y], b1[y]);
           }
       }
       __syncwarp();
@@ -710,87 +688,83 @@ __global__ void __launch_bounds__(32 * kRowsWarps, (RowsCfg<D, E4M3>::kBlocks))
       const int first = at.tile - min(t, at.tile);   // the piece's first tile of the pair
       const bool whole = first == 0 && at.tile + 1 == at.tiles;
       const int slot = 2 * blockIdx.x + (first == 0 ? 1 : 0);
+      float f[2];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        if (row0 + mt * 16 >= R) break;              // uniform: no such rows
-        float f[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float x = l[mt][e];
-          x += __shfl_xor_sync(0xffffffffu, x, 1);
-          x += __shfl_xor_sync(0xffffffffu, x, 2);
-          if (c == 0) sm.ml[warp][g + 8 * e] = make_float2(m[mt][e], x);
-        }
-        __syncthreads();
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float M = -INFINITY;
-#pragma unroll
-          for (int w = 0; w < kRowsWarps; ++w) M = fmaxf(M, sm.ml[w][g + 8 * e].x);
-          f[e] = ex2(m[mt][e] - (M == -INFINITY ? 0.f : M));
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          if (row0 + mt * 16 + g + 8 * e >= R) continue;
-          float* to = sm.red[warp][g + 8 * e];
-          if (!E4M3) {
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-              *reinterpret_cast<float2*>(to + 8 * j + 2 * c) =
-                  make_float2(acc[mt][j][2 * e] * f[e], acc[mt][j][2 * e + 1] * f[e]);
-          } else {
-            // column y of n-tile j is d = (D/8) (2c + y) + j
-#pragma unroll
-            for (int y = 0; y < 2; ++y)
-#pragma unroll
-              for (int j = 0; j < NT; j += 4)
-                *reinterpret_cast<float4*>(to + NT * (2 * c + y) + j) =
-                    make_float4(acc[mt][j][2 * e + y] * f[e], acc[mt][j + 1][2 * e + y] * f[e],
-                                acc[mt][j + 2][2 * e + y] * f[e], acc[mt][j + 3][2 * e + y] * f[e]);
-          }
-        }
-        __syncthreads();
-        // eight threads a row, every eighth float4
-        const int rr = tid >> 3, r = row0 + mt * 16 + rr;
-        if (r < R) {
-          float M = -INFINITY, sum = 0.f;
-#pragma unroll
-          for (int w = 0; w < kRowsWarps; ++w) M = fmaxf(M, sm.ml[w][rr].x);
-          const float mb = M == -INFINITY ? 0.f : M;
-#pragma unroll
-          for (int w = 0; w < kRowsWarps; ++w) sum += ex2(sm.ml[w][rr].x - mb) * sm.ml[w][rr].y;
-          const int i = r % a.T;
-          const bool none = i >= at.s.n || sum == 0.f;
-          const float inv = none ? 0.f : 1.f / sum;
-          const size_t row = whole ? ((size_t)at.b * a.Hq + h * a.G + r / a.T) * a.T + i
-                                   : (size_t)slot * (16 * MT) + mt * 16 + rr;
-#pragma unroll
-          for (int col = 4 * (tid & 7); col < D; col += 32) {
-            float4 v = *reinterpret_cast<const float4*>(&sm.red[0][rr][col]);
-#pragma unroll
-            for (int w = 1; w < kRowsWarps; ++w) {
-              const float4 y = *reinterpret_cast<const float4*>(&sm.red[w][rr][col]);
-              v.x += y.x;
-              v.y += y.y;
-              v.z += y.z;
-              v.w += y.w;
-            }
-            float o4[4] = {v.x, v.y, v.z, v.w};
-            if (whole) {
-#pragma unroll
-              for (int x = 0; x < 4; ++x) o4[x] = none ? 0.f : o4[x] * inv;
-              store4(a.o, a.o_dtype, row * D + col, o4);
-            } else {
-              store4(a.part, 2, row * D + col, o4);
-            }
-          }
-          if ((tid & 7) == 0) {
-            if (!whole) a.part_ml[row] = make_float2(M, sum);
-            else if (a.lse) a.lse[row] = none ? -INFINITY : row_lse(M, sum);
-          }
-        }
-        __syncthreads();
+      for (int e = 0; e < 2; ++e) {
+        float x = l[e];
+        x += __shfl_xor_sync(0xffffffffu, x, 1);
+        x += __shfl_xor_sync(0xffffffffu, x, 2);
+        if (c == 0) sm.ml[warp][g + 8 * e] = make_float2(m[e], x);
       }
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kRowsWarps; ++w) M = fmaxf(M, sm.ml[w][g + 8 * e].x);
+        f[e] = ex2(m[e] - (M == -INFINITY ? 0.f : M));
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if (row0 + g + 8 * e >= R) continue;
+        float* to = sm.red[warp][g + 8 * e];
+        if (!E4M3) {
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+            *reinterpret_cast<float2*>(to + 8 * j + 2 * c) =
+                make_float2(acc[j][2 * e] * f[e], acc[j][2 * e + 1] * f[e]);
+        } else {
+          // column y of n-tile j is d = (D/8) (2c + y) + j
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+#pragma unroll
+            for (int j = 0; j < NT; j += 4)
+              *reinterpret_cast<float4*>(to + NT * (2 * c + y) + j) =
+                  make_float4(acc[j][2 * e + y] * f[e], acc[j + 1][2 * e + y] * f[e],
+                              acc[j + 2][2 * e + y] * f[e], acc[j + 3][2 * e + y] * f[e]);
+        }
+      }
+      __syncthreads();
+      // eight threads a row, every eighth float4
+      const int rr = tid >> 3, r = row0 + rr;
+      if (r < R) {
+        float M = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kRowsWarps; ++w) M = fmaxf(M, sm.ml[w][rr].x);
+        const float mb = M == -INFINITY ? 0.f : M;
+#pragma unroll
+        for (int w = 0; w < kRowsWarps; ++w) sum += ex2(sm.ml[w][rr].x - mb) * sm.ml[w][rr].y;
+        const int i = r % a.T;
+        const bool none = i >= at.s.n || sum == 0.f;
+        const float inv = none ? 0.f : 1.f / sum;
+        const size_t row = whole ? ((size_t)at.b * a.Hq + h * a.G + r / a.T) * a.T + i
+                                 : (size_t)slot * 16 + rr;
+#pragma unroll
+        for (int col = 4 * (tid & 7); col < D; col += 32) {
+          float4 v = *reinterpret_cast<const float4*>(&sm.red[0][rr][col]);
+#pragma unroll
+          for (int w = 1; w < kRowsWarps; ++w) {
+            const float4 y = *reinterpret_cast<const float4*>(&sm.red[w][rr][col]);
+            v.x += y.x;
+            v.y += y.y;
+            v.z += y.z;
+            v.w += y.w;
+          }
+          float o4[4] = {v.x, v.y, v.z, v.w};
+          if (whole) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) o4[x] = none ? 0.f : o4[x] * inv;
+            store4(a.o, a.o_dtype, row * D + col, o4);
+          } else {
+            store4(a.part, 2, row * D + col, o4);
+          }
+        }
+        if ((tid & 7) == 0) {
+          if (!whole) a.part_ml[row] = make_float2(M, sum);
+          else if (a.lse) a.lse[row] = none ? -INFINITY : row_lse(M, sum);
+        }
+      }
+      __syncthreads();
     }
     if (t + 1 < nt) at.next(a, pairs, kRowsTile);
   }
@@ -972,7 +946,7 @@ static cudaError_t launch_join(const TreeArgs& a, int tile, int rows_tile, int g
 template <int D, bool E4M3, bool QBF>
 static cudaError_t launch_rows(TreeArgs a, int dev, cudaMemPool_t pool, cudaStream_t st) {
   using C = RowsCfg<D, E4M3>;
-  a.RT = (a.G * a.T + 16 * MT - 1) / (16 * MT);
+  a.RT = (a.G * a.T + 15) / 16;
   const int grid = C::kBlocks * sm_count(dev);
   CUtensorMap tk, tv;
   const uint64_t rows = (uint64_t)a.c.pages * a.c.Hkv << a.c.page_shift;
@@ -983,7 +957,7 @@ static cudaError_t launch_rows(TreeArgs a, int dev, cudaMemPool_t pool, cudaStre
   cudaError_t e = make_tmap(&tk, a.c.k, 2, dims, strides, box, eb, C::kBoxBytes);
   if (e == cudaSuccess) e = make_tmap(&tv, a.c.v, 2, dims, strides, box, eb, C::kBoxBytes);
   if (e != cudaSuccess) return e;
-  const size_t prow = (size_t)2 * grid * 16 * MT;
+  const size_t prow = (size_t)2 * grid * 16;
   e = split_workspace(&a, prow, D, pool, st);
   if (e != cudaSuccess) return e;
   auto kern = k_tree_rows<D, E4M3, QBF>;
@@ -994,7 +968,7 @@ static cudaError_t launch_rows(TreeArgs a, int dev, cudaMemPool_t pool, cudaStre
     e = cudaGetLastError();
   }
   if (e == cudaSuccess) {
-    e = launch_join<D>(a, kRowsTile, 16 * MT, grid, kRowsLeast, st);
+    e = launch_join<D>(a, kRowsTile, 16, grid, kRowsLeast, st);
   }
   const cudaError_t e2 = cudaFreeAsync(a.part, st);
   return e != cudaSuccess ? e : e2;

@@ -209,15 +209,6 @@ __device__ __forceinline__ void tmem_st16x128_16(uint32_t taddr, const uint32_t 
         "r"(r[15])
       : "memory");
 }
-__device__ __forceinline__ void tmem_ld16x128_16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x128b.x8.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-}
 
 // Does the V row of slot `slot`, or one of its scales, hold an infinity or NaN?
 template <int D, bool E4M3, bool BF>
