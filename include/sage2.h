@@ -270,7 +270,7 @@ sage2_status sage2_attn_fwd_host(const void* q, const void* k, const void* v, vo
  *              SAGE2_E4M3: one code a value and one fp32 scale a row), contiguous,
  *              16-byte aligned.
  *   k_scale, v_scale : f32 [pages, Hkv, page_size], SAGE2_E4M3 only: the row
- *              stands for code * scale.  16-byte aligned.
+ *              stands for code * scale, scale >= 0 (or not finite).  16-byte aligned.
  *   page_size: 16, 32, 64 or 128.  d: 64 or 128.
  * A sequence's slot s is row s % page_size of page table[b][s / page_size];
  * `table` is a DEVICE int32 array [B, max_pages], `lens` a DEVICE int32 array [B]

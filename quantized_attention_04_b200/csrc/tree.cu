@@ -289,14 +289,17 @@ __device__ __forceinline__ float row_lse(float m, float sum) {
 }
 
 // ------------------------------------------------------------ few rows
-// k_tree_rows: a tile of 16 rows (all the rows of a pair where T*G is small)
-// against the keys.  Bound by the cache's bytes: at up to 32 rows a byte of
-// 16-bit cache meets at most 32 multiply-adds, which the legacy tensor path
-// (no TMEM round trip, P stays in registers) sustains well above the rate at
-// which HBM delivers.  Four warps; warp w owns keys 16w..16w+15 of each 64-key
-// tile, with its own ring of TMA-filled stages, its own running maximum and sum
-// and its own accumulator, so that nothing in the loop waits for another warp;
-// they are added when the piece ends.
+// k_tree_rows: a tile of 16 rows (all the rows of a pair where T*G is small, up to 16
+// with a 16-bit cache and 48, three tiles, with an e4m3 one) against the keys.  The legacy
+// tensor path (no TMEM round trip, P stays in registers): two tiles a warp spilled with
+// e4m3 (64 us against 48 to 53 for 20 rows of 8 heads).  Four warps; warp w owns keys
+// 16w..16w+15 of each 64-key tile, with its own ring of TMA-filled stages, its own
+// running maximum and sum and its own accumulator, so that nothing in the loop waits for
+// another warp; they are added when the piece ends.
+//
+// Bound by issue and latency of each warp's chain (load, products, exponentials), not by the
+// cache's bytes: one token over 32768 e4m3 slots of 8 heads takes 28 us here for 69 MB (2.5
+// TB/s), half of its instructions widen codes, and a warp issues in one of five cycles.
 //
 // e4m3 cache: codes become fp16 in registers (exact).  Q (fp16 or bf16) enters as
 // fp16 scaled by a power of two that puts the row's largest value at 2^13 (what
@@ -777,7 +780,10 @@ __global__ void __launch_bounds__(32 * kRowsWarps, (RowsCfg<D, E4M3>::kBlocks))
 // the 37 pieces of one token's heads).  k_tree_join: a block a row, thread d for channel d; for
 // rows of many pieces.  k_tree_join_few: a warp a row.
 constexpr int kMostBlocks = 1024;       // of a split
-constexpr int kJoinFew = 8;             // blocks a pair from which on a row has a block
+// Blocks a pair from which on a row has a block.  Whole call, block / warp a row, us: bf16, d = 128, 1 row a pair (a grid
+// of 296): 1 pair of 32768 slots 28 / 66, 8 pairs 34 / 39, 32 pairs of 16384 51.5 / 52.8, 48 pairs of 8000 43.3 / 43.1;
+// 200 rows (a grid of 148): 8 pairs 68 / 69, 16 pairs 103 / 100, 64 pairs of 8192 126 / 105.
+constexpr int kJoinFew = 8;
 template <int D>
 __global__ void __launch_bounds__(128) k_tree_join_few(const __grid_constant__ TreeArgs a, int tile,
                                                        int rows_tile, int grid, int least) {
@@ -982,9 +988,15 @@ namespace sage2 {
 template <int D, bool E4M3, bool QBF>
 static cudaError_t tree_pick(const TreeArgs& a, int dev, cudaMemPool_t pool, cudaStream_t st) {
   // A row tile of 16 reads the cache once more, from L2 mostly; k_tree_tiles reads it once and costs the same
-  // for 17 rows as for 128.  Measured, us (1 x 32768 / 8 x 4096 / 32 x 1000 slots, 8 heads, d = 128):
-  //   16 bits  16 rows: tiles of 16 37 / 34 / 33, k_tree_tiles 39 / 37 / 39;  20 rows: 54 / 46 / 50, 40 / 37 / 41
-  //   e4m3     44 rows: tiles of 16 71 / 65 / 76, k_tree_tiles 76 / 80 / 97;  64 rows: k_tree_tiles 78 / 80 / 105
+  // for 17 rows as for 128.  Measured, us (1 x 32768 / 8 x 4096 / 32 x 1000 slots), tiles of 16 | k_tree_tiles:
+  //   16 bits  d = 128   8 heads  16 rows  36 / 37 / 36 | 37 / 39 / 40       20 rows  53 / 51 / 55 | 38 / 40 / 41
+  //                     32 heads  16 rows  95 / 95 / 105 | 96 / 98 / 112     20 rows  167 / 172 / 182 | 96 / 98 / 116
+  //            d = 64    8 heads  16 rows  24 / 24 / 23 | 28 / 31 / 31       20 rows  31 / 32 / 32 | 29 / 32 / 32
+  //   e4m3     d = 128   8 heads  48 rows  70 / 72 / 85 | 77 / 87 / 118      64 rows  85 / 87 / 109 | 79 / 89 / 123
+  //                     32 heads  48 rows  216 / 229 / 281 | 269 / 315 / 415  64 rows  277 / 299 / 380 | 275 / 320 / 425
+  //            d = 64    8 heads  48 rows  50 / 52 / 60 | 69 / 73 / 100      64 rows  62 / 65 / 77 | 69 / 74 / 103
+  // Past the limits tiles of 16 lead still for one head of 16 bits (64 rows over 32768 slots 25 | 36), and with e4m3
+  // up to 64 rows for d = 64 and for many short sequences.
   const int R = a.G * a.T;
   if (R <= (E4M3 ? 48 : 16)) return launch_rows<D, E4M3, QBF>(a, dev, pool, st);
   if (R <= kTR) return launch_tiles<D, E4M3, QBF, false>(a, dev, pool, st);

@@ -10,8 +10,8 @@
 // P (16 bits) written over S in TMEM, O += P V with P as the TMEM operand and V as it is
 // cached ([key][d], the "MN-major" form), O in TMEM for the whole run of a pair.  S is
 // double-buffered: S of the next tile is there when the softmax of this one ends, so
-// that the exponentials (16 a cycle and SM: 2048 cycles for 256 rows x 128 keys) and
-// the tensor cores (as many for both products) run side by side.
+// that the exponentials (16 a cycle and SM: 1024 cycles for 256 rows x 64 keys) and
+// the tensor cores (as many for both products, d = 128) run side by side.
 //
 // The softmax passes over S once: exponentials are taken against the reference
 // left by the earlier keys, and only if some score of the warp's rows lies far above
@@ -834,8 +834,9 @@ __global__ void __launch_bounds__(kTThreads<E4M3>, 1)
           lv = sm.lv[SHARE ? 0 : s][t % C::kScales];
         }
         if (key0 + kTK > at.s.len) {
-          // inlined or not, the rest of the loop is compiled otherwise: 16 x 48 tokens over 32768 slots take 870
-          // (inlined) or 1000 us with an e4m3 cache, 507 or 501 with a bf16 one, 4 x 61 over 8192 bf16 95 or 92
+          // inlined or not, the rest of the loop is compiled otherwise.  Inlined | apart, us, 32 heads over 8: 16 x 48
+          // tokens over 32768 slots, e4m3 861 | 1041 (d = 64: 833 | 816), bf16 573 | 575 (447 | 448); 4 x 61 over 8192,
+          // e4m3 105 | 112 (87 | 89), bf16 73.1 | 72.0 (64.4 | 63.4)
           if (E4M3) mask_scores<4>(a, at.s, at.b, tS, key0, r[0] % a.T, r[1] % a.T);
           else mask_scores_apart(a, at.s, at.b, tS, key0, r[0] % a.T, r[1] % a.T);
         }

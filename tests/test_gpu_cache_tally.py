@@ -53,7 +53,7 @@ def test_eviction_clears_the_tally_behind_the_kept(qa, where, kv, keep):
 
 @pytest.mark.parametrize("kv", ["same", "e4m3"])
 def test_rounds_of_drafting_and_eviction(qa, kv):
-    """The loop of a server, as the README gives it, three times over: append, attention, tally, accepted path,
+    """The loop of a server, three times over: append, attention, tally, accepted path,
     and an eviction in each.  The tally of every token is the weight that it has received since it was written (in
     64 bits on the host), and slots without a token have none."""
     B, Hkv, G, T, d, page, keep, sinks, recent = 2, 2, 2, 6, 64, 16, 40, 2, 8
