@@ -345,7 +345,9 @@ sage2_status sage2_attn_tree(const void* q, int dtype, const int64_t* q_strides,
  *   acc[b][h][s] += sum over the query heads hq of h and the tokens i < n[b] that
  *                   attend slot s of exp(sm_scale * q[b][hq][i] . K_s - lse[b][hq][i])
  * with the arguments of sage2_attn_tree and the lse it wrote (rows with lse = -inf
- * add nothing).
+ * add nothing, one with lse = NaN makes every tally that it attends NaN).  With an
+ * SAGE2_E4M3 cache q enters exactly down to 2^-31 of the largest |q| among the (at most 256)
+ * rows of a key/value head that are taken at a time.
  *   acc : f32, slots contiguous, acc_strides {batch, head} in elements (the S slots of
  *         each head its own), S slots a head (a slot >= S is left out and sets the device error
  *         word).  A drafted token's slot is added to as well: its tally is to be 0
